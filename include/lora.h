@@ -90,7 +90,8 @@ typedef enum LORA_ENUM_INT {
     LORA_ERR_HIP = 7,       /* a kernel launch failed */
     LORA_ERR_BAD_ID = 8,    /* (checked mode) an id outside [-1, n_adapters) */
     LORA_ERR_MODE = 9,      /* unknown lora_mode_t */
-    LORA_ERR_POOL = 10      /* (checked mode) a compact-pool adapter's rows leave the pool */
+    LORA_ERR_POOL = 10,     /* (checked mode) a compact-pool adapter's rows leave the pool */
+    LORA_ERR_VALUE = 11     /* a scalar argument outside its range (lora_rmsnorm's eps) */
 } lora_status_t;
 
 typedef enum LORA_ENUM_INT { LORA_BF16 = 0, LORA_F32 = 1 } lora_dtype_t;
@@ -313,6 +314,27 @@ lora_status_t lora_linear_fp8w_profiled(const void *x, const void *W8, const flo
                                         size_t ws_bytes, void *stream, float *kernel_ms,
                                         const char **kernel_names, int32_t max_kernels,
                                         int32_t *n_kernels);
+
+/* The step in front of a projection in a serving loop (the pages take x as given and define no
+ * such call): residual addition and root-mean-square norm of every row, written in bf16, as
+ * 8-bit codes with one scale per row (the x operand of lora_linear_fp8), or both:
+ *     h = x[m] + residual[m]                        (fp32; residual NULL: h = x[m])
+ *     sum[m] = bf16(h)                              (sum NULL: not written)
+ *     n = h / sqrt(mean(h^2) + eps) * weight        (fp32; weight NULL: 1)
+ *     y[m] = bf16(n)                                (y NULL: not written)
+ *     s = max(max|n|, 2^-60) / 448;  y8[m] = E4M3(n / s);  y_scale[m] = s
+ *                                                   (y8 and y_scale both NULL: not written)
+ * The norm is taken of the unrounded h.  x, residual, sum, y: bf16 [M][d]; weight: bf16 [d]; y8:
+ * E4M3 codes (as lora_linear_fp8w's W8) [M][d]; y_scale: fp32 [M].  x, residual, weight, sum, y
+ * and y8 16-byte aligned, y_scale 4-byte.  d a positive multiple of 8, at most 2^20.  sum and
+ * y may each be x or residual itself (in place); outputs must not overlap each other or an input
+ * otherwise.  A row that holds an infinity or a NaN gives NaN wherever the formula does in y,
+ * and NaN for its scale and every code.  Rows are independent; no workspace.
+ * Errors: LORA_ERR_SHAPE (M, d), LORA_ERR_VALUE (eps not finite or below 1e-30), LORA_ERR_NULL
+ * (x; y and y8 both NULL; one of y8 and y_scale alone), LORA_ERR_ALIGN, LORA_ERR_HIP. */
+lora_status_t lora_rmsnorm(const void *x, const void *residual, const void *weight, float eps,
+                           int32_t M, int32_t d, void *sum, void *y, void *y8, float *y_scale,
+                           void *stream);
 
 /* For callers that cannot allocate (code under HIP graph capture, serving loops or
  * harnesses that forbid hipMalloc): lora_linear without a caller workspace.  The call uses a

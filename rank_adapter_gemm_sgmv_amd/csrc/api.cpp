@@ -1,6 +1,7 @@
 // api.cpp -- the C ABI of liblora_mi355x.so (include/lora.h): host-side validation,
 // workspace layout and the launch sequence of each call.  No call allocates device memory or
 // keeps state; only the checked mode and the measurement aids synchronise.
+#include <float.h>
 #include <stdint.h>
 #include <string.h>
 
@@ -1027,6 +1028,23 @@ lora_status_t lora_moe_linear_profiled(const void *x, const void *W, const void 
         kernel_ms, kernel_names, max_kernels, n_kernels);
 }
 
+lora_status_t lora_rmsnorm(const void *x, const void *residual, const void *weight, float eps,
+                           int32_t M, int32_t d, void *sum, void *y, void *y8, float *y_scale,
+                           void *stream) {
+    if (M < 0 || M > LORA_MAX_ROWS || !dim_ok(d)) return LORA_ERR_SHAPE;
+    if (!(eps >= 1e-30f) || eps > FLT_MAX) return LORA_ERR_VALUE;
+    if (M == 0) return LORA_OK;
+    if (!x || (!y && !y8) || !y8 != !y_scale) return LORA_ERR_NULL;
+    for (const void *p : {x, residual, weight, (const void *)sum, (const void *)y, (const void *)y8})
+        if (!aligned(p, 16)) return LORA_ERR_ALIGN;
+    if (!aligned(y_scale, 4)) return LORA_ERR_ALIGN;
+    clear_stale_error();
+    const NormArgs a{static_cast<const uint16_t *>(x), static_cast<const uint16_t *>(residual),
+                     static_cast<const uint16_t *>(weight), static_cast<uint16_t *>(sum),
+                     static_cast<uint16_t *>(y), static_cast<uint8_t *>(y8), y_scale, eps, M, d};
+    return hip_status(launch_rmsnorm(a, (hipStream_t)stream));
+}
+
 const char *lora_status_string(lora_status_t status) {
     switch (status) {
         case LORA_OK: return "LORA_OK";
@@ -1042,6 +1060,7 @@ const char *lora_status_string(lora_status_t status) {
         case LORA_ERR_BAD_ID: return "LORA_ERR_BAD_ID: (checked mode) adapter id or expert id out of range";
         case LORA_ERR_MODE: return "LORA_ERR_MODE: unknown mode";
         case LORA_ERR_POOL: return "LORA_ERR_POOL: (checked mode) an adapter's rank rows leave the compact pool";
+        case LORA_ERR_VALUE: return "LORA_ERR_VALUE: a scalar argument outside its range";
     }
     return "unknown lora_status_t";
 }

@@ -327,6 +327,17 @@ struct MoeReduceArgs {
 hipError_t launch_moe_gemm(const MoePlan &p, const MoeGemmArgs &a, hipStream_t s);
 hipError_t launch_moe_reduce(const MoePlan &p, const MoeReduceArgs &a, bool y_f32, hipStream_t s);
 
+// ---- residual addition + RMS norm (csrc/norm.hip) -------------------------------------------
+struct NormArgs {
+    const uint16_t *x, *residual, *weight;  // [M][d], [M][d] or nullptr, [d] or nullptr (= 1)
+    uint16_t *sum, *y;                      // [M][d] or nullptr
+    uint8_t *y8;                            // [M][d] or nullptr
+    float *y_scale;                         // [M], with y8
+    float eps;
+    int M, d;
+};
+hipError_t launch_rmsnorm(const NormArgs &a, hipStream_t s);
+
 // Records e as the error lora_last_hip_error() reports; LORA_ERR_HIP unless e is hipSuccess.
 lora_status_t hip_error_status(hipError_t e);
 

@@ -31,7 +31,7 @@ LORA_MODE_CHECKED = 0x100  # OR-ed into a mode: sync, check ids and adapter tabl
 STATUS = {
     0: "LORA_OK", 1: "LORA_ERR_NULL", 2: "LORA_ERR_SHAPE", 3: "LORA_ERR_RANK",
     4: "LORA_ERR_ALIGN", 5: "LORA_ERR_WORKSPACE", 6: "LORA_ERR_DTYPE", 7: "LORA_ERR_HIP",
-    8: "LORA_ERR_BAD_ID", 9: "LORA_ERR_MODE", 10: "LORA_ERR_POOL",
+    8: "LORA_ERR_BAD_ID", 9: "LORA_ERR_MODE", 10: "LORA_ERR_POOL", 11: "LORA_ERR_VALUE",
 }
 
 # every symbol include/lora.h declares
@@ -41,7 +41,7 @@ EXPORTS = ("lora_max_tiles", "lora_workspace_bytes", "lora_build_segments", "lor
            "lora_linear_noalloc", "lora_linear_fp8w", "lora_linear_fp8w_profiled",
            "lora_moe_workspace_bytes", "lora_moe_linear", "lora_moe_linear_profiled",
            "lora_workspace_bytes_multi", "lora_linear_multi", "lora_linear_multi_profiled",
-           "lora_status_string", "lora_last_hip_error")
+           "lora_rmsnorm", "lora_status_string", "lora_last_hip_error")
 
 
 class LoraError(RuntimeError):
@@ -127,6 +127,8 @@ def _load():
     lib.lora_linear_multi_profiled.argtypes = lib.lora_linear_multi.argtypes + [
         ctypes.POINTER(ctypes.c_float), ctypes.POINTER(ctypes.c_char_p), I, ctypes.POINTER(I)]
     lib.lora_linear_multi_profiled.restype = ctypes.c_int
+    lib.lora_rmsnorm.argtypes = [P, P, P, ctypes.c_float, I, I, P, P, P, P, P]
+    lib.lora_rmsnorm.restype = ctypes.c_int
     lib.lora_status_string.argtypes = [ctypes.c_int]
     lib.lora_status_string.restype = ctypes.c_char_p
     lib.lora_last_hip_error.argtypes = []
@@ -135,6 +137,8 @@ def _load():
 
 
 _lib = _load()
+
+import torch  # noqa: E402  (after _load, which says why torch comes before the library)
 
 
 def library():
@@ -152,9 +156,8 @@ def _ptr(a) -> Optional[int]:
 
 def _stream(stream) -> Optional[int]:
     if stream is None:
-        import torch
-
-        return torch.cuda.current_stream().cuda_stream
+        torch.cuda.init()
+        return _current_stream(_current_device())
     if isinstance(stream, int):
         return stream
     return stream.cuda_stream
@@ -163,6 +166,33 @@ def _stream(stream) -> Optional[int]:
 def _check(status: int, where: str) -> None:
     if status != 0:
         raise LoraError(status, where)
+
+
+# torch.cuda.current_device() and current_stream() without their Python objects: a decode
+# call's launch costs the host about as much as these do
+_current_device = torch._C._cuda_getDevice
+_current_stream = torch._C._cuda_getCurrentRawStream
+
+_BF16 = (torch.bfloat16,)
+_F32 = (torch.float32,)
+_I32 = (torch.int32,)
+_E4M3 = (torch.float8_e4m3fn, torch.uint8)  # E4M3 codes, under either type
+
+
+def _buf(a, name: str, n: int, dtypes) -> Optional[int]:
+    """_ptr of a buffer of at least n elements: a tensor must be contiguous, of one of the
+    given dtypes and on the current device, else ValueError."""
+    if a is None or isinstance(a, int):
+        return a
+    if a.dtype not in dtypes:
+        raise ValueError(f"{name}: {a.dtype} given, {dtypes[0]} wanted")
+    if not a.is_contiguous() or a.numel() < n:
+        raise ValueError(f"{name}: a contiguous tensor of {n} elements wanted, got {tuple(a.shape)}"
+                         f" with strides {a.stride()}")
+    dev = a.get_device()
+    if dev < 0 or dev != _current_device():
+        raise ValueError(f"{name}: a tensor of the current device wanted, got one on {a.device}")
+    return a.data_ptr()
 
 
 def _seg_struct(seg) -> lora_segments_t:
@@ -394,6 +424,18 @@ def lora_linear_compact_profiled(x, W, A, B, scale, ranks, rank_offsets, pool_ro
         _ptr(ws), ws_bytes, _stream(stream), ms, names, max_kernels, ctypes.byref(n)),
         "lora_linear_compact_profiled")
     return [(names[i].decode(), float(ms[i])) for i in range(n.value)]
+
+
+def lora_rmsnorm(x, residual, weight, eps: float, M: int, d: int, sum, y, y8, y_scale,
+                 stream=None) -> None:
+    """Residual addition + RMS norm of M rows of d: sum = x + residual, y (bf16) and / or y8
+    (E4M3 codes: float8_e4m3fn or uint8) with y_scale per row; any output may be None."""
+    el = M * d
+    _check(_lib.lora_rmsnorm(
+        _buf(x, "x", el, _BF16), _buf(residual, "residual", el, _BF16),
+        _buf(weight, "weight", d, _BF16), eps, M, d, _buf(sum, "sum", el, _BF16),
+        _buf(y, "y", el, _BF16), _buf(y8, "y8", el, _E4M3), _buf(y_scale, "y_scale", M, _F32),
+        _stream(stream)), "lora_rmsnorm")
 
 
 # ---- device buffers (torch is only the allocator here) ----------------------------------
