@@ -91,7 +91,7 @@ typedef enum LORA_ENUM_INT {
     LORA_ERR_BAD_ID = 8,    /* (checked mode) an id outside [-1, n_adapters) */
     LORA_ERR_MODE = 9,      /* unknown lora_mode_t */
     LORA_ERR_POOL = 10,     /* (checked mode) a compact-pool adapter's rows leave the pool */
-    LORA_ERR_VALUE = 11     /* a scalar argument outside its range (lora_rmsnorm's eps) */
+    LORA_ERR_VALUE = 11     /* a scalar argument outside its range (lora_rmsnorm's eps, an activation) */
 } lora_status_t;
 
 typedef enum LORA_ENUM_INT { LORA_BF16 = 0, LORA_F32 = 1 } lora_dtype_t;
@@ -249,6 +249,41 @@ lora_status_t lora_linear_compact(const void *x, const void *W, const void *A, c
                                   int32_t r_max, int32_t n_adapters, const lora_segments_t *segs,
                                   void *y, lora_dtype_t y_dtype, lora_mode_t mode, void *ws,
                                   size_t ws_bytes, void *stream);
+
+/* What follows a projection before its result is stored, element by element in fp32 (the pages
+ * stop at the layer equation and define no such argument):
+ *     y = act(z + bias) * mul + residual            (one rounding, into y's type)
+ * bias: bf16 [d_out].  mul and residual: [M][d_out] in y's type.  Each may be NULL (bias and
+ * residual 0, mul 1); all 16-byte aligned.  mul and residual may be y itself (every element is
+ * read before it is written) and must not overlap it otherwise.  Activations: RELU max(z, 0);
+ * SILU z / (1 + e^-z); GELU z Phi(z) with the normal distribution Phi; GELU_TANH its tanh form,
+ * z / 2 (1 + tanh(sqrt(2 / pi) (z + 0.044715 z^3))).  With silu and mul, a gate projection
+ * ([P1], "How much memory does one LoRA adapter actually cost?", gate_proj) writes the MLP's
+ * silu(gate) * up. */
+typedef enum LORA_ENUM_INT {
+    LORA_ACT_NONE = 0,
+    LORA_ACT_RELU = 1,
+    LORA_ACT_SILU = 2,
+    LORA_ACT_GELU = 3,
+    LORA_ACT_GELU_TANH = 4
+} lora_act_t;
+typedef struct {
+    const void *bias;
+    const void *mul;
+    const void *residual;
+    lora_act_t act;
+} lora_epilogue_t;
+
+/* lora_linear with an epilogue: z = x W + (x A_i) B_i scale_i (rows with id -1: x W), then epi
+ * as above.  epi: a HOST struct read during the call; NULL gives lora_linear's result.  The
+ * other arguments, the workspace (lora_workspace_bytes()), modes and errors are lora_linear's;
+ * also LORA_ERR_VALUE for an unknown activation and LORA_ERR_ALIGN for the epilogue's operands. */
+lora_status_t lora_linear_act(const void *x, const void *W, const void *A, const void *B,
+                              const float *scale, const int32_t *ranks, const int32_t *ids,
+                              int32_t M, int32_t d_in, int32_t d_out, int32_t r_max,
+                              int32_t n_adapters, const lora_segments_t *segs,
+                              const lora_epilogue_t *epi, void *y, lora_dtype_t y_dtype,
+                              lora_mode_t mode, void *ws, size_t ws_bytes, void *stream);
 
 /* Several projections of one layer that read the same input rows, each with its own adapter
  * pool: [P1], "How much memory does one LoRA adapter actually cost?", names the MLP's

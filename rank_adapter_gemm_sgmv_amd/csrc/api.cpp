@@ -269,6 +269,20 @@ lora_status_t check_linear(const void *x, const void *W, const void *A, const vo
     return LORA_OK;
 }
 
+lora_status_t check_epilogue(const lora_epilogue_t *epi) {
+    if (!epi) return LORA_OK;
+    if (epi->act < LORA_ACT_NONE || epi->act > LORA_ACT_GELU_TANH) return LORA_ERR_VALUE;
+    if (!aligned(epi->bias, 16) || !aligned(epi->mul, 16) || !aligned(epi->residual, 16))
+        return LORA_ERR_ALIGN;
+    return LORA_OK;
+}
+
+Epilogue to_epilogue(const lora_epilogue_t *epi, const float *row_scale) {
+    if (!epi) return Epilogue{nullptr, nullptr, nullptr, row_scale, LORA_ACT_NONE};
+    return Epilogue{static_cast<const uint16_t *>(epi->bias), epi->mul, epi->residual, row_scale,
+                    epi->act};
+}
+
 // LORA_MODE_CHECKED: wait for the stream (the tables may be written by work queued on it),
 // copy ids, ranks and rank_offsets to host memory and check them: every id in [-1, n),
 // every rank in [1, r_max], and in a compact pool every adapter's round_up(rank, 8) rows
@@ -308,6 +322,9 @@ lora_status_t check_tables(const int32_t *ids, int32_t M, const int32_t *ranks,
 //   decode otherwise: build_segments, shrink, shrink_finalize, gemm [, splitk_reduce], expand
 //   prefill: build_segments, shrink, gemm with the LoRA epilogue (which adds t from the
 //            shrink's chunk sums)
+// With an epilogue (lora_linear_act) the last launch of each sequence applies it; "decode
+// otherwise" then ends in one pass that adds the split-K slices, t from the chunk sums, the
+// expand and the epilogue, or, where K is not split, takes the prefill sequence.
 // A rank-compact pool (roff != nullptr, lora_linear_compact) takes the same sequences; a padded
 // pool whose r_max is not a rank bucket (8, 16, 32, 64) too, except that its decode batches of
 // at most 128 rows take the second one (the first lays adapters side by side at row stride
@@ -317,8 +334,11 @@ hipError_t run_linear(const void *x, const void *W, const void *A, const void *B
                       int32_t pool_rows, const int32_t *ids, int32_t M, int32_t d_in,
                       int32_t d_out, int32_t r_max, int32_t n_adapters,
                       const lora_segments_t *segs, void *y, lora_dtype_t y_dtype, lora_mode_t mode,
-                      void *ws, hipStream_t s, Marker *mk) {
-    const bool prefill = mode == LORA_MODE_PREFILL || (mode == LORA_MODE_AUTO && M >= LORA_PREFILL_MIN_ROWS);
+                      void *ws, hipStream_t s, Marker *mk, const Epilogue *epi = nullptr) {
+    bool prefill = mode == LORA_MODE_PREFILL || (mode == LORA_MODE_AUTO && M >= LORA_PREFILL_MIN_ROWS);
+    const bool flat = epi && !decode_gemm_supported(M, d_in, d_out) && gemm_splits_k(M, d_in, d_out);
+    if (epi && !flat && !decode_gemm_supported(M, d_in, d_out) && !sk_plan(M, d_in, d_out).use)
+        prefill = true;
     char *p = static_cast<char *>(ws);
     lora_segments_t own = carve_segments(p, M, n_adapters);
     float *t = reinterpret_cast<float *>(p); p += t_bytes(M, r_max);
@@ -349,7 +369,7 @@ hipError_t run_linear(const void *x, const void *W, const void *A, const void *B
                                     true, gpart, nullptr, s)) != hipSuccess)
             return e;
         mark(mk, "decode_gemm_lora");
-        if ((e = launch_decode_reduce(gpart, M, d_in, d_out, y, yf, lo, true, nullptr, s)) != hipSuccess) return e;
+        if ((e = launch_decode_reduce(gpart, M, d_in, d_out, y, yf, lo, true, nullptr, s, epi)) != hipSuccess) return e;
         mark(mk, "decode_reduce_lora");
         return hipSuccess;
     }
@@ -369,7 +389,7 @@ hipError_t run_linear(const void *x, const void *W, const void *A, const void *B
                                d_in, rb, n_adapters, sg, spart, kc, ksplit, s)) != hipSuccess)
             return e;
         mark(mk, "shrink");
-        if ((e = launch_decode_reduce(gpart, M, d_in, d_out, y, yf, lo, false, &sg, s)) != hipSuccess) return e;
+        if ((e = launch_decode_reduce(gpart, M, d_in, d_out, y, yf, lo, false, &sg, s, epi)) != hipSuccess) return e;
         mark(mk, "decode_reduce_lora");
         return hipSuccess;
     }
@@ -384,7 +404,7 @@ hipError_t run_linear(const void *x, const void *W, const void *A, const void *B
     // the stream-K reduction and the prefill GEMM's epilogue add the shrink's chunk sums
     // themselves; the expand reads t
     const bool stream_k = !prefill && sk_plan(M, d_in, d_out).use;
-    if (!stream_k && !prefill) {
+    if (!stream_k && !prefill && !flat) {
         if ((e = launch_shrink_finalize(spart, M, rb, ksplit, sg, t, rb, s)) != hipSuccess)
             return e;
         mark(mk, "shrink_finalize");
@@ -392,7 +412,7 @@ hipError_t run_linear(const void *x, const void *W, const void *A, const void *B
     int gsplit = 1;
     if (prefill) {
         LoraEpilogue ep{spart, ksplit, Bb, scale, ids, rb, n_adapters, ranks, roff, pool_rows, pstride};
-        if ((e = launch_gemm(xb, Wb, M, d_in, d_out, y, yf, true, sg, &ep, nullptr, 0, &gsplit, s)) != hipSuccess)
+        if ((e = launch_gemm(xb, Wb, M, d_in, d_out, y, yf, true, sg, &ep, nullptr, 0, &gsplit, s, epi)) != hipSuccess)
             return e;
         mark(mk, "gemm_prefill_lora");
         return hipSuccess;
@@ -410,9 +430,21 @@ hipError_t run_linear(const void *x, const void *W, const void *A, const void *B
         pj.y[0] = y;
         if ((e = launch_sk_reduce_lora(gpart, M, d_in, d_out, sk_plan(M, d_in, d_out), sg, pj,
                                        ksplit, scale, ids, ranks, roff, pool_rows, pstride, rb,
-                                       n_adapters, yf, s)) != hipSuccess)
+                                       n_adapters, yf, s, epi)) != hipSuccess)
             return e;
         mark(mk, "decode_reduce_lora");
+        return hipSuccess;
+    }
+    if (flat) {
+        // plain split-K slices with an epilogue: slices, delta and epilogue in one pass
+        SkProj pj{};
+        pj.B[0] = Bb;
+        pj.tpart[0] = spart;
+        pj.y[0] = y;
+        if ((e = launch_splitk_reduce_lora(gpart, M, d_out, gsplit, sg, pj, ksplit, scale, ids, ranks,
+                                           pstride, rb, n_adapters, yf, *epi, s)) != hipSuccess)
+            return e;
+        mark(mk, "splitk_reduce_lora");
         return hipSuccess;
     }
     if (gsplit > 1) {
@@ -1026,6 +1058,27 @@ lora_status_t lora_moe_linear_profiled(const void *x, const void *W, const void 
                            d_in, d_out, r_max, n_adapters, y, y_dtype, ws, (hipStream_t)stream, mk);
         },
         kernel_ms, kernel_names, max_kernels, n_kernels);
+}
+
+lora_status_t lora_linear_act(const void *x, const void *W, const void *A, const void *B,
+                              const float *scale, const int32_t *ranks, const int32_t *ids,
+                              int32_t M, int32_t d_in, int32_t d_out, int32_t r_max,
+                              int32_t n_adapters, const lora_segments_t *segs,
+                              const lora_epilogue_t *epi, void *y, lora_dtype_t y_dtype,
+                              lora_mode_t mode, void *ws, size_t ws_bytes, void *stream) {
+    lora_status_t st = check_linear(x, W, A, B, scale, ranks, ids, M, d_in, d_out, r_max, n_adapters,
+                                    segs, y, y_dtype, mode, ws, ws_bytes);
+    if (st == LORA_OK) st = check_epilogue(epi);
+    if (st != LORA_OK || M == 0) return st;
+    clear_stale_error();
+    if ((mode & LORA_MODE_CHECKED) &&
+        (st = check_tables(ids, M, ranks, nullptr, 0, r_max, n_adapters, (hipStream_t)stream)) != LORA_OK)
+        return st;
+    const Epilogue e = to_epilogue(epi, nullptr);
+    return hip_status(run_linear(x, W, A, B, scale, ranks, nullptr, 0, ids, M, d_in, d_out, r_max,
+                                 n_adapters, segs, y, y_dtype,
+                                 (lora_mode_t)(mode & ~LORA_MODE_CHECKED), ws, (hipStream_t)stream,
+                                 nullptr, epi ? &e : nullptr));
 }
 
 lora_status_t lora_rmsnorm(const void *x, const void *residual, const void *weight, float eps,

@@ -96,6 +96,16 @@ constexpr int rank_bucket(int r_max) { return r_max <= 8 ? 8 : r_max <= 16 ? 16 
 // step against 18.3 at rank 16); in a 16-wide slot the second group re-reads the first.
 constexpr int fused_tile_rank(int rb) { return rb < 16 ? 16 : rb; }
 
+// Bias, activation, gate product and residual of lora_linear_act and lora_linear_fp8, applied
+// where y is rounded (csrc/epilogue.h): y = act(row_scale[m] z + bias) * mul + residual.
+struct Epilogue {
+    const uint16_t *bias;    // [N] bf16, or nullptr
+    const void *mul;         // [M][N] in y's type, or nullptr
+    const void *residual;    // [M][N] in y's type, or nullptr; mul and residual may be y
+    const float *row_scale;  // [M] (the fp8 layer's x scales), or nullptr
+    int act;                 // lora_act_t
+};
+
 // ---- kernel launches -------------------------------------------------------------------
 // Every kernel of the library is launched through launch().  Normally it is a plain launch;
 // while a KernelTimer is installed for the calling host thread (lora_linear_profiled), the
@@ -172,12 +182,13 @@ struct LoraEpilogue {
 hipError_t launch_gemm(const uint16_t *x, const uint16_t *W, int M, int K, int N, void *y,
                        bool y_f32, bool prefill, Seg seg, const LoraEpilogue *lora,
                        float *ws_partial, size_t ws_partial_floats, int *ksplit_out,
-                       hipStream_t s);
+                       hipStream_t s, const Epilogue *epi = nullptr);
 // Large-batch MFMA GEMM (csrc/gemm_big.hip): with lora != nullptr, rows in segment order and
 // the LoRA delta of each adapter run added before the only store (prefill); otherwise plain
 // y = x W in natural row order.
 hipError_t launch_gemm_big(const uint16_t *x, const uint16_t *W, int M, int K, int N, void *y,
-                           bool y_f32, Seg seg, const LoraEpilogue *lora, hipStream_t s);
+                           bool y_f32, Seg seg, const LoraEpilogue *lora, hipStream_t s,
+                           const Epilogue *epi = nullptr);
 
 // Stream-K decode GEMM (csrc/gemm_big.hip) for batches of 257-1024 rows whose 256 x 256
 // tiles are too few to fill the chip: L lanes of equal K length, n_tm workgroups per lane.
@@ -207,7 +218,13 @@ hipError_t launch_sk_reduce_lora(const float *partial, int M, int K, int N, cons
                                  Seg seg, const SkProj &pj, int n_chunks, const float *scale,
                                  const int32_t *ids, const int32_t *ranks, const int32_t *roff,
                                  int pool_rows, int pstride, int r_max, int n_adapters,
-                                 bool y_f32, hipStream_t s);
+                                 bool y_f32, hipStream_t s, const Epilogue *epi = nullptr);
+// The same pass over plain split-K slices partial[ks][M][N] (one projection, with epilogue).
+hipError_t launch_splitk_reduce_lora(const float *partial, int M, int N, int ks, Seg seg,
+                                     const SkProj &pj, int n_chunks, const float *scale,
+                                     const int32_t *ids, const int32_t *ranks, int pstride,
+                                     int r_max, int n_adapters, bool y_f32, const Epilogue &epi,
+                                     hipStream_t s);
 
 // Adds the split-K decode GEMM's ksplit > 1 partial slices into y, in order.
 hipError_t launch_splitk_reduce(const float *partial, int M, int N, int ksplit, void *y,
@@ -283,10 +300,13 @@ hipError_t launch_decode_gemm_fp8_lora(const uint16_t *x, const uint8_t *W8, con
 // each load of B_a; the result is the same.
 hipError_t launch_decode_reduce(const float *partial, int M, int K, int N, void *y, bool y_f32,
                                 const DecodeLora &lo, bool adapters, const Seg *seg,
-                                hipStream_t s);
+                                hipStream_t s, const Epilogue *epi = nullptr);
 
 // Workspace floats the decode GEMM needs for split-K partials at these sizes.
 size_t gemm_partial_floats(int M, int K, int N);
+// Whether launch_gemm(prefill = false) splits K into plain slices at these sizes (neither
+// stream-K nor one pass).
+bool gemm_splits_k(int M, int K, int N);
 
 // Split-K plan of the shrink for d_in.
 void shrink_plan(int d_in, int r_max, int *kc, int *ksplit);

@@ -38,6 +38,7 @@
 #include <type_traits>
 
 #include "decode_tiles.h"
+#include "epilogue.h"
 #include "segments_block.h"
 
 namespace lora {
@@ -510,11 +511,12 @@ __global__ __launch_bounds__(kThreads) void decode_gemm_fp8_lora_kernel(
 // MS: the most splits the launch can have (4 or 16; registers for the split partials).
 // PADRM: the pool is padded at stride RM (no roff, pstride == RM); the row addressing then
 // uses the compile-time stride (a runtime stride measured 2 us slower at 256 rows, r_max 64).
-template <int BM, int RM, bool YF32, int MS, bool PADRM>
+// EPI: the epilogue follows before the rounding; its operands are loaded with the partials.
+template <int BM, int RM, bool YF32, int MS, bool PADRM, bool EPI>
 __global__ __launch_bounds__(256) void reduce_lora_kernel(const float *__restrict__ partial,
                                                           int M, int N, int n_tm, int n_tn,
                                                           int n_lt, int n_splits, DecodeLora lo,
-                                                          void *__restrict__ y) {
+                                                          void *y, Epilogue epi) {
     constexpr int kMaxSplits = MS;
     constexpr int APT = AdapterTiles<RM>::APT;
     __shared__ float s_t[RM];
@@ -536,6 +538,8 @@ __global__ __launch_bounds__(256) void reduce_lora_kernel(const float *__restric
 #pragma unroll
     for (int sp = 0; sp < kMaxSplits; ++sp)
         if (sp < n_splits) pv[sp] = *reinterpret_cast<const float4 *>(pp + sp * stride);
+    EpiOperands<4, YF32> eo;
+    if constexpr (EPI) eo.load(epi, m, nc, N);
     // B_a[j, nc .. nc+3] for the adapter's rank rows, issued together (the rank is uniform
     // in the block, so rows at or beyond it are not added, and above r_max 16 not loaded)
     const int width = PADRM || lo.roff ? RM : lo.pstride;
@@ -632,6 +636,11 @@ __global__ __launch_bounds__(256) void reduce_lora_kernel(const float *__restric
         acc.z = fmaf(sc, d2, acc.z); acc.w = fmaf(sc, d3, acc.w);
     }
     if (!col_ok) return;
+    if constexpr (EPI) {
+        float z[4] = {acc.x, acc.y, acc.z, acc.w};
+        eo.apply(epi, z);
+        acc = make_float4(z[0], z[1], z[2], z[3]);
+    }
     if constexpr (YF32) {
         *reinterpret_cast<float4 *>(reinterpret_cast<float *>(y) + (size_t)m * N + n) = acc;
     } else {
@@ -660,12 +669,12 @@ constexpr int kSubRows = 4;
 constexpr int kSegCpt = 2;               // columns per thread
 constexpr int kSegCols = 256 * kSegCpt;  // columns per item
 constexpr int kSegMaxTiles = 512;        // tiles a block scans (lora_max_tiles at M <= 256)
-template <int RM, bool YF32, int MS, bool PADRM>
+template <int RM, bool YF32, int MS, bool PADRM, bool EPI>
 __global__ __launch_bounds__(256) void reduce_seg_kernel(const float *__restrict__ partial,
                                                          int M, int N, int n_tm, int n_tn,
                                                          int bm_log2, int n_splits,
                                                          int max_tiles, DecodeLora lo, Seg seg,
-                                                         void *__restrict__ y) {
+                                                         void *y, Epilogue epi) {
     constexpr int SUB = kSubRows;
     constexpr int TPT = kSegMaxTiles / 256;  // tiles per thread in the scan
     static_assert(SUB * RM <= 256, "one thread per (row, rank column) sums t");
@@ -774,6 +783,11 @@ __global__ __launch_bounds__(256) void reduce_seg_kernel(const float *__restrict
 #pragma unroll
             for (int sp = 0; sp < MS; ++sp)
                 if (sp < n_splits) pv[i][sp] = *reinterpret_cast<const float2 *>(pp[i] + sp * stride);
+    }
+    EpiOperands<2, YF32> eo[EPI ? SUB : 1];
+    if constexpr (EPI) {
+#pragma unroll
+        for (int i = 0; i < SUB; ++i) eo[i].load(epi, m[i], nc, N);
     }
     constexpr int TB = 32;
     const int ti = tid / RM, tj = tid % RM;
@@ -886,6 +900,11 @@ __global__ __launch_bounds__(256) void reduce_seg_kernel(const float *__restrict
             o.y = fmaf(sc, d[i][1], o.y);
         }
         if (!col_ok || i >= nr) continue;
+        if constexpr (EPI) {
+            float z[2] = {o.x, o.y};
+            eo[i].apply(epi, z);
+            o = make_float2(z[0], z[1]);
+        }
         if constexpr (YF32) {
             *reinterpret_cast<float2 *>(reinterpret_cast<float *>(y) + (size_t)m[i] * N + n) = o;
         } else {
@@ -1061,13 +1080,14 @@ hipError_t launch_decode_gemm_fp8_lora(const uint16_t *x, const uint8_t *W8, con
 
 hipError_t launch_decode_reduce(const float *partial, int M, int K, int N, void *y, bool y_f32,
                                 const DecodeLora &lo, bool adapters, const Seg *seg,
-                                hipStream_t s) {
+                                hipStream_t s, const Epilogue *epi) {
     if (!decode_gemm_supported(M, K, N) || partial == nullptr || !rank_ok(lo.r_max) ||
         (!adapters && (lo.tpart == nullptr || lo.n_chunks < 1)))
         return hipErrorInvalidValue;
     const int n_lt = adapters ? adapter_tiles(M, lo.r_max, lo.n_adapters) : 0;
     const DecPlan p = dec_plan(M, K, N, n_lt);
     const bool padrm = lo.roff == nullptr && lo.pstride == lo.r_max;
+    const Epilogue ep = epi ? *epi : Epilogue{};
     // (at most kDecodeMaxRows rows the rows of an adapter are too few to share B; there the
     // row kernel's shorter chain wins)
     if (!adapters && seg != nullptr && M > kDecodeMaxRows &&
@@ -1082,13 +1102,17 @@ hipError_t launch_decode_reduce(const float *partial, int M, int K, int N, void 
         const long max_items = ((long)M + 3L * n_seg + 6) / kSubRows;
         const dim3 sgrid((unsigned)n_cc, (unsigned)max_items);
         const int bl = p.bm == 32 ? 5 : 6;
+#define SEG_PAD(RMX, YF, MSX, PAD, EP)                                                           \
+    launch((reduce_seg_kernel<RMX, YF, MSX, PAD, EP>), sgrid, dim3(256), 0, s, partial, M, N,    \
+           p.n_tm, p.n_tn, bl, p.ks, max_tiles, lo, *seg, y, ep)
 #define SEG_ONE(RMX, YF, MSX)                                                                   \
-    if (padrm)                                                                                  \
-        launch((reduce_seg_kernel<RMX, YF, MSX, true>), sgrid, dim3(256), 0, s, partial, M, N,  \
-               p.n_tm, p.n_tn, bl, p.ks, max_tiles, lo, *seg, y);                                \
-    else                                                                                        \
-        launch((reduce_seg_kernel<RMX, YF, MSX, false>), sgrid, dim3(256), 0, s, partial, M, N, \
-               p.n_tm, p.n_tn, bl, p.ks, max_tiles, lo, *seg, y)
+    if (padrm) {                                                                                \
+        if (epi) SEG_PAD(RMX, YF, MSX, true, true);                                              \
+        else SEG_PAD(RMX, YF, MSX, true, false);                                                 \
+    } else {                                                                                    \
+        if (epi) SEG_PAD(RMX, YF, MSX, false, true);                                             \
+        else SEG_PAD(RMX, YF, MSX, false, false);                                                \
+    }
 #define SEG_LAUNCH(RMX, YF)                                                                     \
     if (p.ks <= 2) {                                                                            \
         SEG_ONE(RMX, YF, 2);                                                                    \
@@ -1110,16 +1134,21 @@ hipError_t launch_decode_reduce(const float *partial, int M, int K, int N, void 
 #undef SEG_RANK
 #undef SEG_LAUNCH
 #undef SEG_ONE
+#undef SEG_PAD
         return hipGetLastError();
     }
     const dim3 rgrid((unsigned)((N + 1023) / 1024), (unsigned)M);
+#define RED_PAD(BM, RMX, YF, MSX, PAD, EP)                                                  \
+    launch((reduce_lora_kernel<BM, RMX, YF, MSX, PAD, EP>), rgrid, dim3(256), 0, s, partial, M, \
+           N, p.n_tm, p.n_tn, p.n_lt, p.ks, lo, y, ep)
 #define RED_ONE(BM, RMX, YF, MSX)                                                           \
-    if (padrm)                                                                              \
-        launch((reduce_lora_kernel<BM, RMX, YF, MSX, true>), rgrid, dim3(256), 0, s, partial, M,\
-               N, p.n_tm, p.n_tn, p.n_lt, p.ks, lo, y);                                      \
-    else                                                                                    \
-        launch((reduce_lora_kernel<BM, RMX, YF, MSX, false>), rgrid, dim3(256), 0, s, partial, \
-               M, N, p.n_tm, p.n_tn, p.n_lt, p.ks, lo, y)
+    if (padrm) {                                                                            \
+        if (epi) RED_PAD(BM, RMX, YF, MSX, true, true);                                      \
+        else RED_PAD(BM, RMX, YF, MSX, true, false);                                         \
+    } else {                                                                                \
+        if (epi) RED_PAD(BM, RMX, YF, MSX, false, true);                                     \
+        else RED_PAD(BM, RMX, YF, MSX, false, false);                                        \
+    }
 #define RED_LAUNCH(BM, RMX, YF)                                                             \
     if (p.ks <= 4) {                                                                        \
         RED_ONE(BM, RMX, YF, 4);                                                            \
@@ -1141,6 +1170,7 @@ hipError_t launch_decode_reduce(const float *partial, int M, int K, int N, void 
 #undef RED_RANK
 #undef RED_LAUNCH
 #undef RED_ONE
+#undef RED_PAD
     return hipGetLastError();
 }
 

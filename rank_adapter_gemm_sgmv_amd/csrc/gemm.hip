@@ -292,6 +292,10 @@ hipError_t launch_cfg(const uint16_t *x, const uint16_t *W, int M, int K, int N,
 
 }  // namespace
 
+bool gemm_splits_k(int M, int K, int N) {
+    return !sk_plan(M, K, N).use && !use_big(M, N) && decode_plan(M, K, N).ksplit > 1;
+}
+
 size_t gemm_partial_floats(int M, int K, int N) {
     const SkPlan sp = sk_plan(M, K, N);
     if (sp.use) return sk_partial_floats(sp);
@@ -303,9 +307,10 @@ size_t gemm_partial_floats(int M, int K, int N) {
 hipError_t launch_gemm(const uint16_t *x, const uint16_t *W, int M, int K, int N, void *y,
                        bool y_f32, bool prefill, Seg seg, const LoraEpilogue *lora,
                        float *ws_partial, size_t ws_partial_floats, int *ksplit_out,
-                       hipStream_t s) {
+                       hipStream_t s, const Epilogue *epi) {
     *ksplit_out = 1;
-    if (prefill) return launch_gemm_big(x, W, M, K, N, y, y_f32, seg, lora, s);
+    if (prefill) return launch_gemm_big(x, W, M, K, N, y, y_f32, seg, lora, s, epi);
+    if (epi) return hipErrorInvalidValue;  // the decode tilings leave it to the reduction
     const SkPlan sp = sk_plan(M, K, N);
     if (sp.use) {
         if (sk_partial_floats(sp) > ws_partial_floats || ws_partial == nullptr)

@@ -33,7 +33,7 @@
 //    x and W panels a tile group shares are read once into that XCD's L2.
 #include <type_traits>
 
-#include "common.h"
+#include "epilogue.h"
 
 namespace lora {
 
@@ -256,12 +256,14 @@ __device__ __forceinline__ void fill_stage(uint4 *xs, uint4 *ws, const uint16_t 
 }
 
 // O32: DMA sources as 32-bit byte offsets (x and W each below 4 GiB).
-template <class C, bool SEGROWS, bool LORA, bool YF32, bool O32>
+// EPI: the epilogue of epilogue.h follows the delta, before the only rounding.
+template <class C, bool SEGROWS, bool LORA, bool YF32, bool O32, bool EPI>
 __global__ __launch_bounds__(C::NT) void gemm_big_kernel(const uint16_t *__restrict__ x,
                                                             const uint16_t *__restrict__ W,
                                                             int M, int K, int N,
-                                                            void *__restrict__ y, int n_tm,
-                                                            int n_tn, Seg seg, LoraEpilogue ep) {
+                                                            void *y, int n_tm, int n_tn,
+                                                            Seg seg, LoraEpilogue ep,
+                                                            Epilogue epi) {
     __shared__ __attribute__((aligned(1024))) uint4 X0[C::XSLOT];
     __shared__ __attribute__((aligned(1024))) uint4 X1[C::XSLOT];
     __shared__ __attribute__((aligned(1024))) uint4 X2[C::XSLOT];
@@ -437,7 +439,66 @@ __global__ __launch_bounds__(C::NT) void gemm_big_kernel(const uint16_t *__restr
 
     // store: accumulator element v of a 32 x 32 block is row (v/4)*8 + (lane/32)*4 + v%4,
     // column lane%32.
-    if constexpr (YF32) {
+    if constexpr (EPI) {
+        // Each wave stages 16 fp32 rows of its tile at a time in its own LDS slot, so that a
+        // lane then holds 8 consecutive columns of a row: the epilogue's operands and y move in
+        // 16-byte pieces.  The next step's operands are loaded before this step's are used.
+        lds_barrier();
+        uint4 *const sl = wave == 0 ? X0 : wave == 1 ? X1 : wave == 2 ? X2 : wave == 3 ? X3
+                        : wave == 4 ? W0 : wave == 5 ? W1 : wave == 6 ? W2 : W3;
+        float *stg = reinterpret_cast<float *>(sl);
+        constexpr int SROW = C::WTN + 8;  // staged row length (floats): 4 rows apart, 32 banks apart
+        constexpr int CPR = C::WTN / 8;   // 8-column pieces per row
+        constexpr int PP = 16 * CPR / 64;  // pieces per lane and step
+        constexpr int STEPS = 2 * C::TM;
+        static_assert(16 * SROW * 4 <= C::XSLOT * 16 && 16 * SROW * 4 <= C::WSLOT * 16,
+                      "staging fits one slot");
+        static_assert(PP * 64 == 16 * CPR, "whole pieces");
+        EpiOperands<8, YF32> eo[2][PP];
+        int mr[2][PP];
+        const int pr = lane / CPR, pc = 8 * (lane % CPR);  // this lane's row (of 64 / CPR) and column
+        const int col = n0 + wn0 + pc;
+        auto operands = [&](int st, int b) {
+#pragma unroll
+            for (int q = 0; q < PP; ++q) {
+                const int rr = min(row0 + wm0 + 16 * st + pr + q * (64 / CPR), M - 1);
+                mr[b][q] = SEGROWS ? seg.perm[rr] : rr;
+                eo[b][q].load(epi, mr[b][q], min(col, N - 8), N);
+            }
+        };
+        operands(0, 0);
+#pragma unroll
+        for (int st = 0; st < STEPS; ++st) {
+            const int i = st >> 1, h = st & 1;
+            if (st + 1 < STEPS) operands(st + 1, (st + 1) & 1);
+#pragma unroll
+            for (int j = 0; j < C::TN; ++j)
+#pragma unroll
+                for (int v = 0; v < 8; ++v)
+                    stg[((v / 4) * 8 + (lane >> 5) * 4 + (v % 4)) * SROW + 32 * j + (lane & 31)] =
+                        acc[i][j][8 * h + v];
+#pragma unroll
+            for (int q = 0; q < PP; ++q) {
+                const float *sp = &stg[(pr + q * (64 / CPR)) * SROW + pc];
+                const float4 a = *reinterpret_cast<const float4 *>(sp);
+                const float4 b = *reinterpret_cast<const float4 *>(sp + 4);
+                float z[8] = {a.x, a.y, a.z, a.w, b.x, b.y, b.z, b.w};
+                eo[st & 1][q].apply(epi, z);
+                if (row0 + wm0 + 16 * st + pr + q * (64 / CPR) < M && col < N) {
+                    const size_t at = (size_t)mr[st & 1][q] * N + col;
+                    if constexpr (YF32) {
+                        float4 *yf = reinterpret_cast<float4 *>(reinterpret_cast<float *>(y) + at);
+                        yf[0] = make_float4(z[0], z[1], z[2], z[3]);
+                        yf[1] = make_float4(z[4], z[5], z[6], z[7]);
+                    } else {
+                        st16(reinterpret_cast<uint16_t *>(y) + at,
+                             make_uint4(pack_bf16x2(z[0], z[1]), pack_bf16x2(z[2], z[3]),
+                                        pack_bf16x2(z[4], z[5]), pack_bf16x2(z[6], z[7])));
+                    }
+                }
+            }
+        }
+    } else if constexpr (YF32) {
 #pragma unroll
         for (int i = 0; i < C::TM; ++i) {
 #pragma unroll
@@ -629,12 +690,15 @@ __global__ __launch_bounds__(C::NT) void gemm_sk_kernel(const uint16_t *__restri
 // and share B_a's rows through L1 and L2.  A block covers 8 positions x 256 columns (one
 // panel), 8 columns per thread; blocks are handed to XCDs in contiguous runs (block b runs
 // on XCD b % 8), panel-major, so one XCD reads a panel's partial slots and B columns.
-template <class C, bool YF32>
+// FLAT: the partial sums are plain split-K slices [L][M][N] instead (n_tn1 panels of 256
+// columns).  EPI: the epilogue follows before the rounding.
+template <class C, bool YF32, bool FLAT, bool EPI>
 __global__ __launch_bounds__(256) void sk_reduce_lora_kernel(
     const float *__restrict__ partial, int M, int K, int N, int n_tm, int n_tn, int n_tn1, int L,
     Seg seg, SkProj pj, int n_chunks, const float *__restrict__ scale,
     const int32_t *__restrict__ ids, const int32_t *__restrict__ ranks,
-    const int32_t *__restrict__ roff, int pool_rows, int pstride, int r_max, int n_adapters) {
+    const int32_t *__restrict__ roff, int pool_rows, int pstride, int r_max, int n_adapters,
+    Epilogue epi) {
     static_assert(C::BN == 256, "one panel per block");
     __shared__ float4 s_part[256];
     __shared__ float s_t[8][64];
@@ -647,7 +711,7 @@ __global__ __launch_bounds__(256) void sk_reduce_lora_kernel(
     const int pr = p / n_tn1;
     const float *__restrict__ tpart = pick_proj(pr, pj.tpart);
     const uint16_t *__restrict__ B = pick_proj(pr, pj.B);
-    void *__restrict__ y = pick_proj(pr, pj.y);
+    void *y = pick_proj(pr, pj.y);
     const int pl = threadIdx.x >> 5;
     const int pos = g * 8 + pl;
     const int n = (p - pr * n_tn1) * C::BN + (threadIdx.x & 31) * 8;
@@ -658,6 +722,20 @@ __global__ __launch_bounds__(256) void sk_reduce_lora_kernel(
     if (live) {
         m = seg.perm[pos];
         a = ids[m];
+    }
+    EpiOperands<8, YF32> eo;
+    if constexpr (EPI) {
+        if (live) eo.load(epi, m, n, N);
+    }
+    if (live && FLAT) {
+        const float *P = partial + (size_t)m * N + n;
+        for (int l = 0; l < L; ++l, P += (size_t)M * N) {
+            const float4 u = *reinterpret_cast<const float4 *>(P);
+            const float4 v = *reinterpret_cast<const float4 *>(P + 4);
+            acc[0] += u.x; acc[1] += u.y; acc[2] += u.z; acc[3] += u.w;
+            acc[4] += v.x; acc[5] += v.y; acc[6] += v.z; acc[7] += v.w;
+        }
+    } else if (live) {
         const int tm = m / C::BM, r = m % C::BM, c = n % C::BN;
         const int KI = K / kBK, total = n_tn * KI;
         const int k0 = p * KI, k1 = k0 + KI;
@@ -738,6 +816,7 @@ __global__ __launch_bounds__(256) void sk_reduce_lora_kernel(
 #pragma unroll
         for (int q = 0; q < 8; ++q) acc[q] += sc * d[q];
     }
+    if constexpr (EPI) eo.apply(epi, acc);
     if constexpr (YF32) {
         float *yf = reinterpret_cast<float *>(y) + (size_t)m * N + n;
         *reinterpret_cast<float4 *>(yf) = make_float4(acc[0], acc[1], acc[2], acc[3]);
@@ -753,28 +832,38 @@ using CfgSk = Big<256, 256, 2, 4>;
 
 template <class C, bool SEGROWS, bool LORA>
 hipError_t launch_big_cfg(const uint16_t *x, const uint16_t *W, int M, int K, int N, void *y,
-                          bool y_f32, Seg seg, const LoraEpilogue *lora, hipStream_t s) {
+                          bool y_f32, Seg seg, const LoraEpilogue *lora, hipStream_t s,
+                          const Epilogue *epi) {
     const int n_tm = (M + C::BM - 1) / C::BM, n_tn = (N + C::BN - 1) / C::BN;
+    const Epilogue e = epi ? *epi : Epilogue{};
     LoraEpilogue ep{};
     if (lora) ep = *lora;
     const dim3 grid(n_tm * n_tn);
     // the LoRA instances take 32-bit load offsets when x and W each fit in 4 GiB
     const bool o32 = LORA && (size_t)M * K * 2 <= 0xFFFFFFFFull && (size_t)K * N * 2 <= 0xFFFFFFFFull;
-    if (o32) {
-        if (y_f32)
-            launch((gemm_big_kernel<C, SEGROWS, LORA, true, LORA>), grid, dim3(C::NT), 0, s, x, W,
-                   M, K, N, y, n_tm, n_tn, seg, ep);
-        else
-            launch((gemm_big_kernel<C, SEGROWS, LORA, false, LORA>), grid, dim3(C::NT), 0, s, x, W,
-                   M, K, N, y, n_tm, n_tn, seg, ep);
-    } else {
-        if (y_f32)
-            launch((gemm_big_kernel<C, SEGROWS, LORA, true, false>), grid, dim3(C::NT), 0, s, x, W,
-                   M, K, N, y, n_tm, n_tn, seg, ep);
-        else
-            launch((gemm_big_kernel<C, SEGROWS, LORA, false, false>), grid, dim3(C::NT), 0, s, x, W,
-                   M, K, N, y, n_tm, n_tn, seg, ep);
+#define BIG_ONE(YF, O32, EP)                                                                    \
+    launch((gemm_big_kernel<C, SEGROWS, LORA, YF, O32, EP>), grid, dim3(C::NT), 0, s, x, W, M, K, \
+           N, y, n_tm, n_tn, seg, ep, e)
+    if constexpr (LORA) {
+        if (epi) {
+            if (o32) {
+                if (y_f32) BIG_ONE(true, true, true);
+                else BIG_ONE(false, true, true);
+            } else {
+                if (y_f32) BIG_ONE(true, false, true);
+                else BIG_ONE(false, false, true);
+            }
+            return hipGetLastError();
+        }
     }
+    if (o32) {
+        if (y_f32) BIG_ONE(true, LORA, false);
+        else BIG_ONE(false, LORA, false);
+    } else {
+        if (y_f32) BIG_ONE(true, false, false);
+        else BIG_ONE(false, false, false);
+    }
+#undef BIG_ONE
     return hipGetLastError();
 }
 
@@ -783,18 +872,20 @@ hipError_t launch_big_cfg(const uint16_t *x, const uint16_t *W, int M, int K, in
 // Large-batch GEMM: prefill (segment-ordered rows, LoRA epilogue) when lora != nullptr,
 // else plain y = x W in natural row order.  Needs N >= 8 (N % 8 == 0) and M >= 1.
 hipError_t launch_gemm_big(const uint16_t *x, const uint16_t *W, int M, int K, int N, void *y,
-                           bool y_f32, Seg seg, const LoraEpilogue *lora, hipStream_t s) {
+                           bool y_f32, Seg seg, const LoraEpilogue *lora, hipStream_t s,
+                           const Epilogue *epi) {
+    if (epi && !lora) return hipErrorInvalidValue;
     const long t256 = (long)((M + 255) / 256) * ((N + 255) / 256);
     if (lora) {
-        if (t256 >= 192) return launch_big_cfg<Big<256, 256, 2, 4>, true, true>(x, W, M, K, N, y, y_f32, seg, lora, s);
+        if (t256 >= 192) return launch_big_cfg<Big<256, 256, 2, 4>, true, true>(x, W, M, K, N, y, y_f32, seg, lora, s, epi);
         if ((long)((M + 255) / 256) * ((N + 127) / 128) >= 192)
-            return launch_big_cfg<Big<256, 128>, true, true>(x, W, M, K, N, y, y_f32, seg, lora, s);
-        return launch_big_cfg<Big<128, 128>, true, true>(x, W, M, K, N, y, y_f32, seg, lora, s);
+            return launch_big_cfg<Big<256, 128>, true, true>(x, W, M, K, N, y, y_f32, seg, lora, s, epi);
+        return launch_big_cfg<Big<128, 128>, true, true>(x, W, M, K, N, y, y_f32, seg, lora, s, epi);
     }
-    if (t256 >= 192) return launch_big_cfg<Big<256, 256, 2, 4>, false, false>(x, W, M, K, N, y, y_f32, seg, nullptr, s);
+    if (t256 >= 192) return launch_big_cfg<Big<256, 256, 2, 4>, false, false>(x, W, M, K, N, y, y_f32, seg, nullptr, s, nullptr);
     if ((long)((M + 255) / 256) * ((N + 127) / 128) >= 192)
-        return launch_big_cfg<Big<256, 128>, false, false>(x, W, M, K, N, y, y_f32, seg, nullptr, s);
-    return launch_big_cfg<Big<128, 128>, false, false>(x, W, M, K, N, y, y_f32, seg, nullptr, s);
+        return launch_big_cfg<Big<256, 128>, false, false>(x, W, M, K, N, y, y_f32, seg, nullptr, s, nullptr);
+    return launch_big_cfg<Big<128, 128>, false, false>(x, W, M, K, N, y, y_f32, seg, nullptr, s, nullptr);
 }
 
 
@@ -837,23 +928,58 @@ hipError_t launch_gemm_sk(const uint16_t *x, const SkProj &pj, int M, int K, int
     return hipGetLastError();
 }
 
+namespace {
+
+// The reduction over stream-K partial tiles, or (flat) over p.L plain split-K slices.
+template <bool FLAT>
+hipError_t launch_reduce(const float *partial, int M, int K, int N, const SkPlan &p, Seg seg,
+                         const SkProj &pj, int n_chunks, const float *scale, const int32_t *ids,
+                         const int32_t *ranks, const int32_t *roff, int pool_rows, int pstride,
+                         int r_max, int n_adapters, bool y_f32, const Epilogue *epi,
+                         hipStream_t s) {
+    if (r_max < 8 || r_max > 64 || (r_max & (r_max - 1)) != 0) return hipErrorInvalidValue;
+    if (roff == nullptr && (pstride < 1 || pstride > r_max)) return hipErrorInvalidValue;
+    const dim3 grid((unsigned)(((M + 7) / 8) * p.n_tn));
+    const Epilogue e = epi ? *epi : Epilogue{};
+#define SK_RED(YF, EP)                                                                          \
+    launch(sk_reduce_lora_kernel<CfgSk, YF, FLAT, EP>, grid, dim3(256), 0, s, partial, M, K, N,   \
+           p.n_tm, p.n_tn, p.n_tn1, p.L, seg, pj, n_chunks, scale, ids, ranks, roff, pool_rows,  \
+           pstride, r_max, n_adapters, e)
+    if constexpr (!FLAT) {
+        if (!epi) {
+            if (y_f32) SK_RED(true, false);
+            else SK_RED(false, false);
+            return hipGetLastError();
+        }
+    }
+    if (y_f32) SK_RED(true, true);
+    else SK_RED(false, true);
+#undef SK_RED
+    return hipGetLastError();
+}
+
+}  // namespace
+
 hipError_t launch_sk_reduce_lora(const float *partial, int M, int K, int N, const SkPlan &p,
                                  Seg seg, const SkProj &pj, int n_chunks, const float *scale,
                                  const int32_t *ids, const int32_t *ranks, const int32_t *roff,
                                  int pool_rows, int pstride, int r_max, int n_adapters,
-                                 bool y_f32, hipStream_t s) {
-    if (r_max < 8 || r_max > 64 || (r_max & (r_max - 1)) != 0) return hipErrorInvalidValue;
-    if (roff == nullptr && (pstride < 1 || pstride > r_max)) return hipErrorInvalidValue;
-    const dim3 grid((unsigned)(((M + 7) / 8) * p.n_tn));
-    if (y_f32)
-        launch(sk_reduce_lora_kernel<CfgSk, true>, grid, dim3(256), 0, s, partial, M, K, N, p.n_tm,
-               p.n_tn, p.n_tn1, p.L, seg, pj, n_chunks, scale, ids, ranks, roff, pool_rows, pstride,
-               r_max, n_adapters);
-    else
-        launch(sk_reduce_lora_kernel<CfgSk, false>, grid, dim3(256), 0, s, partial, M, K, N, p.n_tm,
-               p.n_tn, p.n_tn1, p.L, seg, pj, n_chunks, scale, ids, ranks, roff, pool_rows, pstride,
-               r_max, n_adapters);
-    return hipGetLastError();
+                                 bool y_f32, hipStream_t s, const Epilogue *epi) {
+    return launch_reduce<false>(partial, M, K, N, p, seg, pj, n_chunks, scale, ids, ranks, roff,
+                                pool_rows, pstride, r_max, n_adapters, y_f32, epi, s);
+}
+
+hipError_t launch_splitk_reduce_lora(const float *partial, int M, int N, int ks, Seg seg,
+                                     const SkProj &pj, int n_chunks, const float *scale,
+                                     const int32_t *ids, const int32_t *ranks, int pstride,
+                                     int r_max, int n_adapters, bool y_f32, const Epilogue &epi,
+                                     hipStream_t s) {
+    SkPlan p{};
+    p.n_proj = 1;
+    p.n_tn = p.n_tn1 = (N + CfgSk::BN - 1) / CfgSk::BN;
+    p.L = ks;
+    return launch_reduce<true>(partial, M, 0, N, p, seg, pj, n_chunks, scale, ids, ranks, nullptr, 0,
+                               pstride, r_max, n_adapters, y_f32, &epi, s);
 }
 
 }  // namespace lora

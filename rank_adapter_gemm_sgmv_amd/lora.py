@@ -25,6 +25,7 @@ LORA_NOALLOC_SCRATCH_BYTES = 32 << 20
 LORA_MOE_MAX_PAIRS = 8192
 
 LORA_BF16, LORA_F32 = 0, 1
+LORA_ACT_NONE, LORA_ACT_RELU, LORA_ACT_SILU, LORA_ACT_GELU, LORA_ACT_GELU_TANH = 0, 1, 2, 3, 4
 LORA_MODE_AUTO, LORA_MODE_DECODE, LORA_MODE_PREFILL = 0, 1, 2
 LORA_MODE_CHECKED = 0x100  # OR-ed into a mode: sync, check ids and adapter tables on the host
 
@@ -41,7 +42,7 @@ EXPORTS = ("lora_max_tiles", "lora_workspace_bytes", "lora_build_segments", "lor
            "lora_linear_noalloc", "lora_linear_fp8w", "lora_linear_fp8w_profiled",
            "lora_moe_workspace_bytes", "lora_moe_linear", "lora_moe_linear_profiled",
            "lora_workspace_bytes_multi", "lora_linear_multi", "lora_linear_multi_profiled",
-           "lora_rmsnorm", "lora_status_string", "lora_last_hip_error")
+           "lora_rmsnorm", "lora_linear_act", "lora_status_string", "lora_last_hip_error")
 
 
 class LoraError(RuntimeError):
@@ -57,6 +58,11 @@ class lora_segments_t(ctypes.Structure):
     _fields_ = [("perm", ctypes.c_void_p), ("offsets", ctypes.c_void_p),
                 ("seg_adapter", ctypes.c_void_p), ("tiles", ctypes.c_void_p),
                 ("meta", ctypes.c_void_p)]
+
+
+class lora_epilogue_t(ctypes.Structure):
+    _fields_ = [("bias", ctypes.c_void_p), ("mul", ctypes.c_void_p),
+                ("residual", ctypes.c_void_p), ("act", ctypes.c_int32)]
 
 
 def _load():
@@ -127,6 +133,11 @@ def _load():
     lib.lora_linear_multi_profiled.argtypes = lib.lora_linear_multi.argtypes + [
         ctypes.POINTER(ctypes.c_float), ctypes.POINTER(ctypes.c_char_p), I, ctypes.POINTER(I)]
     lib.lora_linear_multi_profiled.restype = ctypes.c_int
+    lib.lora_linear_act.argtypes = [P, P, P, P, P, P, P, I, I, I, I, I,
+                                    ctypes.POINTER(lora_segments_t),
+                                    ctypes.POINTER(lora_epilogue_t), P, ctypes.c_int, ctypes.c_int,
+                                    P, S, P]
+    lib.lora_linear_act.restype = ctypes.c_int
     lib.lora_rmsnorm.argtypes = [P, P, P, ctypes.c_float, I, I, P, P, P, P, P]
     lib.lora_rmsnorm.restype = ctypes.c_int
     lib.lora_status_string.argtypes = [ctypes.c_int]
@@ -176,6 +187,7 @@ _current_stream = torch._C._cuda_getCurrentRawStream
 _BF16 = (torch.bfloat16,)
 _F32 = (torch.float32,)
 _I32 = (torch.int32,)
+_U8 = (torch.uint8,)
 _E4M3 = (torch.float8_e4m3fn, torch.uint8)  # E4M3 codes, under either type
 
 
@@ -424,6 +436,38 @@ def lora_linear_compact_profiled(x, W, A, B, scale, ranks, rank_offsets, pool_ro
         _ptr(ws), ws_bytes, _stream(stream), ms, names, max_kernels, ctypes.byref(n)),
         "lora_linear_compact_profiled")
     return [(names[i].decode(), float(ms[i])) for i in range(n.value)]
+
+
+class lora_epilogue:
+    """y = act(z + bias) * mul + residual (any of the three tensors may be None)."""
+
+    __slots__ = ("act", "bias", "mul", "residual")
+
+    def __init__(self, act: int = LORA_ACT_NONE, bias=None, mul=None, residual=None):
+        self.act, self.bias, self.mul, self.residual = act, bias, mul, residual
+
+
+def _epi_struct(epi, M: int, d_out: int, y_types):
+    if epi is None or isinstance(epi, lora_epilogue_t):
+        return epi
+    el = M * d_out
+    return lora_epilogue_t(_buf(epi.bias, "bias", d_out, _BF16), _buf(epi.mul, "mul", el, y_types),
+                           _buf(epi.residual, "residual", el, y_types), epi.act)
+
+
+def lora_linear_act(x, W, A, B, scale, ranks, ids, M: int, d_in: int, d_out: int, r_max: int,
+                    n_adapters: int, segs, epi, y, y_dtype: int, mode: int, ws, ws_bytes: int,
+                    stream=None) -> None:
+    """lora_linear followed by epi (a lora_epilogue, or None) before y is rounded."""
+    y_types = _F32 if y_dtype == LORA_F32 else _BF16
+    _check(_lib.lora_linear_act(
+        _buf(x, "x", M * d_in, _BF16), _buf(W, "W", d_in * d_out, _BF16),
+        _buf(A, "A", n_adapters * d_in * r_max, _BF16), _buf(B, "B", n_adapters * r_max * d_out, _BF16),
+        _buf(scale, "scale", n_adapters, _F32), _buf(ranks, "ranks", n_adapters, _I32),
+        _buf(ids, "ids", M, _I32), M, d_in, d_out, r_max, n_adapters,
+        None if segs is None else _seg_struct(segs), _epi_struct(epi, M, d_out, y_types),
+        _buf(y, "y", M * d_out, y_types), y_dtype, mode, _buf(ws, "ws", ws_bytes, _U8), ws_bytes,
+        _stream(stream)), "lora_linear_act")
 
 
 def lora_rmsnorm(x, residual, weight, eps: float, M: int, d: int, sum, y, y8, y_scale,
