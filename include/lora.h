@@ -350,6 +350,30 @@ lora_status_t lora_linear_fp8w_profiled(const void *x, const void *W8, const flo
                                         const char **kernel_names, int32_t max_kernels,
                                         int32_t *n_kernels);
 
+/* The whole layer on 8-bit operands, with an epilogue: x as lora_rmsnorm writes it, the base as
+ * lora_linear_fp8w holds it (the adapters stay bf16, so the delta runs in another type than the
+ * base: [P1], "Where does multi-LoRA serving actually break?", item 4):
+ *     z = x_scale[m] * ( sum_k dec(x8[m, k]) dec(W8[c, k]) w_scale[c]
+ *                        + scale_i ((dec(x8[m, :]) A_i) B_i)[c] ),   i = ids[m]
+ * (rows with id -1: the first sum alone), then y = act(z + bias) * mul + residual (epi, as for
+ * lora_linear_act; NULL: y = z).  x8: E4M3 codes [M][d_in]; x_scale fp32 [M]; W8: E4M3 codes
+ * [d_out][d_in]; w_scale fp32 [d_out].  Sums are fp32; with y in bf16,
+ * products below 2^-13 of the largest in their octet of k may be dropped from them (the 8-bit
+ * matrix instruction's own adder), with y in fp32 none are.  A NaN code gives NaN in its row (x8) or
+ * column (W8).  A, B, scale, ranks, ids, y and segs as for lora_linear.  Any number of rows;
+ * d_in a multiple of 16 (else LORA_ERR_SHAPE).  mode: LORA_MODE_AUTO (else LORA_ERR_MODE; the
+ * launches follow from the sizes), LORA_MODE_CHECKED may be OR-ed in.  ws:
+ * lora_fp8_workspace_bytes() bytes of the same sizes.  Errors as lora_linear_act. */
+size_t lora_fp8_workspace_bytes(int32_t M, int32_t d_in, int32_t d_out, int32_t r_max,
+                                int32_t n_adapters);
+lora_status_t lora_linear_fp8(const void *x8, const float *x_scale, const void *W8,
+                              const float *w_scale, const void *A, const void *B,
+                              const float *scale, const int32_t *ranks, const int32_t *ids,
+                              int32_t M, int32_t d_in, int32_t d_out, int32_t r_max,
+                              int32_t n_adapters, const lora_segments_t *segs,
+                              const lora_epilogue_t *epi, void *y, lora_dtype_t y_dtype,
+                              lora_mode_t mode, void *ws, size_t ws_bytes, void *stream);
+
 /* The step in front of a projection in a serving loop (the pages take x as given and define no
  * such call): residual addition and root-mean-square norm of every row, written in bf16, as
  * 8-bit codes with one scale per row (the x operand of lora_linear_fp8), or both:

@@ -546,6 +546,41 @@ lora_status_t check_fp8w(const void *x, const void *W8, const float *w_scale, co
 
 }  // namespace
 
+namespace {
+
+// lora_linear_fp8: build_segments, the shrink on the codes (chunk sums), then the fp8 GEMM with
+// delta and epilogue, or its split-K slices and the pass that adds slices, delta and epilogue.
+hipError_t run_fp8(const Fp8Gemm &g, const uint16_t *A, const uint16_t *B, const float *scale,
+                   const int32_t *ranks, const int32_t *ids, int32_t r_max, int32_t n_adapters,
+                   const lora_segments_t *segs, const Epilogue &epi, void *y, bool y_f32, void *ws,
+                   hipStream_t s) {
+    char *p = static_cast<char *>(ws);
+    lora_segments_t own = carve_segments(p, g.M, n_adapters);
+    float *spart = reinterpret_cast<float *>(p); p += shrink_partial_bytes(g.M, g.K, r_max);
+    float *gpart = reinterpret_cast<float *>(p);
+    const Seg sg = to_seg(segs ? *segs : own);
+    const int rb = rank_bucket(r_max);
+    int kc, ksplit;
+    shrink_plan(g.K, rb, &kc, &ksplit);
+    hipError_t e;
+    if (!segs && (e = launch_build_segments(ids, g.M, n_adapters, sg, s)) != hipSuccess) return e;
+    if ((e = launch_shrink_x8(g.x8, A, ranks, r_max, g.M, g.K, rb, n_adapters, sg, spart, kc, ksplit,
+                              s)) != hipSuccess)
+        return e;
+    const LoraEpilogue ep{spart, ksplit, B, scale, ids, rb, n_adapters, ranks, nullptr, 0, r_max};
+    const Fp8Plan pl = fp8_plan(g.M, g.K, g.N, y_f32);
+    if ((e = launch_gemm_fp8(g, pl, y, y_f32, sg, ep, epi, gpart, s)) != hipSuccess || pl.ks == 1)
+        return e;
+    SkProj pj{};
+    pj.B[0] = B;
+    pj.tpart[0] = spart;
+    pj.y[0] = y;
+    return launch_splitk_reduce_lora(gpart, g.M, g.N, pl.ks, sg, pj, ksplit, scale, ids, ranks, r_max,
+                                     rb, n_adapters, y_f32, epi, s);
+}
+
+}  // namespace
+
 // lora_linear's body on a given workspace: shared with the entry point that brings its own
 // device-resident scratch (csrc/noalloc.hip).
 lora_status_t lora::linear_on_workspace(const void *x, const void *W, const void *A,
@@ -1079,6 +1114,48 @@ lora_status_t lora_linear_act(const void *x, const void *W, const void *A, const
                                  n_adapters, segs, y, y_dtype,
                                  (lora_mode_t)(mode & ~LORA_MODE_CHECKED), ws, (hipStream_t)stream,
                                  nullptr, epi ? &e : nullptr));
+}
+
+size_t lora_fp8_workspace_bytes(int32_t M, int32_t d_in, int32_t d_out, int32_t r_max,
+                                int32_t n_adapters) {
+    if (check_common(M, r_max, n_adapters) != LORA_OK || !dim_ok(d_in) || !dim_ok(d_out) || d_in % 16 != 0)
+        return 0;
+    if (M == 0) return 0;
+    return segments_bytes(M, n_adapters) + shrink_partial_bytes(M, d_in, r_max) +
+           round_up(fp8_partial_floats(M, d_in, d_out) * sizeof(float));
+}
+
+lora_status_t lora_linear_fp8(const void *x8, const float *x_scale, const void *W8,
+                              const float *w_scale, const void *A, const void *B,
+                              const float *scale, const int32_t *ranks, const int32_t *ids,
+                              int32_t M, int32_t d_in, int32_t d_out, int32_t r_max,
+                              int32_t n_adapters, const lora_segments_t *segs,
+                              const lora_epilogue_t *epi, void *y, lora_dtype_t y_dtype,
+                              lora_mode_t mode, void *ws, size_t ws_bytes, void *stream) {
+    lora_status_t st = check_common(M, r_max, n_adapters);
+    if (st != LORA_OK) return st;
+    if (!dim_ok(d_in) || !dim_ok(d_out) || d_in % 16 != 0) return LORA_ERR_SHAPE;
+    if (y_dtype != LORA_BF16 && y_dtype != LORA_F32) return LORA_ERR_DTYPE;
+    if ((mode & ~LORA_MODE_CHECKED) != LORA_MODE_AUTO) return LORA_ERR_MODE;
+    if ((st = check_epilogue(epi)) != LORA_OK) return st;
+    if (M == 0) return LORA_OK;
+    if (!x8 || !x_scale || !W8 || !w_scale || !A || !B || !scale || !ids || !y || !ws)
+        return LORA_ERR_NULL;
+    if (segs && (st = check_seg(*segs)) != LORA_OK) return st;
+    if (!aligned(x8, 16) || !aligned(W8, 16) || !aligned(A, 16) || !aligned(B, 16) || !aligned(y, 16) ||
+        !aligned(ws, kAlign) || !aligned(x_scale, 4) || !aligned(w_scale, 4) || !aligned(scale, 4) ||
+        !aligned(ids, 4) || (ranks && !aligned(ranks, 4)))
+        return LORA_ERR_ALIGN;
+    if (ws_bytes < lora_fp8_workspace_bytes(M, d_in, d_out, r_max, n_adapters)) return LORA_ERR_WORKSPACE;
+    clear_stale_error();
+    if ((mode & LORA_MODE_CHECKED) &&
+        (st = check_tables(ids, M, ranks, nullptr, 0, r_max, n_adapters, (hipStream_t)stream)) != LORA_OK)
+        return st;
+    return hip_status(run_fp8(Fp8Gemm{static_cast<const uint8_t *>(x8), static_cast<const uint8_t *>(W8),
+                                      w_scale, M, d_in, d_out},
+                              static_cast<const uint16_t *>(A), static_cast<const uint16_t *>(B), scale,
+                              ranks, ids, r_max, n_adapters, segs, to_epilogue(epi, x_scale), y,
+                              y_dtype == LORA_F32, ws, (hipStream_t)stream));
 }
 
 lora_status_t lora_rmsnorm(const void *x, const void *residual, const void *weight, float eps,

@@ -49,6 +49,17 @@ __device__ __forceinline__ void unpack8(const uint4 v, float f[8]) {
     f[6] = bf16_lo(v.w); f[7] = bf16_hi(v.w);
 }
 
+// 8 E4M3 codes (two dwords) -> 8 bf16 of the same values (exact)
+typedef __bf16 bf16x2_t __attribute__((ext_vector_type(2)));
+__device__ __forceinline__ uint4 e4m3x8_to_bf16(uint32_t lo, uint32_t hi) {
+    const bf16x2_t a = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(lo, 1.0f, false);
+    const bf16x2_t b = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(lo, 1.0f, true);
+    const bf16x2_t c = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(hi, 1.0f, false);
+    const bf16x2_t d = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(hi, 1.0f, true);
+    return make_uint4(__builtin_bit_cast(uint32_t, a), __builtin_bit_cast(uint32_t, b),
+                      __builtin_bit_cast(uint32_t, c), __builtin_bit_cast(uint32_t, d));
+}
+
 __device__ __forceinline__ uint4 ld16(const void *p) { return *reinterpret_cast<const uint4 *>(p); }
 __device__ __forceinline__ void st16(void *p, uint4 v) { *reinterpret_cast<uint4 *>(p) = v; }
 // A store that writes through the L2 to memory (sc0 sc1), for data only a later kernel reads:
@@ -144,6 +155,10 @@ hipError_t launch_shrink(const uint16_t *x, const uint16_t *A, const int32_t *ra
                          const int32_t *roff, int pool_rows, int pstride, int M, int d_in,
                          int r_max, int n_adapters, Seg seg, float *partial, int kc, int ksplit,
                          hipStream_t s);
+// The same on E4M3 codes x8[M][d_in] (a padded pool): t of the codes' values, unscaled.
+hipError_t launch_shrink_x8(const uint8_t *x8, const uint16_t *A, const int32_t *ranks,
+                            int pstride, int M, int d_in, int r_max, int n_adapters, Seg seg,
+                            float *partial, int kc, int ksplit, hipStream_t s);
 // The same over n_proj <= kMaxProj pools that share x, the tables and the segments
 // (lora_linear_multi) in one launch: pool p reads A[p] and writes partial[p].
 hipError_t launch_shrink_multi(const uint16_t *x, int n_proj, const uint16_t *const *A,
@@ -346,6 +361,26 @@ struct MoeReduceArgs {
 };
 hipError_t launch_moe_gemm(const MoePlan &p, const MoeGemmArgs &a, hipStream_t s);
 hipError_t launch_moe_reduce(const MoePlan &p, const MoeReduceArgs &a, bool y_f32, hipStream_t s);
+
+// ---- the layer on 8-bit operands (csrc/gemm_fp8.hip) ------------------------------------------
+struct Fp8Gemm {
+    const uint8_t *x8;     // [M][K] E4M3 codes
+    const uint8_t *W8;     // [N][K] E4M3 codes
+    const float *w_scale;  // [N]
+    int M, K, N;           // K % 16 == 0, N % 8 == 0
+};
+// big: 256 x 256 tiles (bf16 y), else 128 x 128; ks > 1 slices of k_per_split of K.
+struct Fp8Plan {
+    bool big;
+    int ks, k_per_split;
+};
+Fp8Plan fp8_plan(int M, int K, int N, bool y_f32);
+size_t fp8_partial_floats(int M, int K, int N);
+// p.ks == 1: y from rows in segment order, with the delta and the epilogue.  p.ks > 1: slices
+// partial[ks][M][N] of x8 W8^T w_scale (launch_splitk_reduce_lora must follow).
+hipError_t launch_gemm_fp8(const Fp8Gemm &g, const Fp8Plan &p, void *y, bool y_f32, Seg seg,
+                           const LoraEpilogue &ep, const Epilogue &epi, float *partial,
+                           hipStream_t s);
 
 // ---- residual addition + RMS norm (csrc/norm.hip) -------------------------------------------
 struct NormArgs {

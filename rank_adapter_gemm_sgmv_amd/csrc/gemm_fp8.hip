@@ -1,0 +1,339 @@
+// gemm_fp8.hip -- z = (x8 W8^T) w_scale on 8-bit operands (E4M3) with fp32 sums, for
+// lora_linear_fp8: x8[M][K] codes with a scale per row (applied with the epilogue), W8[N][K]
+// codes with a scale per column.
+//
+// gfx950 design
+//  * v_mfma_f32_32x32x64_f8f6f4: 64 k per instruction at twice the bf16 rate (its unscaled form:
+//    the scales here belong to rows and columns, not to blocks of 32 k).
+//  * The tiles, waves and 4-stage LDS ring of the bf16 kernel (gemm_big.hip), with 64 k per
+//    stage: a row of a stage is 64 bytes there too, and W8 lies as x8 does (K contiguous), so both
+//    operands are staged and swizzled as x is there (16-byte chunk c of row r at c ^ ((r / 4) % 4))
+//    and read with ds_read_b128; no transposing reads.
+//  * That instruction's adder aligns the eight products of an octet of k to the largest of them and
+//    drops what lies 14 or more binary places below (measured: of 2^12 + 2^(12 - d) - 2^12 the
+//    second term survives to d = 13; between octets, and into the sum, to d = 23).  On random
+//    codes the result is off by 1.6e-5 of its size (4096 k), a hundredth of y's own rounding to
+//    bf16; the quantisation of x8 moved it by 4e-2.  A caller who asks for y in fp32 gets sums
+//    whose products are all kept: the codes widened to bf16 (exact) on v_mfma_f32_32x32x16_bf16,
+//    at half the rate (the 8-bit 32x32x16 instruction has the same adder).
+//  * A lane's 32 codes of an operand are chunks g and g + 2 of its row (g = lane / 32).  Which k
+//    they are does not matter as long as both operands agree, as the MFMA pairs equal places.
+//  * Enough tiles to fill the chip: rows in segment order, the LoRA delta as extra bf16 MFMA
+//    steps, then the epilogue and the only store (big_tiles.h).  Fewer: K is split over ks
+//    workgroups per tile, which write scaled fp32 slices [ks][M][N]; the reduction that follows
+//    (launch_splitk_reduce_lora) adds them, the delta and the epilogue.
+#include <type_traits>
+
+#include "big_tiles.h"
+
+namespace lora {
+
+namespace {
+
+constexpr int kK8 = 64;  // k per stage
+
+typedef int i32x8_t __attribute__((ext_vector_type(8)));
+typedef int i32x4_t __attribute__((ext_vector_type(4)));
+
+template <class C>
+struct Frags8 {
+    i32x8_t a[C::TM];
+    i32x8_t b[C::TN];
+};
+
+__device__ __forceinline__ i32x8_t read_row8(const uint4 *__restrict__ s, int row, int g) {
+    const int sw = (row >> 2) & 3;
+    const i32x4_t lo = *reinterpret_cast<const i32x4_t *>(&s[row * 4 + (g ^ sw)]);
+    const i32x4_t hi = *reinterpret_cast<const i32x4_t *>(&s[row * 4 + ((g + 2) ^ sw)]);
+    return __builtin_shufflevector(lo, hi, 0, 1, 2, 3, 4, 5, 6, 7);
+}
+
+template <class C>
+__device__ __forceinline__ void read_frags8(Frags8<C> &f, const uint4 *__restrict__ xs,
+                                            const uint4 *__restrict__ ws, int lane, int wm0,
+                                            int wn0) {
+    const int li = lane & 31, g = lane >> 5;
+#pragma unroll
+    for (int i = 0; i < C::TM; ++i) f.a[i] = read_row8(xs, wm0 + 32 * i + li, g);
+#pragma unroll
+    for (int j = 0; j < C::TN; ++j) f.b[j] = read_row8(ws, wn0 + 32 * j + li, g);
+}
+
+// WIDE: the codes widened to bf16, octet by octet.
+template <class C, bool WIDE>
+__device__ __forceinline__ void mfma_frags8(f32x16_t (&acc)[C::TM][C::TN], const Frags8<C> &f) {
+    if constexpr (WIDE) {
+#pragma unroll
+        for (int q = 0; q < 4; ++q) {
+            bf16x8_t b[C::TN];
+#pragma unroll
+            for (int j = 0; j < C::TN; ++j)
+                b[j] = __builtin_bit_cast(bf16x8_t, e4m3x8_to_bf16((uint32_t)f.b[j][2 * q],
+                                                                   (uint32_t)f.b[j][2 * q + 1]));
+#pragma unroll
+            for (int i = 0; i < C::TM; ++i) {
+                const bf16x8_t a = __builtin_bit_cast(
+                    bf16x8_t, e4m3x8_to_bf16((uint32_t)f.a[i][2 * q], (uint32_t)f.a[i][2 * q + 1]));
+#pragma unroll
+                for (int j = 0; j < C::TN; ++j)
+                    acc[i][j] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(a, b[j], acc[i][j], 0, 0, 0);
+            }
+        }
+        return;
+    }
+#pragma unroll
+    for (int i = 0; i < C::TM; ++i)
+#pragma unroll
+        for (int j = 0; j < C::TN; ++j)
+            acc[i][j] = __builtin_amdgcn_mfma_scale_f32_32x32x64_f8f6f4(f.a[i], f.b[j], acc[i][j], 0, 0, 0,
+                                                                        0, 0, 0);
+}
+
+// The next step's LDS reads among this step's MFMAs.
+template <class C>
+__device__ __forceinline__ void interleave_reads8() {
+    constexpr int reads = 2 * (C::TM + C::TN), mfmas = C::TM * C::TN;
+    constexpr int groups = mfmas < 4 ? mfmas : 4;
+#pragma unroll
+    for (int gi = 0; gi < groups; ++gi) {
+        __builtin_amdgcn_sched_group_barrier(0x100, (reads + groups - 1) / groups, 0);  // DS reads
+        __builtin_amdgcn_sched_group_barrier(0x008, mfmas / groups, 0);                 // MFMA
+    }
+}
+
+// Direct-load sources of a lane, k = 0: load q of an operand covers tile rows 16 q .. 16 q + 15;
+// lane i fills row 16 q + i / 4, stored chunk i % 4, which holds chunk (i % 4) ^ ((i / 16) % 4).
+// As 32-bit byte offsets when both operands fit in 4 GiB (one VGPR per address).
+template <class C>
+struct Src8 {
+    const uint8_t *xp[C::XINS], *wp[C::WINS];
+    __device__ __forceinline__ const uint8_t *x(int j, int k0) const { return xp[j] + k0; }
+    __device__ __forceinline__ const uint8_t *w(int j, int k0) const { return wp[j] + k0; }
+};
+template <class C>
+struct Src8O32 {
+    const uint8_t *xb, *wb;
+    uint32_t xo[C::XINS], wo[C::WINS];
+    __device__ __forceinline__ const uint8_t *x(int j, int k0) const { return xb + (uint32_t)(xo[j] + (uint32_t)k0); }
+    __device__ __forceinline__ const uint8_t *w(int j, int k0) const { return wb + (uint32_t)(wo[j] + (uint32_t)k0); }
+};
+
+template <class C, class S>
+__device__ __forceinline__ void issue8(const S &src, uint4 *__restrict__ xslot,
+                                       uint4 *__restrict__ wslot, int wave, int k0) {
+#pragma unroll
+    for (int j = 0; j < C::XINS; ++j)
+        __builtin_amdgcn_global_load_lds((const void *)src.x(j, k0),
+                                         (lds_void_t *)&xslot[(wave * C::XINS + j) * 64], 16, 0, 0);
+#pragma unroll
+    for (int j = 0; j < C::WINS; ++j)
+        __builtin_amdgcn_global_load_lds((const void *)src.w(j, k0),
+                                         (lds_void_t *)&wslot[(wave * C::WINS + j) * 64], 16, 0, 0);
+}
+
+// Register-path fill of a slot with rows r0 .. of an operand [rows][K], k0 .. k0 + 63 (zero
+// beyond k1), for the steps the ring does not cover.
+template <int ROWS, int NT>
+__device__ __forceinline__ void fill8(uint4 *slot, const uint8_t *__restrict__ src, int rows,
+                                      int K, int r0, int k0, int k1, const int32_t *perm, int tid) {
+    for (int c = tid; c < ROWS * 4; c += NT) {
+        const int row = c >> 2, lc = c & 3;
+        const int rr = min(r0 + row, rows - 1);
+        const int k = k0 + lc * 16;
+        uint4 v = make_uint4(0, 0, 0, 0);
+        if (k < k1) v = ld16(src + (size_t)(perm ? perm[rr] : rr) * K + k);
+        slot[row * 4 + (lc ^ ((row >> 2) & 3))] = v;
+    }
+}
+
+// WIDE: y is fp32 (see the top).  FUSED: whole K, rows in segment order, delta and epilogue; else slice blockIdx.y of K, rows in
+// their own order, into partial[blockIdx.y][M][N].
+template <class C, bool FUSED, bool WIDE, bool O32>
+__global__ __launch_bounds__(C::NT) void gemm_fp8_kernel(
+    const uint8_t *__restrict__ x8, const uint8_t *__restrict__ W8,
+    const float *__restrict__ w_scale, int M, int K, int N, int k_per_split,
+    float *__restrict__ partial, void *y, int n_tm, int n_tn, Seg seg, LoraEpilogue ep,
+    Epilogue epi) {
+    static_assert(C::XSLOT == C::BM * kK8 / 16 && C::WSLOT == C::BN * kK8 / 16, "64-byte rows");
+    __shared__ __attribute__((aligned(1024))) uint4 X0[C::XSLOT];
+    __shared__ __attribute__((aligned(1024))) uint4 X1[C::XSLOT];
+    __shared__ __attribute__((aligned(1024))) uint4 X2[C::XSLOT];
+    __shared__ __attribute__((aligned(1024))) uint4 X3[C::XSLOT];
+    __shared__ __attribute__((aligned(1024))) uint4 W0[C::WSLOT];
+    __shared__ __attribute__((aligned(1024))) uint4 W1[C::WSLOT];
+    __shared__ __attribute__((aligned(1024))) uint4 W2[C::WSLOT];
+    __shared__ __attribute__((aligned(1024))) uint4 W3[C::WSLOT];
+
+    const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
+    const int wm0 = (wave / C::WN) * C::WTM, wn0 = (wave % C::WN) * C::WTN;
+    int tmi, tni;
+    tile_of(blockIdx.x, n_tm, n_tn, tmi, tni);
+    const int row0 = tmi * C::BM, n0 = tni * C::BN;
+    const int k_lo = FUSED ? 0 : (int)blockIdx.y * k_per_split;
+    const int k_hi = FUSED ? K : min(K, k_lo + k_per_split);
+
+    // rows beyond M and columns beyond N repeat the last one; their results are never stored
+    std::conditional_t<O32, Src8O32<C>, Src8<C>> src;
+    if constexpr (O32) {
+        src.xb = x8;
+        src.wb = W8;
+    }
+    const int lrow = lane >> 2, lch = ((lane & 3) ^ ((lane >> 4) & 3)) * 16;
+#pragma unroll
+    for (int j = 0; j < C::XINS; ++j) {
+        const int rr = min(row0 + 16 * (wave * C::XINS + j) + lrow, M - 1);
+        const size_t o = (size_t)(FUSED ? seg.perm[rr] : rr) * K + lch;
+        if constexpr (O32) src.xo[j] = (uint32_t)o;
+        else src.xp[j] = x8 + o;
+    }
+#pragma unroll
+    for (int j = 0; j < C::WINS; ++j) {
+        const size_t o = (size_t)min(n0 + 16 * (wave * C::WINS + j) + lrow, N - 1) * K + lch;
+        if constexpr (O32) src.wo[j] = (uint32_t)o;
+        else src.wp[j] = W8 + o;
+    }
+
+    f32x16_t acc[C::TM][C::TN];
+#pragma unroll
+    for (int i = 0; i < C::TM; ++i)
+#pragma unroll
+        for (int j = 0; j < C::TN; ++j)
+#pragma unroll
+            for (int v = 0; v < 16; ++v) acc[i][j][v] = 0.0f;
+
+    // The ring of the bf16 kernel: steps 0 .. nmain-1, four per trip; loads past the last step
+    // reload it into slots that are never multiplied, so every wait counts the same loads.
+    const int nmain = ((k_hi - k_lo) / kK8) & ~3;
+    if (nmain > 0) {
+        Frags8<C> fa, fb;
+        issue8<C>(src, X0, W0, wave, k_lo);
+        issue8<C>(src, X1, W1, wave, k_lo + kK8);
+        issue8<C>(src, X2, W2, wave, k_lo + 2 * kK8);
+        wait_vm<2 * C::PER>();
+        lds_barrier();
+        read_frags8<C>(fa, X0, W0, lane, wm0, wn0);
+        issue8<C>(src, X3, W3, wave, k_lo + 3 * kK8);
+#define LORA_FP8_STEP(SS, FC, FN, XN, WN, XF, WF)                                 \
+        wait_vm<2 * C::PER>();                                                   \
+        lds_barrier();                                                           \
+        issue8<C>(src, XF, WF, wave, k_lo + min((SS) + 4, nmain - 1) * kK8);     \
+        read_frags8<C>(FN, XN, WN, lane, wm0, wn0);                              \
+        mfma_frags8<C, WIDE>(acc, FC);                                           \
+        if constexpr (!WIDE) interleave_reads8<C>();
+        for (int s = 0; s < nmain; s += 4) {
+            LORA_FP8_STEP(s, fa, fb, X1, W1, X0, W0)
+            LORA_FP8_STEP(s + 1, fb, fa, X2, W2, X1, W1)
+            LORA_FP8_STEP(s + 2, fa, fb, X3, W3, X2, W2)
+            LORA_FP8_STEP(s + 3, fb, fa, X0, W0, X3, W3)
+        }
+#undef LORA_FP8_STEP
+        wait_vm<0>();
+    }
+    // remaining steps, the last one possibly partial: through registers, zero beyond k_hi
+    for (int k0 = k_lo + nmain * kK8; k0 < k_hi; k0 += kK8) {
+        lds_barrier();
+        fill8<C::BM, C::NT>(X0, x8, M, K, row0, k0, k_hi, FUSED ? seg.perm : nullptr, tid);
+        fill8<C::BN, C::NT>(W0, W8, N, K, n0, k0, k_hi, nullptr, tid);
+        __syncthreads();
+        Frags8<C> f;
+        read_frags8<C>(f, X0, W0, lane, wm0, wn0);
+        mfma_frags8<C, WIDE>(acc, f);
+    }
+
+    // the columns' scales
+#pragma unroll
+    for (int j = 0; j < C::TN; ++j) {
+        const float ws = w_scale[min(n0 + wn0 + 32 * j + (lane & 31), N - 1)];
+#pragma unroll
+        for (int i = 0; i < C::TM; ++i)
+#pragma unroll
+            for (int v = 0; v < 16; ++v) acc[i][j][v] *= ws;
+    }
+
+    if constexpr (FUSED) {
+        add_lora_runs<C>(acc, X0, W0, ep, seg, M, N, row0, n0, tid, lane, wm0, wn0);
+        lds_barrier();
+        uint4 *const sl = wave == 0 ? X0 : wave == 1 ? X1 : wave == 2 ? X2 : wave == 3 ? X3
+                        : wave == 4 ? W0 : wave == 5 ? W1 : wave == 6 ? W2 : W3;
+        store_epilogue<C, true, WIDE>(acc, reinterpret_cast<float *>(sl), epi, y, seg.perm, M, N,
+                                      row0 + wm0, n0 + wn0, lane);
+    } else {
+        float *P = partial + (size_t)blockIdx.y * M * N;
+#pragma unroll
+        for (int i = 0; i < C::TM; ++i)
+#pragma unroll
+            for (int v = 0; v < 16; ++v) {
+                const int rr = row0 + wm0 + 32 * i + (v / 4) * 8 + (lane >> 5) * 4 + (v % 4);
+                if (rr >= M) continue;
+#pragma unroll
+                for (int j = 0; j < C::TN; ++j) {
+                    const int col = n0 + wn0 + 32 * j + (lane & 31);
+                    if (col < N) P[(size_t)rr * N + col] = acc[i][j][v];
+                }
+            }
+    }
+}
+
+template <class C, bool FUSED>
+hipError_t launch_fp8_cfg(const Fp8Gemm &g, const Fp8Plan &p, void *y, bool y_f32, Seg seg,
+                          const LoraEpilogue &ep, const Epilogue &epi, float *partial,
+                          hipStream_t s) {
+    const int n_tm = (g.M + C::BM - 1) / C::BM, n_tn = (g.N + C::BN - 1) / C::BN;
+    const bool o32 = (size_t)g.M * g.K <= 0xFFFFFFFFull && (size_t)g.N * g.K <= 0xFFFFFFFFull;
+    const dim3 grid(n_tm * n_tn, p.ks);
+#define FP8_ONE(WIDE, O32)                                                                     \
+    launch((gemm_fp8_kernel<C, FUSED, WIDE, O32>), grid, dim3(C::NT), 0, s, g.x8, g.W8, g.w_scale, \
+           g.M, g.K, g.N, p.k_per_split, partial, y, n_tm, n_tn, seg, ep, epi)
+    if constexpr (C::BM == 128) {  // (fp8_plan: fp32 y takes the small tiles)
+        if (y_f32) {
+            if (o32) FP8_ONE(true, true);
+            else FP8_ONE(true, false);
+            return hipGetLastError();
+        }
+    }
+    if (y_f32) return hipErrorInvalidValue;
+    if (o32) FP8_ONE(false, true);
+    else FP8_ONE(false, false);
+#undef FP8_ONE
+    return hipGetLastError();
+}
+
+}  // namespace
+
+Fp8Plan fp8_plan(int M, int K, int N, bool y_f32) {
+    Fp8Plan p{};
+    p.ks = 1;
+    p.k_per_split = K;
+    const long t256 = (long)((M + 255) / 256) * ((N + 255) / 256);
+    const long t128 = (long)((M + 127) / 128) * ((N + 127) / 128);
+    p.big = t256 >= 192 && !y_f32;
+    if (t256 < 192 && t128 < 256) {
+        const int steps = (K + 4 * kK8 - 1) / (4 * kK8);  // trips of the ring
+        int ks = (int)((512 + t128 - 1) / t128);           // two workgroups per CU
+        if (ks > 16) ks = 16;
+        if (ks > steps) ks = steps;
+        const int per = (steps + ks - 1) / ks;
+        p.k_per_split = per * 4 * kK8;
+        p.ks = (K + p.k_per_split - 1) / p.k_per_split;
+    }
+    return p;
+}
+
+size_t fp8_partial_floats(int M, int K, int N) {
+    const Fp8Plan p = fp8_plan(M, K, N, true);  // (the split does not depend on y's type)
+    return p.ks > 1 ? (size_t)p.ks * M * N : 0;
+}
+
+hipError_t launch_gemm_fp8(const Fp8Gemm &g, const Fp8Plan &p, void *y, bool y_f32, Seg seg,
+                           const LoraEpilogue &ep, const Epilogue &epi, float *partial,
+                           hipStream_t s) {
+    if (g.M < 1 || g.K < 16 || g.K % 16 != 0 || g.N < 8 || g.N % 8 != 0) return hipErrorInvalidValue;
+    if (p.ks > 1) {
+        if (partial == nullptr || p.k_per_split % (4 * kK8) != 0) return hipErrorInvalidValue;
+        return launch_fp8_cfg<Big<128, 128>, false>(g, p, y, y_f32, seg, ep, epi, partial, s);
+    }
+    if (p.big) return launch_fp8_cfg<Big<256, 256, 2, 4>, true>(g, p, y, y_f32, seg, ep, epi, nullptr, s);
+    return launch_fp8_cfg<Big<128, 128>, true>(g, p, y, y_f32, seg, ep, epi, nullptr, s);
+}
+
+}  // namespace lora

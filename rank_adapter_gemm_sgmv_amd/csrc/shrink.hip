@@ -19,6 +19,8 @@
 // partial[chunk][row][0:r_max] (zero beyond the rank); the consumers add the chunks in
 // ascending order, so the result does not depend on scheduling.  Summing the quarters in
 // the workgroup leaves a quarter as many chunk sums to write and to read back.
+#include <type_traits>
+
 #include "common.h"
 
 namespace lora {
@@ -56,13 +58,16 @@ struct MfmaShrink {
 
 // The MFMA steps over one LDS fill: rows kb .. kb + KS of the chunk (x beyond k_hi masked),
 // v_mfma_f32_16x16x32_bf16 per 16 rank columns below the rank.
-template <class C, int RM>
-__device__ __forceinline__ void shrink_mfma_fill(f32x4_t (&acc)[C::NB], const uint4 (&xv)[C::STEPS],
+template <class C, int RM, class XV>
+__device__ __forceinline__ void shrink_mfma_fill(f32x4_t (&acc)[C::NB], const XV (&xv)[C::STEPS],
                                                  const lds_char_t *wl, int kb, int k_hi, int g,
                                                  int li, int r) {
 #pragma unroll
     for (int st = 0; st < C::STEPS; ++st) {
-        const uint4 xs = kb + 32 * st + 8 * g < k_hi ? xv[st] : make_uint4(0, 0, 0, 0);
+        uint4 xw;
+        if constexpr (std::is_same_v<XV, uint2>) xw = e4m3x8_to_bf16(xv[st].x, xv[st].y);
+        else xw = xv[st];
+        const uint4 xs = kb + 32 * st + 8 * g < k_hi ? xw : make_uint4(0, 0, 0, 0);
         const bf16x8_t xa = __builtin_bit_cast(bf16x8_t, xs);
 #pragma unroll
         for (int b = 0; b < C::NB; ++b) {
@@ -103,9 +108,11 @@ struct ShrinkPools {
     int n;
 };
 
-template <int RM, int LAYOUT>
+// X8: x holds E4M3 codes instead (t of their values; the row's scale is applied with the
+// epilogue): half the bytes, each lane's 8 codes widened to bf16 (exactly) when they are used.
+template <int RM, int LAYOUT, bool X8>
 __global__ __launch_bounds__(64 * kWavesPerBlock) void shrink_mfma_kernel(
-    const uint16_t *__restrict__ x, ShrinkPools pools, const int32_t *__restrict__ ranks,
+    const void *__restrict__ x, ShrinkPools pools, const int32_t *__restrict__ ranks,
     const int32_t *__restrict__ roff, int pool_rows, int pstride, int M, int d_in, int n_adapters,
     Seg seg, int n_chunks, int kc) {
     using C = MfmaShrink<RM>;
@@ -146,7 +153,10 @@ __global__ __launch_bounds__(64 * kWavesPerBlock) void shrink_mfma_kernel(
         const int k_lo = min(k0, d_in), k_hi = min(k0 + kw, d_in);
         // this lane's x row (rows beyond the tile repeat its last row; their sums are dropped)
         const int mrow = seg.perm[p0 + min(li, rows - 1)];
-        const uint16_t *xr = x + (size_t)mrow * d_in;
+        using XV = std::conditional_t<X8, uint2, uint4>;  // 8 elements of x
+        using XE = std::conditional_t<X8, uint8_t, uint16_t>;
+        const XE *xr = static_cast<const XE *>(x) + (size_t)mrow * d_in;
+        auto load_x = [&](int k) { return *reinterpret_cast<const XV *>(xr + min(k, d_in - 8)); };
         const uint16_t *Aa = A + (size_t)row0 * d_in;
 
         f32x4_t acc[C::NB];
@@ -161,7 +171,7 @@ __global__ __launch_bounds__(64 * kWavesPerBlock) void shrink_mfma_kernel(
             // offsets are 32-bit bytes from the adapter's block (one VGPR per address).
             const char *ab = reinterpret_cast<const char *>(Aa);
             // fill f's loads: A_a rows kb .. kb + KS (zeros past k_hi) and this lane's x
-            auto load_fill = [&](int kb, uint4(&av)[C::AL], uint4(&xv)[C::STEPS]) {
+            auto load_fill = [&](int kb, uint4(&av)[C::AL], XV(&xv)[C::STEPS]) {
 #pragma unroll
                 for (int i = 0; i < C::AL; ++i) {
                     const int u = lane + 64 * i, kr = kb + u / C::GR, gr = u % C::GR;
@@ -173,7 +183,7 @@ __global__ __launch_bounds__(64 * kWavesPerBlock) void shrink_mfma_kernel(
                                               : make_uint4(0, 0, 0, 0);
                 }
 #pragma unroll
-                for (int st = 0; st < C::STEPS; ++st) xv[st] = ld16(xr + min(kb + 32 * st + 8 * g, d_in - 8));
+                for (int st = 0; st < C::STEPS; ++st) xv[st] = load_x(kb + 32 * st + 8 * g);
             };
             // At r_max <= 16 every fill's loads are issued before the first fill is used (one
             // round trip per chunk instead of one per fill; at r_max 16, 30 more VGPRs and four
@@ -181,7 +191,8 @@ __global__ __launch_bounds__(64 * kWavesPerBlock) void shrink_mfma_kernel(
             // 11008-deep shrink 16.0 -> 15.7 us.  Above r_max 16 the registers would cost a
             // wave per SIMD.
             constexpr bool UPFRONT = RM <= 16;
-            uint4 pav[UPFRONT ? C::FILLS : 1][C::AL], pxv[UPFRONT ? C::FILLS : 1][C::STEPS];
+            uint4 pav[UPFRONT ? C::FILLS : 1][C::AL];
+            XV pxv[UPFRONT ? C::FILLS : 1][C::STEPS];
             if constexpr (UPFRONT) {
 #pragma unroll
                 for (int f = 0; f < C::FILLS; ++f) load_fill(k_lo + f * C::KS, pav[f], pxv[f]);
@@ -190,7 +201,8 @@ __global__ __launch_bounds__(64 * kWavesPerBlock) void shrink_mfma_kernel(
             for (int f = 0; f < C::FILLS; ++f) {
                 const int kb = k_lo + f * C::KS;
                 if (kb >= k_hi) break;  // uniform: the wave's range ends inside this chunk
-                uint4 av[C::AL], xv[C::STEPS];
+                uint4 av[C::AL];
+                XV xv[C::STEPS];
                 if constexpr (UPFRONT) {
 #pragma unroll
                     for (int i = 0; i < C::AL; ++i) av[i] = pav[f][i];
@@ -243,9 +255,9 @@ __global__ __launch_bounds__(64 * kWavesPerBlock) void shrink_mfma_kernel(
                         }
                     }
                 }
-                uint4 xv[C::STEPS];
+                XV xv[C::STEPS];
 #pragma unroll
-                for (int st = 0; st < C::STEPS; ++st) xv[st] = ld16(xr + min(kb + 32 * st + 8 * g, d_in - 8));
+                for (int st = 0; st < C::STEPS; ++st) xv[st] = load_x(kb + 32 * st + 8 * g);
                 __builtin_amdgcn_s_waitcnt(0xC07F);  // lgkmcnt(0): this wave's LDS writes are done
                 shrink_mfma_fill<C, RM>(acc, xv, wl, kb, k_hi, g, li, r);
                 __builtin_amdgcn_s_waitcnt(0xC07F);  // LDS reads done before the next fill overwrites
@@ -327,7 +339,8 @@ void shrink_plan(int d_in, int r_max, int *kc, int *ksplit) {
 
 namespace {
 
-hipError_t launch_shrink_pools(const uint16_t *x, const ShrinkPools &pools, const int32_t *ranks,
+template <bool X8>
+hipError_t launch_shrink_pools(const void *x, const ShrinkPools &pools, const int32_t *ranks,
                                const int32_t *roff, int pool_rows, int pstride, int M, int d_in,
                                int r_max, int n_adapters, Seg seg, int kc, int ksplit,
                                hipStream_t s) {
@@ -343,7 +356,7 @@ hipError_t launch_shrink_pools(const uint16_t *x, const ShrinkPools &pools, cons
                        : (pstride & 7) != 0  ? kFlat
                                              : kVarW;
 #define LORA_SHRINK_ONE(RMV, LAY)                                                                \
-    launch(shrink_mfma_kernel<RMV, LAY>, wgrid, wblock, 0, s, x, pools, ranks, roff, pool_rows,  \
+    launch(shrink_mfma_kernel<RMV, LAY, X8>, wgrid, wblock, 0, s, x, pools, ranks, roff, pool_rows,  \
            pstride, M, d_in, n_adapters, seg, ksplit, kc)
 #define LORA_SHRINK_LAUNCH(RMV)                                                                  \
     if (layout == kPadRM) LORA_SHRINK_ONE(RMV, kPadRM);                                          \
@@ -371,8 +384,19 @@ hipError_t launch_shrink(const uint16_t *x, const uint16_t *A, const int32_t *ra
     pools.A[0] = A;
     pools.partial[0] = partial;
     pools.n = 1;
-    return launch_shrink_pools(x, pools, ranks, roff, pool_rows, pstride, M, d_in, r_max,
+    return launch_shrink_pools<false>(x, pools, ranks, roff, pool_rows, pstride, M, d_in, r_max,
                                n_adapters, seg, kc, ksplit, s);
+}
+
+hipError_t launch_shrink_x8(const uint8_t *x8, const uint16_t *A, const int32_t *ranks,
+                            int pstride, int M, int d_in, int r_max, int n_adapters, Seg seg,
+                            float *partial, int kc, int ksplit, hipStream_t s) {
+    ShrinkPools pools{};
+    pools.A[0] = A;
+    pools.partial[0] = partial;
+    pools.n = 1;
+    return launch_shrink_pools<true>(x8, pools, ranks, nullptr, 0, pstride, M, d_in, r_max, n_adapters,
+                                     seg, kc, ksplit, s);
 }
 
 hipError_t launch_shrink_multi(const uint16_t *x, int n_proj, const uint16_t *const *A,
@@ -386,7 +410,7 @@ hipError_t launch_shrink_multi(const uint16_t *x, int n_proj, const uint16_t *co
         pools.partial[p] = partial[p];
     }
     pools.n = n_proj;
-    return launch_shrink_pools(x, pools, ranks, nullptr, 0, pstride, M, d_in, r_max, n_adapters,
+    return launch_shrink_pools<false>(x, pools, ranks, nullptr, 0, pstride, M, d_in, r_max, n_adapters,
                                seg, kc, ksplit, s);
 }
 

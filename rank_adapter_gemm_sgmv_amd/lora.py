@@ -42,7 +42,8 @@ EXPORTS = ("lora_max_tiles", "lora_workspace_bytes", "lora_build_segments", "lor
            "lora_linear_noalloc", "lora_linear_fp8w", "lora_linear_fp8w_profiled",
            "lora_moe_workspace_bytes", "lora_moe_linear", "lora_moe_linear_profiled",
            "lora_workspace_bytes_multi", "lora_linear_multi", "lora_linear_multi_profiled",
-           "lora_rmsnorm", "lora_linear_act", "lora_status_string", "lora_last_hip_error")
+           "lora_rmsnorm", "lora_linear_act", "lora_fp8_workspace_bytes",
+           "lora_linear_fp8", "lora_status_string", "lora_last_hip_error")
 
 
 class LoraError(RuntimeError):
@@ -138,6 +139,10 @@ def _load():
                                     ctypes.POINTER(lora_epilogue_t), P, ctypes.c_int, ctypes.c_int,
                                     P, S, P]
     lib.lora_linear_act.restype = ctypes.c_int
+    lib.lora_fp8_workspace_bytes.argtypes = [I, I, I, I, I]
+    lib.lora_fp8_workspace_bytes.restype = S
+    lib.lora_linear_fp8.argtypes = [P, P, P, P] + lib.lora_linear_act.argtypes[2:]
+    lib.lora_linear_fp8.restype = ctypes.c_int
     lib.lora_rmsnorm.argtypes = [P, P, P, ctypes.c_float, I, I, P, P, P, P, P]
     lib.lora_rmsnorm.restype = ctypes.c_int
     lib.lora_status_string.argtypes = [ctypes.c_int]
@@ -468,6 +473,33 @@ def lora_linear_act(x, W, A, B, scale, ranks, ids, M: int, d_in: int, d_out: int
         None if segs is None else _seg_struct(segs), _epi_struct(epi, M, d_out, y_types),
         _buf(y, "y", M * d_out, y_types), y_dtype, mode, _buf(ws, "ws", ws_bytes, _U8), ws_bytes,
         _stream(stream)), "lora_linear_act")
+
+
+def lora_fp8_workspace_bytes(M: int, d_in: int, d_out: int, r_max: int, n_adapters: int) -> int:
+    return int(_lib.lora_fp8_workspace_bytes(M, d_in, d_out, r_max, n_adapters))
+
+
+def fp8_workspace(M: int, d_in: int, d_out: int, r_max: int, n_adapters: int, device="cuda"):
+    """A uint8 device tensor of lora_fp8_workspace_bytes() bytes (256-byte aligned by torch)."""
+    nbytes = lora_fp8_workspace_bytes(M, d_in, d_out, r_max, n_adapters)
+    return torch.empty(max(nbytes, 256), dtype=torch.uint8, device=device), nbytes
+
+
+def lora_linear_fp8(x8, x_scale, W8, w_scale, A, B, scale, ranks, ids, M: int, d_in: int,
+                    d_out: int, r_max: int, n_adapters: int, segs, epi, y, y_dtype: int, mode: int,
+                    ws, ws_bytes: int, stream=None) -> None:
+    """The layer on E4M3 codes x8[M, d_in] (scale per row) and W8[d_out, d_in] (scale per column:
+    float8_e4m3fn or uint8 tensors), followed by epi (a lora_epilogue, or None)."""
+    y_types = _F32 if y_dtype == LORA_F32 else _BF16
+    _check(_lib.lora_linear_fp8(
+        _buf(x8, "x8", M * d_in, _E4M3), _buf(x_scale, "x_scale", M, _F32),
+        _buf(W8, "W8", d_in * d_out, _E4M3), _buf(w_scale, "w_scale", d_out, _F32),
+        _buf(A, "A", n_adapters * d_in * r_max, _BF16), _buf(B, "B", n_adapters * r_max * d_out, _BF16),
+        _buf(scale, "scale", n_adapters, _F32), _buf(ranks, "ranks", n_adapters, _I32),
+        _buf(ids, "ids", M, _I32), M, d_in, d_out, r_max, n_adapters,
+        None if segs is None else _seg_struct(segs), _epi_struct(epi, M, d_out, y_types),
+        _buf(y, "y", M * d_out, y_types), y_dtype, mode, _buf(ws, "ws", ws_bytes, _U8), ws_bytes,
+        _stream(stream)), "lora_linear_fp8")
 
 
 def lora_rmsnorm(x, residual, weight, eps: float, M: int, d: int, sum, y, y8, y_scale,
