@@ -142,6 +142,29 @@ __device__ __forceinline__ void tile_of(int b, int n_tm, int n_tn, int &tm, int 
     tn = in / gsz;
 }
 
+// What the end of a tile needs of its rows (positions of perm), read once at its start, in the
+// shadow of the first stage's loads: a chain perm -> ids, row scale per step of the store cost a
+// prefill tile more than its MFMAs' last third.
+template <class C>
+struct RowTable {
+    int32_t m[C::BM];    // row of x and y (rows past the last repeat it)
+    int32_t id[C::BM];   // its adapter
+    float scale[C::BM];  // its x scale (1 without)
+};
+
+// Thread tid fills row tid, whose row of x is m (read before the first stage's loads are
+// issued; this follows them).  A barrier must come before the table is read.
+template <class C>
+__device__ __forceinline__ void fill_row(RowTable<C> &t, int m, const int32_t *ids,
+                                         const float *row_scale, int tid) {
+    static_assert(C::NT >= C::BM, "one row per thread");
+    if (tid < C::BM) {
+        t.m[tid] = m;
+        t.id[tid] = ids[m];
+        t.scale[tid] = row_scale ? row_scale[m] : 1.0f;
+    }
+}
+
 // The LoRA delta of one output tile (rows in segment order), after its K loop: acc += scale_a
 // t[rows, :] B_a[:, columns] for every run of one adapter among the tile's rows.  X0 and W0 are
 // LDS slots free for staging once every wave has passed the first barrier here.
@@ -155,16 +178,16 @@ __device__ __forceinline__ void tile_of(int b, int n_tm, int n_tn, int &tm, int 
 // not rounded to bf16 precision before it is added.
 template <class C>
 __device__ __forceinline__ void add_lora_runs(f32x16_t (&acc)[C::TM][C::TN], uint4 *X0, uint4 *W0,
-                                              const LoraEpilogue &ep, const Seg &seg, int M, int N,
-                                              int row0, int n0, int tid, int lane, int wm0,
-                                              int wn0) {
+                                              const LoraEpilogue &ep, const Seg &seg,
+                                              const RowTable<C> &rows, int M, int N, int row0,
+                                              int n0, int tid, int lane, int wm0, int wn0) {
     const int n_lora = seg.meta[1];
     const int RM = ep.r_max;
     constexpr int kHalf = kBK / 2;
     int p = row0;
     const int p_end = min(row0 + C::BM, n_lora);
     while (p < p_end) {
-        const int a = ep.ids[seg.perm[p]];
+        const int a = rows.id[p - row0];
         if (a < 0 || a >= ep.n_adapters) break;  // segments not built for these ids
         const int q_end = min(seg.offsets[a + 1], p_end);
         if (q_end <= p) break;
@@ -183,7 +206,7 @@ __device__ __forceinline__ void add_lora_runs(f32x16_t (&acc)[C::TM][C::TN], uin
                 if (pos >= p && pos < q_end && j < RM) {
                     // t[m, j .. j+7]: the shrink's chunk sums added in chunk order, four
                     // chunks' loads in flight at a time
-                    const float *tp = ep.tpart + (size_t)seg.perm[pos] * RM + j;
+                    const float *tp = ep.tpart + (size_t)rows.m[row] * RM + j;
                     const size_t cs = (size_t)M * RM;
                     float t[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
                     for (int c0 = 0; c0 < ep.n_chunks; c0 += 4) {
@@ -230,40 +253,43 @@ __device__ __forceinline__ void add_lora_runs(f32x16_t (&acc)[C::TM][C::TN], uin
     }
 }
 
-// Stores a wave's WTM x WTN block of the tile (first row r0, first column c0) with the epilogue.
-// It stages 16 fp32 rows at a time in its own LDS slot stg, so that a lane then holds 8
-// consecutive columns of a row: the epilogue's operands and y move in 16-byte pieces.  The next
-// step's operands are loaded before this step's are used.  LDS accesses of one wave complete in
-// order, so the staging needs no barrier beyond the one that freed the slots.  Rows are
-// positions of perm (SEGROWS) or rows of y.
-template <class C, bool SEGROWS, bool YF32>
+// Stores a wave's WTM x WTN block of the tile (first position row0 + wm0, first column c0) with
+// the epilogue.  It stages 16 fp32 rows at a time in its own LDS slot stg, so that a lane then holds
+// 8 consecutive columns of a row: mul, residual and y move in 16-byte pieces.  mul and residual
+// are loaded AHEAD steps before their use (what the accumulators leave of the registers).  bf16 y
+// is stored nontemporally, so that the end of the kernel finds fewer dirty lines in the L2s (fp8
+// 4096 x 4096 x 4096: 72.5 -> 69.4 us, 4096 x 4096 x 11008 without gate: 210 -> 193 us).  LDS
+// accesses of one wave complete in order, so the staging needs no barrier beyond the one that
+// freed the slots.
+template <class C, bool YF32>
 __device__ __forceinline__ void store_epilogue(const f32x16_t (&acc)[C::TM][C::TN], float *stg,
-                                               const Epilogue &epi, void *y, const int32_t *perm,
-                                               int M, int N, int r0, int c0, int lane) {
-    constexpr int SROW = C::WTN + 8;  // staged row length (floats): 4 rows apart, 32 banks apart
-    constexpr int CPR = C::WTN / 8;   // 8-column pieces per row
+                                               const Epilogue &epi, void *y,
+                                               const RowTable<C> &rows, int M, int N, int row0,
+                                               int wm0, int c0, int lane) {
+    constexpr int SROW = C::WTN + 8;   // staged row length (floats): 4 rows apart, 32 banks apart
+    constexpr int CPR = C::WTN / 8;    // 8-column pieces per row
     constexpr int PP = 16 * CPR / 64;  // pieces per lane and step
     constexpr int STEPS = 2 * C::TM;
+    constexpr int AHEAD = YF32 ? 1 : 3;
     static_assert(16 * SROW * 4 <= C::XSLOT * 16 && 16 * SROW * 4 <= C::WSLOT * 16,
                   "staging fits one slot");
     static_assert(PP * 64 == 16 * CPR, "whole pieces");
-    EpiOperands<8, YF32> eo[2][PP];
-    int mr[2][PP];
+    EpiOperands<8, YF32> eo[AHEAD + 1][PP];
     const int pr = lane / CPR, pc = 8 * (lane % CPR);  // this lane's row (of 64 / CPR) and column
-    const int col = c0 + pc;
-    auto operands = [&](int st, int b) {
+    const int col = c0 + pc, colc = min(col, N - 8);
+    EpiOperands<8, YF32> fixed;
+    fixed.load_bias(epi, colc);
+    auto row_of = [&](int st, int q) { return wm0 + 16 * st + pr + q * (64 / CPR); };
+    auto operands = [&](int st) {
 #pragma unroll
-        for (int q = 0; q < PP; ++q) {
-            const int rr = min(r0 + 16 * st + pr + q * (64 / CPR), M - 1);
-            mr[b][q] = SEGROWS ? perm[rr] : rr;
-            eo[b][q].load(epi, mr[b][q], min(col, N - 8), N);
-        }
+        for (int q = 0; q < PP; ++q) eo[st % (AHEAD + 1)][q].load_row(epi, rows.m[row_of(st, q)], colc, N);
     };
-    operands(0, 0);
+#pragma unroll
+    for (int st = 0; st < AHEAD; ++st) operands(st);
 #pragma unroll
     for (int st = 0; st < STEPS; ++st) {
         const int i = st >> 1, h = st & 1;
-        if (st + 1 < STEPS) operands(st + 1, (st + 1) & 1);
+        if (st + AHEAD < STEPS) operands(st + AHEAD);
 #pragma unroll
         for (int j = 0; j < C::TN; ++j)
 #pragma unroll
@@ -276,17 +302,22 @@ __device__ __forceinline__ void store_epilogue(const f32x16_t (&acc)[C::TM][C::T
             const float4 a = *reinterpret_cast<const float4 *>(sp);
             const float4 b = *reinterpret_cast<const float4 *>(sp + 4);
             float z[8] = {a.x, a.y, a.z, a.w, b.x, b.y, b.z, b.w};
-            eo[st & 1][q].apply(epi, z);
-            if (r0 + 16 * st + pr + q * (64 / CPR) < M && col < N) {
-                const size_t at = (size_t)mr[st & 1][q] * N + col;
+            const int lr = row_of(st, q);
+            EpiOperands<8, YF32> &o = eo[st % (AHEAD + 1)][q];
+#pragma unroll
+            for (int w = 0; w < 4; ++w) o.b[w] = fixed.b[w];
+            o.rs = rows.scale[lr];
+            o.apply(epi, z);
+            if (row0 + lr < M && col < N) {
+                const size_t at = (size_t)rows.m[lr] * N + col;
                 if constexpr (YF32) {
                     float4 *yf = reinterpret_cast<float4 *>(reinterpret_cast<float *>(y) + at);
                     yf[0] = make_float4(z[0], z[1], z[2], z[3]);
                     yf[1] = make_float4(z[4], z[5], z[6], z[7]);
                 } else {
-                    st16(reinterpret_cast<uint16_t *>(y) + at,
-                         make_uint4(pack_bf16x2(z[0], z[1]), pack_bf16x2(z[2], z[3]),
-                                    pack_bf16x2(z[4], z[5]), pack_bf16x2(z[6], z[7])));
+                    st16_nt(reinterpret_cast<uint16_t *>(y) + at,
+                            make_uint4(cvt_bf16x2(z[0], z[1]), cvt_bf16x2(z[2], z[3]),
+                                       cvt_bf16x2(z[4], z[5]), cvt_bf16x2(z[6], z[7])));
                 }
             }
         }

@@ -49,8 +49,14 @@ __device__ __forceinline__ void unpack8(const uint4 v, float f[8]) {
     f[6] = bf16_lo(v.w); f[7] = bf16_hi(v.w);
 }
 
-// 8 E4M3 codes (two dwords) -> 8 bf16 of the same values (exact)
 typedef __bf16 bf16x2_t __attribute__((ext_vector_type(2)));
+// The same rounding in one instruction (v_cvt_pk_bf16_f32).
+__device__ __forceinline__ uint32_t cvt_bf16x2(float lo, float hi) {
+    typedef float f32x2_t __attribute__((ext_vector_type(2)));
+    return __builtin_bit_cast(uint32_t, __builtin_convertvector(f32x2_t{lo, hi}, bf16x2_t));
+}
+
+// 8 E4M3 codes (two dwords) -> 8 bf16 of the same values (exact)
 __device__ __forceinline__ uint4 e4m3x8_to_bf16(uint32_t lo, uint32_t hi) {
     const bf16x2_t a = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(lo, 1.0f, false);
     const bf16x2_t b = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(lo, 1.0f, true);
@@ -62,6 +68,11 @@ __device__ __forceinline__ uint4 e4m3x8_to_bf16(uint32_t lo, uint32_t hi) {
 
 __device__ __forceinline__ uint4 ld16(const void *p) { return *reinterpret_cast<const uint4 *>(p); }
 __device__ __forceinline__ void st16(void *p, uint4 v) { *reinterpret_cast<uint4 *>(p) = v; }
+// A store of data that this kernel does not read again (nontemporal).
+__device__ __forceinline__ void st16_nt(void *p, uint4 v) {
+    typedef uint32_t u32x4_t __attribute__((ext_vector_type(4)));
+    __builtin_nontemporal_store(u32x4_t{v.x, v.y, v.z, v.w}, reinterpret_cast<u32x4_t *>(p));
+}
 // A store that writes through the L2 to memory (sc0 sc1), for data only a later kernel reads:
 // the end-of-kernel write-back then finds no dirty lines of it.  A vector store; p is global.
 __device__ __forceinline__ void st_wt(float *p, float v) {

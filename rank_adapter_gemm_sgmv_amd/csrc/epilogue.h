@@ -6,11 +6,11 @@
 // z is x W plus the adapter's delta.  Every kernel that writes y applies it where the fp32 sum
 // is still in registers, so the four optional operands cost their own bytes and nothing else.
 //
-// Activations use the hardware's exp2 and reciprocal (about 1 ulp each); exp's argument is
-// rounded once, a relative error of |z| 2^-24 in e^z where e^z matters (|z| of a few).  GELU's
-// Gaussian is Abramowitz and Stegun 7.1.26 in its erfc form, |error| <= 1.5e-7: the library's
-// erf costs three times the instructions, which a prefill tile cannot hide behind MFMAs (its
-// epilogue runs after the last of them).
+// Activations use the hardware's exp2 and reciprocal (about 1 ulp each); exp2's argument is
+// rounded once or twice, a relative error of |z| 2^-23 in e^z where e^z matters (|z| of a few).
+// GELU's Gaussian is Abramowitz and Stegun 7.1.26 in its erfc form, |error| <= 1.5e-7: the
+// library's erf costs three times the instructions, which a prefill tile cannot hide behind
+// MFMAs (its epilogue runs after the last of them).
 #pragma once
 
 #include "common.h"
@@ -34,31 +34,49 @@ __device__ __forceinline__ void ld_words(uint32_t (&r)[W], const void *p) {
     }
 }
 
-__device__ __forceinline__ float epi_sigmoid(float z) {  // 1 / (1 + e^-z); 0 where e^-z overflows
-    return __builtin_amdgcn_rcpf(1.0f + __expf(-z));
+constexpr float kLog2e = 1.4426950408889634f;
+
+// z / (1 + e^-z); e^-z overflows to a factor of 0
+__device__ __forceinline__ float epi_silu(float z) {
+    return z * __builtin_amdgcn_rcpf(1.0f + __builtin_amdgcn_exp2f(-kLog2e * z));
 }
 
-// Phi(z), the standard normal distribution: erfc(|u|) / 2 on one side, its complement on the
-// other, u = z / sqrt(2)
-__device__ __forceinline__ float epi_normal_cdf(float z) {
-    const float u = fabsf(z) * 0.70710678118654752f;
-    const float t = __builtin_amdgcn_rcpf(fmaf(0.3275911f, u, 1.0f));
-    float p = fmaf(1.061405429f, t, -1.453152027f);
-    p = fmaf(p, t, 1.421413741f);
-    p = fmaf(p, t, -0.284496736f);
-    p = fmaf(p, t, 0.254829592f);
-    const float half = 0.5f * p * t * __expf(-u * u);
-    return z < 0.0f ? half : 1.0f - half;
+// z (1 + tanh v) / 2 = z / (1 + e^-2v), v = sqrt(2 / pi) (z + 0.044715 z^3)
+__device__ __forceinline__ float epi_gelu_tanh(float z) {
+    constexpr float c1 = -2.0f * 0.79788456080286536f * kLog2e;
+    const float e = __builtin_amdgcn_exp2f(z * fmaf(0.044715f * c1, z * z, c1));
+    return z * __builtin_amdgcn_rcpf(1.0f + e);
 }
 
-// SiLU is z sigmoid(z), the tanh form of GELU z sigmoid(2 sqrt(2 / pi) (z + 0.044715 z^3)),
-// since (1 + tanh v) / 2 = sigmoid(2 v): one code for both, with c the cubic's coefficients.
-__device__ __forceinline__ float epi_act(float z, int act) {
-    if (act == LORA_ACT_RELU) return z < 0.0f ? 0.0f : z;  // (a NaN stays one)
-    if (act == LORA_ACT_GELU) return z * epi_normal_cdf(z);
-    const float c1 = act == LORA_ACT_SILU ? 1.0f : 1.5957691216057308f;
-    const float c3 = act == LORA_ACT_SILU ? 0.0f : 0.071354816272600f;
-    return z * epi_sigmoid(fmaf(c3 * z * z, z, c1 * z));
+// z Phi(z) = max(z, 0) - |z| erfc(|z| / sqrt(2)) / 2, with erfc(u) = t (a1 + t (a2 + ...)) e^-u^2,
+// t = 1 / (1 + p u); |z| is kept finite against 0 (it is inf - inf 0 otherwise)
+__device__ __forceinline__ float epi_gelu(float z) {
+    const float t = __builtin_amdgcn_rcpf(fmaf(0.3275911f * 0.70710678118654752f, fabsf(z), 1.0f));
+    float p = fmaf(0.5f * 1.061405429f, t, 0.5f * -1.453152027f);
+    p = fmaf(p, t, 0.5f * 1.421413741f);
+    p = fmaf(p, t, 0.5f * -0.284496736f);
+    p = fmaf(p, t, 0.5f * 0.254829592f);
+    const float tail = p * t * __builtin_amdgcn_exp2f(-0.5f * kLog2e * z * z);
+    return fmaf(-fminf(fabsf(z), 3e38f), tail, fmaxf(z, 0.0f));
+}
+
+// The activation of V elements (one branch for all of them).
+template <int V>
+__device__ __forceinline__ void epi_act(float (&z)[V], int act) {
+    if (act == LORA_ACT_NONE) return;
+    if (act == LORA_ACT_SILU) {
+#pragma unroll
+        for (int i = 0; i < V; ++i) z[i] = epi_silu(z[i]);
+    } else if (act == LORA_ACT_GELU) {
+#pragma unroll
+        for (int i = 0; i < V; ++i) z[i] = epi_gelu(z[i]);
+    } else if (act == LORA_ACT_GELU_TANH) {
+#pragma unroll
+        for (int i = 0; i < V; ++i) z[i] = epi_gelu_tanh(z[i]);
+    } else {
+#pragma unroll
+        for (int i = 0; i < V; ++i) z[i] = z[i] < 0.0f ? 0.0f : z[i];  // (a NaN stays one)
+    }
 }
 
 // The operands of V consecutive elements of one row, loaded ahead of their use.
@@ -69,9 +87,15 @@ struct EpiOperands {
     float rs;
 
     __device__ __forceinline__ void load(const Epilogue &e, int m, int n, int N) {
-        const size_t at = ((size_t)m * N + n) * (YF32 ? 4 : 2);
         rs = e.row_scale ? e.row_scale[m] : 1.0f;
+        load_bias(e, n);
+        load_row(e, m, n, N);
+    }
+    __device__ __forceinline__ void load_bias(const Epilogue &e, int n) {
         if (e.bias) ld_words(b, e.bias + n);
+    }
+    __device__ __forceinline__ void load_row(const Epilogue &e, int m, int n, int N) {
+        const size_t at = ((size_t)m * N + n) * (YF32 ? 4 : 2);
         if (e.mul) ld_words(mu, static_cast<const char *>(e.mul) + at);
         if (e.residual) ld_words(re, static_cast<const char *>(e.residual) + at);
     }
@@ -81,19 +105,22 @@ struct EpiOperands {
     }
     // z -> y, element by element
     __device__ __forceinline__ void apply(const Epilogue &e, float (&z)[V]) const {
+        if (e.row_scale) {
 #pragma unroll
-        for (int i = 0; i < V; ++i) {
-            if (e.row_scale) z[i] *= rs;
-            if (e.bias) z[i] += (i & 1) ? bf16_hi(b[i / 2]) : bf16_lo(b[i / 2]);
+            for (int i = 0; i < V; ++i) z[i] *= rs;
         }
-        if (e.act != LORA_ACT_NONE) {
+        if (e.bias) {
 #pragma unroll
-            for (int i = 0; i < V; ++i) z[i] = epi_act(z[i], e.act);
+            for (int i = 0; i < V; ++i) z[i] += (i & 1) ? bf16_hi(b[i / 2]) : bf16_lo(b[i / 2]);
         }
+        epi_act<V>(z, e.act);
+        if (e.mul) {
 #pragma unroll
-        for (int i = 0; i < V; ++i) {
-            if (e.mul) z[i] *= of(mu, i);
-            if (e.residual) z[i] += of(re, i);
+            for (int i = 0; i < V; ++i) z[i] *= of(mu, i);
+        }
+        if (e.residual) {
+#pragma unroll
+            for (int i = 0; i < V; ++i) z[i] += of(re, i);
         }
     }
 };

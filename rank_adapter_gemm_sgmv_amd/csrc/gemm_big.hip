@@ -145,6 +145,8 @@ __global__ __launch_bounds__(C::NT) void gemm_big_kernel(const uint16_t *__restr
     int tmi, tni;
     tile_of(blockIdx.x, n_tm, n_tn, tmi, tni);
     const int row0 = tmi * C::BM, n0 = tni * C::BN;
+    __shared__ RowTable<C> rows;
+    const int my_row = LORA ? seg.perm[min(row0 + tid, M - 1)] : 0;
 
     // DMA sources of this lane (rows beyond M and columns beyond N are clamped in bounds;
     // their results are never stored)
@@ -195,6 +197,7 @@ __global__ __launch_bounds__(C::NT) void gemm_big_kernel(const uint16_t *__restr
         issue_stage<C>(src, X0, W0, wave, 0, N);
         issue_stage<C>(src, X1, W1, wave, min(1, nmain - 1) * kBK, N);
         issue_stage<C>(src, X2, W2, wave, min(2, nmain - 1) * kBK, N);
+        if constexpr (LORA) fill_row<C>(rows, my_row, ep.ids, epi.row_scale, tid);
         wait_vm<2 * C::PER>();
         lds_barrier();
         read_frags<C>(fa, X0, W0, lane, wm0, wn0);
@@ -214,6 +217,8 @@ __global__ __launch_bounds__(C::NT) void gemm_big_kernel(const uint16_t *__restr
         }
 #undef LORA_BIG_STEP
         wait_vm<0>();
+    } else if constexpr (LORA) {
+        fill_row<C>(rows, my_row, ep.ids, epi.row_scale, tid);
     }
     // remaining steps (K not a multiple of 128), the last one possibly partial: through
     // registers into slot 0, zero beyond K
@@ -224,7 +229,8 @@ __global__ __launch_bounds__(C::NT) void gemm_big_kernel(const uint16_t *__restr
         mfma_stage<C>(acc, X0, W0, lane, wm0, wn0);
     }
 
-    if constexpr (LORA) add_lora_runs<C>(acc, X0, W0, ep, seg, M, N, row0, n0, tid, lane, wm0, wn0);
+    if constexpr (LORA)
+        add_lora_runs<C>(acc, X0, W0, ep, seg, rows, M, N, row0, n0, tid, lane, wm0, wn0);
 
     // store: accumulator element v of a 32 x 32 block is row (v/4)*8 + (lane/32)*4 + v%4,
     // column lane%32.
@@ -233,8 +239,8 @@ __global__ __launch_bounds__(C::NT) void gemm_big_kernel(const uint16_t *__restr
         // wave w stages in slot w of X0 .. X3, W0 .. W3
         uint4 *const sl = wave == 0 ? X0 : wave == 1 ? X1 : wave == 2 ? X2 : wave == 3 ? X3
                         : wave == 4 ? W0 : wave == 5 ? W1 : wave == 6 ? W2 : W3;
-        store_epilogue<C, SEGROWS, YF32>(acc, reinterpret_cast<float *>(sl), epi, y, seg.perm, M, N,
-                                         row0 + wm0, n0 + wn0, lane);
+        store_epilogue<C, YF32>(acc, reinterpret_cast<float *>(sl), epi, y, rows, M, N, row0, wm0,
+                                n0 + wn0, lane);
     } else if constexpr (YF32) {
 #pragma unroll
         for (int i = 0; i < C::TM; ++i) {

@@ -71,12 +71,10 @@ __device__ __forceinline__ NormFactors norm_factors(float r, float top) {
 // and the reader that follows takes it from memory's own cache.  Residual, sum and both
 // outputs at d 4096, plain stores -> these: 10.7 -> 8.3 us at 1024 rows, 54.0 -> 51.8 us at
 // 8192 (5.8 TB/s; a large copy reaches 5.5), the same at 64 rows and below.
-typedef uint32_t u32x4_t __attribute__((ext_vector_type(4)));
 typedef uint32_t u32x2_t __attribute__((ext_vector_type(2)));
 __device__ __forceinline__ void st_bf16x8(uint16_t *p, const float f[8], float k) {
-    const u32x4_t v = {pack_bf16x2(f[0] * k, f[1] * k), pack_bf16x2(f[2] * k, f[3] * k),
-                       pack_bf16x2(f[4] * k, f[5] * k), pack_bf16x2(f[6] * k, f[7] * k)};
-    __builtin_nontemporal_store(v, reinterpret_cast<u32x4_t *>(p));
+    st16_nt(p, make_uint4(cvt_bf16x2(f[0] * k, f[1] * k), cvt_bf16x2(f[2] * k, f[3] * k),
+                          cvt_bf16x2(f[4] * k, f[5] * k), cvt_bf16x2(f[6] * k, f[7] * k)));
 }
 
 __device__ __forceinline__ void norm_store8(const NormArgs &a, size_t at, const float h[8],
