@@ -77,6 +77,12 @@ size_t gemm_bytes(int32_t M, int32_t d_in, int32_t d_out, int32_t r_max, int32_t
     return round_up((a > b ? a : b) * sizeof(float));
 }
 
+// The same of lora_linear_fp8: its tiles' K slices or, for decode batches, the decode plans'.
+size_t fp8_gemm_bytes(int32_t M, int32_t d_in, int32_t d_out, int32_t r_max, int32_t n_adapters) {
+    const size_t a = fp8_partial_floats(M, d_in, d_out),
+                 b = decode_fp8_partial_floats(M, d_in, d_out, rank_bucket(r_max), n_adapters);
+    return round_up((a > b ? a : b) * sizeof(float));
+}
 
 thread_local hipError_t g_last_hip_error = hipSuccess;
 
@@ -548,8 +554,17 @@ lora_status_t check_fp8w(const void *x, const void *W8, const float *w_scale, co
 
 namespace {
 
-// lora_linear_fp8: build_segments, the shrink on the codes (chunk sums), then the fp8 GEMM with
-// delta and epilogue, or its split-K slices and the pass that adds slices, delta and epilogue.
+// lora_linear_fp8 (arguments already validated, M > 0):
+//   up to 128 rows, pool padded at a rank bucket: the split-K fp8 GEMM with the shrink as
+//            adapter tiles of the same launch, then the reduction (two launches, no segments)
+//   up to 192 rows: the split-K fp8 GEMM with build_segments in one extra workgroup, the shrink
+//            on the codes (chunk sums), the reduction
+//   otherwise: build_segments, the shrink, then the 128 x 128 or 256 x 256 tiles of gemm_fp8.hip
+//            with delta and epilogue fused or, where they are too few to fill the chip, K
+//            slices and the pass that adds slices, delta and epilogue
+// 4096 x 4104, rank 16, us per call of the three: 1 row 12.4, 15.8, 29.1; 64 rows 17.5, 18.4, 38.6;
+// 117 rows 20.8, 24.0, 40.7; 160 rows -, 31.2, 41.8; 256 rows -, 42.1, 44.7 (11008 x 4096 with 256
+// adapters: 69.6, 61.8).
 hipError_t run_fp8(const Fp8Gemm &g, const uint16_t *A, const uint16_t *B, const float *scale,
                    const int32_t *ranks, const int32_t *ids, int32_t r_max, int32_t n_adapters,
                    const lora_segments_t *segs, const Epilogue &epi, void *y, bool y_f32, void *ws,
@@ -563,6 +578,24 @@ hipError_t run_fp8(const Fp8Gemm &g, const uint16_t *A, const uint16_t *B, const
     int kc, ksplit;
     shrink_plan(g.K, rb, &kc, &ksplit);
     hipError_t e;
+    const DecodeLora lo{spart, ksplit, B, scale, ids, ranks, rb, n_adapters, nullptr, 0, r_max};
+    const bool decode = decode_fp8_supported(g.M, g.K, g.N);
+    if (decode && g.M <= kDecodeMaxRows && r_max == rb) {
+        if ((e = launch_decode_gemm_fp8_lora_x8(g.x8, g.W8, g.w_scale, A, g.M, g.K, g.N, lo, gpart, s)) !=
+            hipSuccess)
+            return e;
+        return launch_decode_reduce(gpart, g.M, g.K, g.N, y, y_f32, lo, true, nullptr, s, &epi);
+    }
+    if (decode) {
+        const SegBuild bld{ids, n_adapters, sg};
+        if ((e = launch_decode_gemm_fp8_x8(g.x8, g.W8, g.w_scale, g.M, g.K, g.N, gpart,
+                                           segs ? nullptr : &bld, s)) != hipSuccess)
+            return e;
+        if ((e = launch_shrink_x8(g.x8, A, ranks, r_max, g.M, g.K, rb, n_adapters, sg, spart, kc, ksplit,
+                                  s)) != hipSuccess)
+            return e;
+        return launch_decode_reduce(gpart, g.M, g.K, g.N, y, y_f32, lo, false, &sg, s, &epi);
+    }
     if (!segs && (e = launch_build_segments(ids, g.M, n_adapters, sg, s)) != hipSuccess) return e;
     if ((e = launch_shrink_x8(g.x8, A, ranks, r_max, g.M, g.K, rb, n_adapters, sg, spart, kc, ksplit,
                               s)) != hipSuccess)
@@ -1122,7 +1155,7 @@ size_t lora_fp8_workspace_bytes(int32_t M, int32_t d_in, int32_t d_out, int32_t 
         return 0;
     if (M == 0) return 0;
     return segments_bytes(M, n_adapters) + shrink_partial_bytes(M, d_in, r_max) +
-           round_up(fp8_partial_floats(M, d_in, d_out) * sizeof(float));
+           fp8_gemm_bytes(M, d_in, d_out, r_max, n_adapters);
 }
 
 lora_status_t lora_linear_fp8(const void *x8, const float *x_scale, const void *W8,

@@ -320,6 +320,18 @@ hipError_t launch_decode_gemm_fp8_lora(const uint16_t *x, const uint8_t *W8, con
                                        const uint16_t *A, int M, int K, int N,
                                        const DecodeLora &lo, float *partial, hipStream_t s);
 
+// Both with E4M3 x (lora_linear_fp8; the rows' scales are the reduction's epilogue's), for which
+// K may be any multiple of 16 from 128 (decode_fp8_supported).
+constexpr int kFp8DecodeMaxRows = 192;
+bool decode_fp8_supported(int M, int K, int N);
+size_t decode_fp8_partial_floats(int M, int K, int N, int r_max, int n_adapters);
+hipError_t launch_decode_gemm_fp8_x8(const uint8_t *x8, const uint8_t *W8, const float *w_scale,
+                                     int M, int K, int N, float *partial, const SegBuild *build,
+                                     hipStream_t s);
+hipError_t launch_decode_gemm_fp8_lora_x8(const uint8_t *x8, const uint8_t *W8, const float *w_scale,
+                                          const uint16_t *A, int M, int K, int N,
+                                          const DecodeLora &lo, float *partial, hipStream_t s);
+
 // y = (split partials added in order) + scale_a * t B_a, t from the adapter tiles' splits
 // (`adapters`) or from the segment-path shrink's chunk sums; rounds once into y.  With the
 // chunk sums and `seg` (the segments of these ids, nullable) the rows of one adapter share

@@ -117,14 +117,14 @@ __device__ __forceinline__ bool dec_adapter_src(S &src, const DecodeLora &lo, co
 // x rows m0 .. m0 + BM of a tile: lane l fills position l % 8 of row 8 q + l / 8, chunk
 // (l % 8) ^ (l / 8); rows past the batch repeat its last.
 template <class C, class S>
-__device__ __forceinline__ void dec_x_src(S &src, const uint16_t *x, int M, int K, int m0,
+__device__ __forceinline__ void dec_x_src(S &src, const typename C::X *x, int M, int K, int m0,
                                           int lane) {
 #pragma unroll
     for (int q = 0; q < C::XINS; ++q) {
         const int row = 8 * q + (lane >> 3);
         const int lc = (lane & 7) ^ (lane >> 3);
         const int m = min(m0 + row, M - 1);
-        src.xp[q] = x + (size_t)m * K + lc * 8;
+        src.xp[q] = x + (size_t)m * K + lc * (16 / (int)sizeof(typename C::X));
     }
 }
 
@@ -288,11 +288,15 @@ __global__ __launch_bounds__(kThreads) void decode_gemm_kernel(
 //    accumulators.
 constexpr int kF8K = 128;  // k per fp8 stage
 
-template <int BM_>
+// X8: x holds E4M3 codes too (lora_linear_fp8): row r, 16-k chunk kc at slot 8 r + (kc ^ ((r >> 1) &
+// 7)), as a column of W8, and the codes become bf16 as they are read for the MFMAs.
+template <int BM_, bool X8_ = false>
 struct DecF8 {
     static constexpr int BM = BM_;
+    static constexpr bool X8 = X8_;
+    using X = std::conditional_t<X8, uint8_t, uint16_t>;
     static constexpr int TM = BM / 32;
-    static constexpr int XSLOT = BM * kF8K * 2 / 16;      // uint4 per x stage
+    static constexpr int XSLOT = BM * kF8K * (int)sizeof(X) / 16;  // uint4 per x stage
     static constexpr int WSLOT_W = 32 * kF8K / 16;         // uint4 per W stage of one wave
     static constexpr int XI = XSLOT / kWaves / 64;         // x loads per wave per stage
     static constexpr int WI = WSLOT_W / 64;                // W loads per wave per stage (4)
@@ -316,7 +320,7 @@ __device__ __forceinline__ bf16x8_t dec_fp8x8(uint32_t lo, uint32_t hi) {
 // tiles per split), through the L2 with WT (small batches, as dec_tile_out).  Every thread
 // must call it (barriers).
 template <class C, bool WT>
-__device__ __forceinline__ void f8_tile(uint4 *lds, const uint16_t *__restrict__ x,
+__device__ __forceinline__ void f8_tile(uint4 *lds, const typename C::X *__restrict__ x,
                                         const uint8_t *__restrict__ W8,
                                         const float *__restrict__ w_scale, int M, int K, int N,
                                         int n_tiles, int tile, int split, int tm, int tn,
@@ -342,13 +346,20 @@ __device__ __forceinline__ void f8_tile(uint4 *lds, const uint16_t *__restrict__
     }
     // x load q of a stage, lane l (this wave's part): row r = 4 (XI wave + q) + l / 16, chunk
     // (l % 16) ^ (r % 16), to slot 16 r + (l % 16) (rows past the batch repeat its last)
-    const uint16_t *xp[C::XI];
+    // (X8: row r = 8 (XI wave + q) + l / 8, chunk (l % 8) ^ ((r >> 1) & 7), to slot 8 r + (l % 8))
+    const typename C::X *xp[C::XI];
     int xlc[C::XI];
 #pragma unroll
     for (int q = 0; q < C::XI; ++q) {
-        const int r = 4 * (C::XI * wave + q) + (lane >> 4);
-        xp[q] = x + (size_t)min(m0 + r, M - 1) * K;
-        xlc[q] = (lane & 15) ^ (r & 15);
+        if constexpr (C::X8) {
+            const int r = 8 * (C::XI * wave + q) + (lane >> 3);
+            xp[q] = x + (size_t)min(m0 + r, M - 1) * K;
+            xlc[q] = (lane & 7) ^ ((r >> 1) & 7);
+        } else {
+            const int r = 4 * (C::XI * wave + q) + (lane >> 4);
+            xp[q] = x + (size_t)min(m0 + r, M - 1) * K;
+            xlc[q] = (lane & 15) ^ (r & 15);
+        }
     }
 
     auto issue = [&](int u, uint4 *slot) {
@@ -358,7 +369,8 @@ __device__ __forceinline__ void f8_tile(uint4 *lds, const uint16_t *__restrict__
         uint4 *xs = slot, *ws = slot + C::XSLOT + wave * C::WSLOT_W;
 #pragma unroll
         for (int q = 0; q < C::XI; ++q)
-            dma16(xp[q] + min(k0 + 8 * xlc[q], K - 8), (const lds_void_t *)&xs[(C::XI * wave + q) * 64]);
+            dma16(xp[q] + min(k0 + (C::X8 ? 16 : 8) * xlc[q], K - (C::X8 ? 16 : 8)),
+                  (const lds_void_t *)&xs[(C::XI * wave + q) * 64]);
 #pragma unroll
         for (int q = 0; q < C::WI; ++q)
             dma16(wp[q] + min(k0 + 16 * wkc[q], klast), (const lds_void_t *)&ws[q * 64]);
@@ -394,7 +406,13 @@ __device__ __forceinline__ void f8_tile(uint4 *lds, const uint16_t *__restrict__
 #pragma unroll
             for (int i = 0; i < C::TM; ++i) {
                 const int r = 32 * i + c;
-                const bf16x8_t a = *reinterpret_cast<const bf16x8_t *>(&xs[16 * r + ((2 * st + g) ^ (r & 15))]);
+                bf16x8_t a;
+                if constexpr (C::X8) {
+                    const u32x2_t xv = *(const lds_u32x2_t *)((const lds_char_t *)xs + (8 * r + (st ^ ((r >> 1) & 7))) * 16 + 8 * g);
+                    a = dec_fp8x8(xv[0], xv[1]);
+                } else {
+                    a = *reinterpret_cast<const bf16x8_t *>(&xs[16 * r + ((2 * st + g) ^ (r & 15))]);
+                }
                 acc[i][st & 1] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(a, b, acc[i][st & 1], 0, 0, 0);
             }
         }
@@ -421,7 +439,7 @@ __device__ __forceinline__ void f8_tile(uint4 *lds, const uint16_t *__restrict__
 // segments instead.
 template <class C, bool BUILD>
 __global__ __launch_bounds__(kThreads) void decode_gemm_fp8_kernel(
-    const uint16_t *__restrict__ x, const uint8_t *__restrict__ W8, const float *__restrict__ w_scale,
+    const typename C::X *__restrict__ x, const uint8_t *__restrict__ W8, const float *__restrict__ w_scale,
     int M, int K, int N, int n_tm, int n_tn, int k_per_split, float *__restrict__ partial,
     int n_gemm_blocks, SegBuild build) {
     __shared__ __attribute__((aligned(1024))) uint4 lds[C::LDS16];
@@ -457,10 +475,10 @@ __global__ __launch_bounds__(kThreads) void decode_gemm_fp8_kernel(
 // decode_gemm_kernel.  Both kinds of workgroup share one LDS array sized for the larger.
 template <class CF, class CB, int RM>
 __global__ __launch_bounds__(kThreads) void decode_gemm_fp8_lora_kernel(
-    const uint16_t *__restrict__ x, const uint8_t *__restrict__ W8, const float *__restrict__ w_scale,
+    const typename CF::X *__restrict__ x, const uint8_t *__restrict__ W8, const float *__restrict__ w_scale,
     const uint16_t *__restrict__ A, int M, int K, int N, int n_tm, int n_tn, int n_lt,
     int k_per_split, float *__restrict__ partial, DecodeLora lo, int n_gemm_blocks) {
-    static_assert(CF::BM == CB::BM && CF::TILE == CB::TILE, "one tile shape");
+    static_assert(CF::BM == CB::BM && CF::TILE == CB::TILE && CF::X8 == CB::X8, "one tile shape");
     constexpr int L16 = CF::LDS16 > kWaves * CB::WAVE ? CF::LDS16 : kWaves * CB::WAVE;
     __shared__ __attribute__((aligned(1024))) uint4 lds[L16];
 
@@ -952,6 +970,28 @@ bool decode_fused_supported(int M, int K, int N) {
     return decode_gemm_supported(M, K, N) && M <= kDecodeMaxRows;
 }
 
+// The split plan itself and the 8-bit x (16-code chunks) need K in 16s only; the bf16 calls keep
+// decode_gemm_supported's 32.
+static bool decode_plan_ok(int M, int K, int N) {
+    return M >= 1 && M <= kDecodeGemmMaxRows && K % 16 == 0 && K >= 128 && N >= 8 && N % 4 == 0;
+}
+
+bool decode_fp8_supported(int M, int K, int N) {
+    return decode_plan_ok(M, K, N) && M <= kFp8DecodeMaxRows && N % 8 == 0;
+}
+
+size_t decode_fp8_partial_floats(int M, int K, int N, int r_max, int n_adapters) {
+    if (!decode_fp8_supported(M, K, N)) return 0;
+    const DecPlan p0 = dec_plan(M, K, N, 0);
+    size_t f = (size_t)p0.ks * p0.n_tm * p0.n_tn * p0.bm * kBN;
+    if (M <= kDecodeMaxRows) {
+        const DecPlan p = dec_plan(M, K, N, adapter_tiles(M, r_max, n_adapters));
+        const size_t fa = (size_t)p.ks * p.n_tm * (p.n_tn + p.n_lt) * p.bm * kBN;
+        if (fa > f) f = fa;
+    }
+    return f;
+}
+
 size_t decode_gemm_partial_floats(int M, int K, int N, int r_max, int n_adapters) {
     if (!decode_gemm_supported(M, K, N)) return 0;
     // every plan a call of these sizes may run: without adapter tiles (batches of 129-256
@@ -1015,10 +1055,13 @@ hipError_t launch_decode_gemm(const uint16_t *x, const uint16_t *W, const uint16
     return hipGetLastError();
 }
 
-hipError_t launch_decode_gemm_fp8(const uint16_t *x, const uint8_t *W8, const float *w_scale,
-                                  int M, int K, int N, float *partial, const SegBuild *build,
-                                  hipStream_t s) {
-    if (!decode_gemm_supported(M, K, N) || N % 8 != 0 || partial == nullptr || w_scale == nullptr)
+namespace {
+
+template <class X>
+hipError_t launch_f8(const X *x, const uint8_t *W8, const float *w_scale, int M, int K, int N,
+                     float *partial, const SegBuild *build, hipStream_t s) {
+    constexpr bool X8 = sizeof(X) == 1;
+    if (!(X8 ? decode_fp8_supported(M, K, N) : decode_gemm_supported(M, K, N)) || N % 8 != 0 || partial == nullptr || w_scale == nullptr)
         return hipErrorInvalidValue;
     if (build && (build->ids == nullptr || build->n_adapters < 1 || build->n_adapters > LORA_MAX_ADAPTERS))
         return hipErrorInvalidValue;
@@ -1028,10 +1071,10 @@ hipError_t launch_decode_gemm_fp8(const uint16_t *x, const uint8_t *W8, const fl
     const SegBuild bld = build ? *build : SegBuild{nullptr, 1, Seg{}};
 #define F8_LAUNCH(BM)                                                                          \
     if (build)                                                                                 \
-        launch((decode_gemm_fp8_kernel<DecF8<BM>, true>), grid, dim3(kThreads), 0, s, x, W8,     \
+        launch((decode_gemm_fp8_kernel<DecF8<BM, X8>, true>), grid, dim3(kThreads), 0, s, x, W8,     \
                w_scale, M, K, N, p.n_tm, p.n_tn, p.k_per_split, partial, n_gemm, bld);          \
     else                                                                                       \
-        launch((decode_gemm_fp8_kernel<DecF8<BM>, false>), grid, dim3(kThreads), 0, s, x, W8,    \
+        launch((decode_gemm_fp8_kernel<DecF8<BM, X8>, false>), grid, dim3(kThreads), 0, s, x, W8,    \
                w_scale, M, K, N, p.n_tm, p.n_tn, p.k_per_split, partial, n_gemm, bld)
     if (p.bm == 32) {
         F8_LAUNCH(32);
@@ -1042,10 +1085,11 @@ hipError_t launch_decode_gemm_fp8(const uint16_t *x, const uint8_t *W8, const fl
     return hipGetLastError();
 }
 
-hipError_t launch_decode_gemm_fp8_lora(const uint16_t *x, const uint8_t *W8, const float *w_scale,
-                                       const uint16_t *A, int M, int K, int N,
-                                       const DecodeLora &lo, float *partial, hipStream_t s) {
-    if (!decode_fused_supported(M, K, N) || N % 8 != 0 || partial == nullptr ||
+template <class X>
+hipError_t launch_f8_lora(const X *x, const uint8_t *W8, const float *w_scale, const uint16_t *A, int M,
+                          int K, int N, const DecodeLora &lo, float *partial, hipStream_t s) {
+    constexpr bool X8 = sizeof(X) == 1;
+    if (!(X8 ? decode_fp8_supported(M, K, N) : decode_gemm_supported(M, K, N)) || M > kDecodeMaxRows || N % 8 != 0 || partial == nullptr ||
         w_scale == nullptr || A == nullptr || lo.ids == nullptr || !rank_ok(lo.r_max) ||
         lo.n_adapters < 1)
         return hipErrorInvalidValue;
@@ -1053,7 +1097,7 @@ hipError_t launch_decode_gemm_fp8_lora(const uint16_t *x, const uint8_t *W8, con
     const DecPlan p = dec_plan(M, K, N, n_lt);
     const int n_gemm = p.n_tm * (p.n_tn + n_lt) * p.ks;
 #define F8L_ONE(BM, RMX)                                                                        \
-    launch((decode_gemm_fp8_lora_kernel<DecF8<BM>, Dec<BM>, RMX>), dim3(n_gemm), dim3(kThreads), \
+    launch((decode_gemm_fp8_lora_kernel<DecF8<BM, X8>, Dec<BM, X8>, RMX>), dim3(n_gemm), dim3(kThreads), \
            0, s, x, W8, w_scale, A, M, K, N, p.n_tm, p.n_tn, n_lt, p.k_per_split, partial, lo,   \
            n_gemm)
 #define F8L_RANK(BM)                                                                            \
@@ -1073,10 +1117,36 @@ hipError_t launch_decode_gemm_fp8_lora(const uint16_t *x, const uint8_t *W8, con
     return hipGetLastError();
 }
 
+}  // namespace
+
+hipError_t launch_decode_gemm_fp8(const uint16_t *x, const uint8_t *W8, const float *w_scale,
+                                  int M, int K, int N, float *partial, const SegBuild *build,
+                                  hipStream_t s) {
+    return launch_f8(x, W8, w_scale, M, K, N, partial, build, s);
+}
+
+hipError_t launch_decode_gemm_fp8_x8(const uint8_t *x8, const uint8_t *W8, const float *w_scale,
+                                     int M, int K, int N, float *partial, const SegBuild *build,
+                                     hipStream_t s) {
+    return launch_f8(x8, W8, w_scale, M, K, N, partial, build, s);
+}
+
+hipError_t launch_decode_gemm_fp8_lora(const uint16_t *x, const uint8_t *W8, const float *w_scale,
+                                       const uint16_t *A, int M, int K, int N,
+                                       const DecodeLora &lo, float *partial, hipStream_t s) {
+    return launch_f8_lora(x, W8, w_scale, A, M, K, N, lo, partial, s);
+}
+
+hipError_t launch_decode_gemm_fp8_lora_x8(const uint8_t *x8, const uint8_t *W8, const float *w_scale,
+                                          const uint16_t *A, int M, int K, int N,
+                                          const DecodeLora &lo, float *partial, hipStream_t s) {
+    return launch_f8_lora(x8, W8, w_scale, A, M, K, N, lo, partial, s);
+}
+
 hipError_t launch_decode_reduce(const float *partial, int M, int K, int N, void *y, bool y_f32,
                                 const DecodeLora &lo, bool adapters, const Seg *seg,
                                 hipStream_t s, const Epilogue *epi) {
-    if (!decode_gemm_supported(M, K, N) || partial == nullptr || !rank_ok(lo.r_max) ||
+    if (!decode_plan_ok(M, K, N) || partial == nullptr || !rank_ok(lo.r_max) ||
         (!adapters && (lo.tpart == nullptr || lo.n_chunks < 1)))
         return hipErrorInvalidValue;
     const int n_lt = adapters ? adapter_tiles(M, lo.r_max, lo.n_adapters) : 0;

@@ -9,6 +9,8 @@
 // Models Raise the Bar" (split-K for the skinny products).
 #pragma once
 
+#include <type_traits>
+
 #include "common.h"
 
 namespace lora {
@@ -24,18 +26,23 @@ typedef __attribute__((address_space(3))) char lds_char_t;
 
 constexpr int kBN = 128;  // columns of a tile
 constexpr int kBKW = 16;  // k of a W stage (one step)
-constexpr int kBKX = 64;  // k of an x stage (four steps)
+constexpr int kBKX = 64;  // k of an x stage (four steps); 128 (eight) when x holds 8-bit codes
 constexpr int kWaves = 4;
 constexpr int kThreads = 64 * kWaves;
 
 // Per wave: four W stages of 16 rows x 128 columns (256-byte rows, one direct load covers 4
 // whole rows) and two x stages of BM rows x 64 k (128-byte rows, 8 whole rows per load).  A
 // 128-column tile reads each x byte for twice the W bytes a 64-column tile did.
-template <int BM_>
+// X8: x holds E4M3 codes; a stage's rows are the same 128 bytes, so 128 k, and the codes become
+// bf16 (exactly) as they are read for the MFMAs.
+template <int BM_, bool X8_ = false>
 struct Dec {
     static constexpr int BM = BM_;
+    static constexpr bool X8 = X8_;
+    static constexpr int KX = X8 ? 2 * kBKX : kBKX;  // k of an x stage
+    using X = std::conditional_t<X8, uint8_t, uint16_t>;
     static constexpr int TM = BM / 32, TN = kBN / 32;
-    static constexpr int XSLOT = BM * kBKX * 2 / 16;     // uint4 per x stage
+    static constexpr int XSLOT = BM * kBKX * 2 / 16;     // uint4 per x stage (128-byte rows)
     static constexpr int WSLOT = kBKW * kBN * 2 / 16;    // uint4 per W stage
     static constexpr int XINS = XSLOT / 64;              // direct loads per x stage
     static constexpr int WINS = WSLOT / 64;              // direct loads per W stage
@@ -57,7 +64,8 @@ __device__ __forceinline__ void wait_lgkm0() { __builtin_amdgcn_s_waitcnt(0xC07F
 // distinct banks.  x stage rows are 128 bytes; chunk c of row r is stored at c ^ (r % 8).
 __device__ __forceinline__ int wsw(int r) { return (r & 3) << 1; }
 
-// acc += x[rows, k .. k+15] W[k .. k+15, tile]: `quarter` picks the x stage's 16 k.
+// acc += x[rows, k .. k+15] W[k .. k+15, tile]: `quarter` picks the x stage's 16 k (of four, or
+// eight with X8).
 template <class C>
 __device__ __forceinline__ void dec_mfma(f32x16_t (&acc)[C::TM][C::TN], const uint4 *__restrict__ xs,
                                          int quarter, const uint4 *__restrict__ ws, int lane) {
@@ -67,8 +75,13 @@ __device__ __forceinline__ void dec_mfma(f32x16_t (&acc)[C::TM][C::TN], const ui
 #pragma unroll
     for (int i = 0; i < C::TM; ++i) {
         const int row = 32 * i + (lane & 31);
-        const int lc = 2 * quarter + (lane >> 5);
-        af[i] = *reinterpret_cast<const bf16x8_t *>(&xs[row * 8 + (lc ^ (row & 7))]);
+        if constexpr (C::X8) {
+            const uint2 v = reinterpret_cast<const uint2 *>(&xs[row * 8 + (quarter ^ (row & 7))])[lane >> 5];
+            af[i] = __builtin_bit_cast(bf16x8_t, e4m3x8_to_bf16(v.x, v.y));
+        } else {
+            const int lc = 2 * quarter + (lane >> 5);
+            af[i] = *reinterpret_cast<const bf16x8_t *>(&xs[row * 8 + (lc ^ (row & 7))]);
+        }
     }
 #pragma unroll
     for (int j = 0; j < C::TN; ++j) {
@@ -89,14 +102,14 @@ __device__ __forceinline__ void dec_mfma(f32x16_t (&acc)[C::TM][C::TN], const ui
 
 template <class C>
 struct DecSrc {
-    const uint16_t *xp[C::XINS];
+    const typename C::X *xp[C::XINS];
     const uint16_t *wp[C::WINS];
 };
 // The same with a row stride per W load: adapters of a rank-compact pool side by side in one
 // tile, each load reading its own adapter's block (rows round8(rank) wide).
 template <class C>
 struct DecSrcVS {
-    const uint16_t *xp[C::XINS];
+    const typename C::X *xp[C::XINS];
     const uint16_t *wp[C::WINS];
     uint32_t ws[C::WINS];  // row stride of load q, elements
 };
@@ -126,7 +139,7 @@ __device__ __forceinline__ void dec_issue_w(const S &src, uint4 *__restrict__ ws
     for (int q = 0; q < C::WINS; ++q)
         dma16(src.wp[q] + (size_t)k0 * dec_wstride<C>(src, q, ldw), (const lds_void_t *)&wslot[q * 64]);
 }
-// An x stage of this wave: x[rows][k0 .. k0+63].
+// An x stage of this wave: x[rows][k0 .. k0 + KX - 1].
 template <class C, class S>
 __device__ __forceinline__ void dec_issue_x(const S &src, uint4 *__restrict__ xslot, int k0) {
 #pragma unroll
@@ -187,34 +200,40 @@ __device__ __forceinline__ void dec_kloop(f32x16_t (&acc)[C::TM][C::TN], const S
     uint4 *const X0 = mine_lds, *const X1 = mine_lds + C::XSLOT;
     uint4 *const W0 = mine_lds + 2 * C::XSLOT, *const W1 = W0 + C::WSLOT, *const W2 = W1 + C::WSLOT,
                  *const W3 = W2 + C::WSLOT;
-    // W stage s holds k = KW(s) .. +15, x stage u holds k = KX(u) .. +63; stages past the last
-    // reload the last one (an empty range loads k = 0), and an x stage that would run past K
-    // starts at K - 64 instead, its later quarters then holding the wave's last steps
-    const int kxl = nst > 0 ? min(kw0 + ((nst - 1) >> 2) * kBKX, K - kBKX) : 0;
+    // W stage s holds k = KW(s) .. +15, x stage u holds k = KX(u) .. + KX - 1; stages past the
+    // last reload the last one (an empty range loads k = 0), and an x stage that would run past K
+    // starts at K - KX instead, its later quarters then holding the wave's last steps
+    constexpr int XS = C::KX / kBKW;  // steps per x stage: 4, or 8 with X8
+    const int kxl = nst > 0 ? min(kw0 + (nst - 1) / XS * C::KX, K - C::KX) : 0;
 #define KW(S) (nst > 0 ? kw0 + min((S), nst - 1) * kBKW : 0)
-#define KX(U) (nst > 0 ? min(kw0 + (U) * kBKX, kxl) : 0)
-    // Issue order: x(0), W(0), W(1), W(2); then step s issues x(s / 4 + 1) when s % 4 == 0,
+#define KX(U) (nst > 0 ? min(kw0 + (U) * C::KX, kxl) : 0)
+    // Issue order: x(0), W(0), W(1), W(2); then step s issues x(s / XS + 1) when s % XS == 0,
     // then W(s + 3).  When step s starts, what was issued after the stages it needs (W(s),
-    // and x(s / 4), which is older) is two W stages when s % 4 is 0 or 3, and two W stages
-    // and an x stage when it is 1 or 2.
+    // and x(s / XS), which is older) is two W stages, and an x stage too when s % XS is 1 or 2.
     dec_issue_x<C>(src, X0, KX(0));
     dec_issue_w<C>(src, W0, KW(0), ldw);
     dec_issue_w<C>(src, W1, KW(1), ldw);
     dec_issue_w<C>(src, W2, KW(2), ldw);
 #define DEC_STEP(SS, PAT, XC, XN, WC, WN)                                                     \
-    if (PAT == 0 || PAT == 3) wait_vm<2 * C::WINS>();                                         \
-    else wait_vm<2 * C::WINS + C::XINS>();                                                    \
+    if (PAT == 1 || PAT == 2) wait_vm<2 * C::WINS + C::XINS>();                               \
+    else wait_vm<2 * C::WINS>();                                                              \
     wait_lgkm0();                                                                             \
-    if (PAT == 0) dec_issue_x<C>(src, XN, KX((SS) / 4 + 1));                                  \
+    if (PAT == 0) dec_issue_x<C>(src, XN, KX((SS) / XS + 1));                                 \
     dec_issue_w<C>(src, WN, KW((SS) + 3), ldw);                                               \
-    if ((SS) < nst) dec_mfma<C>(acc, XC, (kw0 + (SS) * kBKW - KX((SS) / 4)) / kBKW, WC, lane);
-    for (int s = 0; s < nst; s += 4) {
-        // x stage s / 4 is in X0 when s / 4 is even
-        uint4 *const XC = (s & 4) ? X1 : X0, *const XN = (s & 4) ? X0 : X1;
+    if ((SS) < nst) dec_mfma<C>(acc, XC, (kw0 + (SS) * kBKW - KX((SS) / XS)) / kBKW, WC, lane);
+    for (int s = 0; s < nst; s += XS) {
+        // x stage s / XS is in X0 when s / XS is even
+        uint4 *const XC = (s & XS) ? X1 : X0, *const XN = (s & XS) ? X0 : X1;
         DEC_STEP(s, 0, XC, XN, W0, W3)
         DEC_STEP(s + 1, 1, XC, XN, W1, W0)
         DEC_STEP(s + 2, 2, XC, XN, W2, W1)
         DEC_STEP(s + 3, 3, XC, XN, W3, W2)
+        if constexpr (XS == 8) {
+            DEC_STEP(s + 4, 4, XC, XN, W0, W3)
+            DEC_STEP(s + 5, 5, XC, XN, W1, W0)
+            DEC_STEP(s + 6, 6, XC, XN, W2, W1)
+            DEC_STEP(s + 7, 7, XC, XN, W3, W2)
+        }
     }
 #undef DEC_STEP
 #undef KW
