@@ -140,7 +140,7 @@ typedef struct {
  * or n_adapters <= 0. */
 int32_t lora_max_tiles(int32_t M, int32_t n_adapters);
 
-/* Workspace bytes needed by lora_linear, lora_linear_compact, lora_shrink and
+/* Workspace bytes needed by lora_linear, lora_linear_compact, lora_linear_act, lora_shrink and
  * lora_shrink_compact for these sizes (0 when M = 0): the segment buffers, t and the split-K
  * partial sums of the shrink and of the base GEMM ([P3], "MoE Models Raise the Bar": split-K
  * for the skinny products).  Returns 0 for arguments that the calls would reject.  The

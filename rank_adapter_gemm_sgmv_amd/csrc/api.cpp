@@ -71,9 +71,13 @@ size_t t_bytes(int32_t M, int32_t r_max) {
     return round_up((size_t)M * rank_bucket(r_max) * sizeof(float));
 }
 
-size_t gemm_bytes(int32_t M, int32_t d_in, int32_t d_out, int32_t r_max, int32_t n_adapters) {
+// act: what lora_linear_act may need too (its decode kernels also take a d_in that is not a
+// multiple of 32).
+size_t gemm_bytes(int32_t M, int32_t d_in, int32_t d_out, int32_t r_max, int32_t n_adapters, bool act) {
     const size_t a = gemm_partial_floats(M, d_in, d_out),
-                 b = decode_gemm_partial_floats(M, d_in, d_out, rank_bucket(r_max), n_adapters);
+                 b = act || decode_gemm_supported(M, d_in, d_out)
+                         ? decode_gemm_partial_floats(M, d_in, d_out, rank_bucket(r_max), n_adapters)
+                         : 0;
     return round_up((a > b ? a : b) * sizeof(float));
 }
 
@@ -97,6 +101,14 @@ void clear_stale_error() { (void)hipGetLastError(); }
 
 }  // namespace
 
+// Workspace of lora_linear, or (act) of lora_linear_act and every other call.
+size_t lora::linear_workspace_bytes(int32_t M, int32_t d_in, int32_t d_out, int32_t r_max, int32_t n_adapters, bool act) {
+    if (check_common(M, r_max, n_adapters) != LORA_OK || !dim_ok(d_in) || !dim_ok(d_out)) return 0;
+    if (M == 0) return 0;
+    return segments_bytes(M, n_adapters) + t_bytes(M, r_max) + shrink_partial_bytes(M, d_in, r_max) +
+           gemm_bytes(M, d_in, d_out, r_max, n_adapters, act);
+}
+
 extern "C" {
 
 int32_t lora_max_tiles(int32_t M, int32_t n_adapters) {
@@ -107,10 +119,7 @@ int32_t lora_max_tiles(int32_t M, int32_t n_adapters) {
 
 size_t lora_workspace_bytes(int32_t M, int32_t d_in, int32_t d_out, int32_t r_max,
                             int32_t n_adapters) {
-    if (check_common(M, r_max, n_adapters) != LORA_OK || !dim_ok(d_in) || !dim_ok(d_out)) return 0;
-    if (M == 0) return 0;
-    return segments_bytes(M, n_adapters) + t_bytes(M, r_max) + shrink_partial_bytes(M, d_in, r_max) +
-           gemm_bytes(M, d_in, d_out, r_max, n_adapters);
+    return linear_workspace_bytes(M, d_in, d_out, r_max, n_adapters, true);
 }
 
 lora_status_t lora_build_segments(const int32_t *ids, int32_t M, int32_t n_adapters,
@@ -256,7 +265,7 @@ lora_status_t check_linear(const void *x, const void *W, const void *A, const vo
                            const float *scale, const int32_t *ranks, const int32_t *ids, int32_t M,
                            int32_t d_in, int32_t d_out, int32_t r_max, int32_t n_adapters,
                            const lora_segments_t *segs, void *y, lora_dtype_t y_dtype,
-                           lora_mode_t mode, void *ws, size_t ws_bytes) {
+                           lora_mode_t mode, void *ws, size_t ws_bytes, bool act = false) {
     lora_status_t st = check_common(M, r_max, n_adapters);
     if (st != LORA_OK) return st;
     if (!dim_ok(d_in) || !dim_ok(d_out)) return LORA_ERR_SHAPE;
@@ -271,7 +280,7 @@ lora_status_t check_linear(const void *x, const void *W, const void *A, const vo
         !aligned(y, 16) || !aligned(ws, kAlign) || !aligned(scale, 4) || !aligned(ids, 4) ||
         (ranks && !aligned(ranks, 4)))
         return LORA_ERR_ALIGN;
-    if (ws_bytes < lora_workspace_bytes(M, d_in, d_out, r_max, n_adapters)) return LORA_ERR_WORKSPACE;
+    if (ws_bytes < linear_workspace_bytes(M, d_in, d_out, r_max, n_adapters, act)) return LORA_ERR_WORKSPACE;
     return LORA_OK;
 }
 
@@ -342,9 +351,17 @@ hipError_t run_linear(const void *x, const void *W, const void *A, const void *B
                       const lora_segments_t *segs, void *y, lora_dtype_t y_dtype, lora_mode_t mode,
                       void *ws, hipStream_t s, Marker *mk, const Epilogue *epi = nullptr) {
     bool prefill = mode == LORA_MODE_PREFILL || (mode == LORA_MODE_AUTO && M >= LORA_PREFILL_MIN_ROWS);
-    const bool flat = epi && !decode_gemm_supported(M, d_in, d_out) && gemm_splits_k(M, d_in, d_out);
-    if (epi && !flat && !decode_gemm_supported(M, d_in, d_out) && !sk_plan(M, d_in, d_out).use)
-        prefill = true;
+    // the split-K decode kernels (up to 256 rows); with an epilogue, plain split-K slices and one
+    // pass over them, or where K is not split the prefill sequence
+    const bool dec = epi ? decode_act_supported(M, d_in, d_out) : decode_gemm_supported(M, d_in, d_out);
+    const bool flat = epi && !dec && gemm_splits_k(M, d_in, d_out);
+    const bool splits = flat || (epi && sk_plan(M, d_in, d_out).use);
+    if (epi && !splits && !dec) prefill = true;
+    // AUTO batches whose 128 x 128 tiles would leave most CUs idle split K instead (decode and
+    // prefill sequence: 22 tiles 32.9 and 43.7 us, 28 tiles 38.9 and 52.9, 64 tiles 47.1 and 61.8,
+    // 52.1 and 55.6; 96 tiles 39.4 and 28.9, 112 tiles 47.0 and 37.1)
+    if (prefill && mode == LORA_MODE_AUTO && splits && (long)((M + 127) / 128) * ((d_out + 127) / 128) <= 64)
+        prefill = false;
     char *p = static_cast<char *>(ws);
     lora_segments_t own = carve_segments(p, M, n_adapters);
     float *t = reinterpret_cast<float *>(p); p += t_bytes(M, r_max);
@@ -366,7 +383,7 @@ hipError_t run_linear(const void *x, const void *W, const void *A, const void *B
     // (the fused path lays adapters side by side in slots fused_tile_rank(rb) columns wide,
     // each adapter's rows read at its own width: a padded pool's stride when that is a
     // multiple of 8 (16-byte loads), or a rank-compact adapter's round8(rank))
-    if (!prefill && (roff != nullptr || r_max % 8 == 0) && decode_fused_supported(M, d_in, d_out)) {
+    if (!prefill && (roff != nullptr || r_max % 8 == 0) && dec && M <= kDecodeMaxRows) {
         // small decode batch: x W and the shrink x A_i as tiles of one split-K GEMM, then one
         // reduction adds the splits and the expand
         const DecodeLora lo{nullptr, 0, Bb, scale, ids, ranks,
@@ -379,7 +396,7 @@ hipError_t run_linear(const void *x, const void *W, const void *A, const void *B
         mark(mk, "decode_reduce_lora");
         return hipSuccess;
     }
-    if (!prefill && decode_gemm_supported(M, d_in, d_out)) {
+    if (!prefill && dec) {
         // medium decode batch: the split-K GEMM, with the segment build in one extra
         // workgroup of the same launch (unless the caller passed segments); then the
         // segment-path shrink, whose per-chunk partial sums have the layout the decode
@@ -1135,7 +1152,7 @@ lora_status_t lora_linear_act(const void *x, const void *W, const void *A, const
                               const lora_epilogue_t *epi, void *y, lora_dtype_t y_dtype,
                               lora_mode_t mode, void *ws, size_t ws_bytes, void *stream) {
     lora_status_t st = check_linear(x, W, A, B, scale, ranks, ids, M, d_in, d_out, r_max, n_adapters,
-                                    segs, y, y_dtype, mode, ws, ws_bytes);
+                                    segs, y, y_dtype, mode, ws, ws_bytes, true);
     if (st == LORA_OK) st = check_epilogue(epi);
     if (st != LORA_OK || M == 0) return st;
     clear_stale_error();

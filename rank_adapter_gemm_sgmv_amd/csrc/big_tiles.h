@@ -143,114 +143,241 @@ __device__ __forceinline__ void tile_of(int b, int n_tm, int n_tn, int &tm, int 
 }
 
 // What the end of a tile needs of its rows (positions of perm), read once at its start, in the
-// shadow of the first stage's loads: a chain perm -> ids, row scale per step of the store cost a
-// prefill tile more than its MFMAs' last third.
+// shadow of the first stage's loads: a chain perm -> ids -> ... at every step of the delta and the
+// store took longer than their bytes do.
 template <class C>
 struct RowTable {
-    int32_t m[C::BM];    // row of x and y (rows past the last repeat it)
-    int32_t id[C::BM];   // its adapter
-    float scale[C::BM];  // its x scale (1 without)
+    int32_t m[C::BM];        // row of x and y (rows past the last repeat it)
+    int32_t id[C::BM];       // its adapter, -1 without one
+    float lora[C::BM];       // the adapter's scale
+    float scale[C::BM];      // the row's x scale (1 without)
+    int32_t run[C::BM + 1];  // first row of each run of one adapter, then BM
+    int32_t n_runs;
 };
 
 // Thread tid fills row tid, whose row of x is m (read before the first stage's loads are
 // issued; this follows them).  A barrier must come before the table is read.
 template <class C>
-__device__ __forceinline__ void fill_row(RowTable<C> &t, int m, const int32_t *ids,
-                                         const float *row_scale, int tid) {
+__device__ __forceinline__ void fill_row(RowTable<C> &t, int m, const LoraEpilogue &ep, const Seg &seg,
+                                         const float *row_scale, int row0, int tid) {
     static_assert(C::NT >= C::BM, "one row per thread");
     if (tid < C::BM) {
+        // (positions at or past the LoRA row count, and ids outside the pool -- segments not built
+        // for these ids -- have no t)
+        const int id = ep.ids[m];
+        const bool has = row0 + tid < seg.meta[1] && id >= 0 && id < ep.n_adapters;
         t.m[tid] = m;
-        t.id[tid] = ids[m];
+        t.id[tid] = has ? id : -1;
+        t.lora[tid] = has ? ep.scale[id] : 0.0f;
         t.scale[tid] = row_scale ? row_scale[m] : 1.0f;
     }
 }
 
-// The LoRA delta of one output tile (rows in segment order), after its K loop: acc += scale_a
-// t[rows, :] B_a[:, columns] for every run of one adapter among the tile's rows.  X0 and W0 are
-// LDS slots free for staging once every wave has passed the first barrier here.
-//
-// Runs of one adapter among this tile's rows (positions of perm): for each run, 16
-// rank columns at a time, stage T = scale_a * t[rows, :] (zero outside the run) in
-// slot 0's x layout as a pair of bf16 values per element -- k slots 0..15 the value
-// rounded to bf16, slots 16..31 the remainder (exact in fp32) rounded to bf16 -- and
-// B_a's same 16 rank rows twice in its W layout (zero beyond the rank), then one more
-// MFMA step.  The pair carries scale * t to about 16 significant bits, so the delta is
-// not rounded to bf16 precision before it is added.
+// The runs of the table's rows, by one wave (which must see the whole table).
 template <class C>
-__device__ __forceinline__ void add_lora_runs(f32x16_t (&acc)[C::TM][C::TN], uint4 *X0, uint4 *W0,
-                                              const LoraEpilogue &ep, const Seg &seg,
-                                              const RowTable<C> &rows, int M, int N, int row0,
-                                              int n0, int tid, int lane, int wm0, int wn0) {
-    const int n_lora = seg.meta[1];
-    const int RM = ep.r_max;
-    constexpr int kHalf = kBK / 2;
-    int p = row0;
-    const int p_end = min(row0 + C::BM, n_lora);
-    while (p < p_end) {
-        const int a = rows.id[p - row0];
-        if (a < 0 || a >= ep.n_adapters) break;  // segments not built for these ids
-        const int q_end = min(seg.offsets[a + 1], p_end);
-        if (q_end <= p) break;
-        const float s = ep.scale[a];
-        // B_a's rank rows: all of a padded pool's stride (zero past the rank), the
-        // rank's in a compact one
-        int ra = ep.roff ? min(max(ep.ranks[a], 0), RM) : ep.pstride;
-        const int brow0 = adapter_row0(ep.roff, ep.pool_rows, a, ep.pstride, ra);
-        for (int rc = 0; rc < RM; rc += kHalf) {
-            lds_barrier();
-            for (int c = tid; c < C::BM * 4; c += C::NT) {
-                const int row = c >> 2, lc = c & 3;
-                const int pos = row0 + row;
-                const int j = rc + (lc & 1) * 8;
-                uint4 v = make_uint4(0, 0, 0, 0);
-                if (pos >= p && pos < q_end && j < RM) {
-                    // t[m, j .. j+7]: the shrink's chunk sums added in chunk order, four
-                    // chunks' loads in flight at a time
-                    const float *tp = ep.tpart + (size_t)rows.m[row] * RM + j;
-                    const size_t cs = (size_t)M * RM;
-                    float t[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
-                    for (int c0 = 0; c0 < ep.n_chunks; c0 += 4) {
-                        float4 v[4][2];
+__device__ __forceinline__ void fill_runs(RowTable<C> &t, int lane) {
+    int n = 0;
 #pragma unroll
-                        for (int c = 0; c < 4; ++c) {
-                            const bool in = c0 + c < ep.n_chunks;
-                            const float *q = tp + (size_t)(in ? c0 + c : 0) * cs;
-                            v[c][0] = in ? *reinterpret_cast<const float4 *>(q) : make_float4(0.f, 0.f, 0.f, 0.f);
-                            v[c][1] = in ? *reinterpret_cast<const float4 *>(q + 4) : make_float4(0.f, 0.f, 0.f, 0.f);
-                        }
-#pragma unroll
-                        for (int c = 0; c < 4; ++c) {
-                            if (c0 + c < ep.n_chunks) {
-                                t[0] += v[c][0].x; t[1] += v[c][0].y; t[2] += v[c][0].z; t[3] += v[c][0].w;
-                                t[4] += v[c][1].x; t[5] += v[c][1].y; t[6] += v[c][1].z; t[7] += v[c][1].w;
-                            }
-                        }
-                    }
-                    float f[8];
-#pragma unroll
-                    for (int e = 0; e < 8; ++e) f[e] = s * t[e];
-                    if (lc >= 2) {  // the remainder after rounding to bf16
-#pragma unroll
-                        for (int e = 0; e < 8; ++e) f[e] -= __uint_as_float(f32_to_bf16_rne(f[e]) << 16);
-                    }
-                    v = make_uint4(pack_bf16x2(f[0], f[1]), pack_bf16x2(f[2], f[3]),
-                                   pack_bf16x2(f[4], f[5]), pack_bf16x2(f[6], f[7]));
-                }
-                X0[row * 4 + (lc ^ ((row >> 2) & 3))] = v;
-            }
-            for (int c = tid; c < kBK * C::WCH; c += C::NT) {
-                const int r = c / C::WCH, lc = c % C::WCH;
-                const int rank = rc + (r & (kHalf - 1));
-                const int n = n0 + lc * 8;
-                uint4 v = make_uint4(0, 0, 0, 0);
-                if (rank < ra && n < N) v = ld16(ep.B + ((size_t)brow0 + rank) * N + n);
-                W0[r * C::WCH + (lc ^ ((r & 3) << 2))] = v;
-            }
-            __syncthreads();
-            mfma_stage<C>(acc, X0, W0, lane, wm0, wn0);
-        }
-        p = q_end;
+    for (int r0 = 0; r0 < C::BM; r0 += 64) {
+        const int r = r0 + lane;
+        const bool first = r == 0 || t.id[r] != t.id[r - 1];
+        const uint64_t mask = __ballot(first);
+        if (first) t.run[n + __popcll(mask & ((1ull << lane) - 1))] = r;
+        n += __popcll(mask);
     }
+    if (lane == 0) {
+        t.run[n] = C::BM;
+        t.n_runs = n;
+    }
+}
+
+// One bf16 step of the delta: T (xs) holds every row's own, so rows outside lo <= row < hi (tile
+// rows) are taken as zeros.  BY_ROW: and the products are added to the rows inside alone, so that
+// 0 x infinity and 0 x NaN reach no other row.
+template <class C, bool BY_ROW>
+__device__ __forceinline__ void mfma_run(f32x16_t (&acc)[C::TM][C::TN], const uint4 *__restrict__ xs,
+                                         const uint4 *__restrict__ ws, int lane, int wm0, int wn0,
+                                         int lo, int hi) {
+    Frags<C> f;
+    read_frags<C>(f, xs, ws, lane, wm0, wn0);
+#pragma unroll
+    for (int i = 0; i < C::TM; ++i) {
+        const int r0 = wm0 + 32 * i, row = r0 + (lane & 31);
+        if (hi <= r0 || lo >= r0 + 32) continue;  // uniform: a block without a row of the run
+#pragma unroll
+        for (int kk = 0; kk < 2; ++kk)
+            if (row < lo || row >= hi) f.a[kk][i] = __builtin_bit_cast(bf16x8_t, make_uint4(0, 0, 0, 0));
+#pragma unroll
+        for (int j = 0; j < C::TN; ++j) {
+            if constexpr (BY_ROW) {
+                f32x16_t p;
+#pragma unroll
+                for (int v = 0; v < 16; ++v) p[v] = 0.0f;
+#pragma unroll
+                for (int kk = 0; kk < 2; ++kk)
+                    p = __builtin_amdgcn_mfma_f32_32x32x16_bf16(f.a[kk][i], f.b[kk][j], p, 0, 0, 0);
+#pragma unroll
+                for (int v = 0; v < 16; ++v) {
+                    const int rv = r0 + (v / 4) * 8 + (lane >> 5) * 4 + (v % 4);
+                    acc[i][j][v] = rv >= lo && rv < hi ? acc[i][j][v] + p[v] : acc[i][j][v];
+                }
+            } else {
+#pragma unroll
+                for (int kk = 0; kk < 2; ++kk)
+                    acc[i][j] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(f.a[kk][i], f.b[kk][j], acc[i][j], 0, 0, 0);
+            }
+        }
+    }
+}
+
+// T = scale_a * t of the tile's rows, every row with its own adapter: rank chunk q (16 columns) in
+// slot q's x layout, as a pair of bf16 values per element -- k slots 0..15 the value rounded to
+// bf16, slots 16..31 the remainder (exact in fp32) rounded to bf16.  The pair carries scale * t to
+// about 16 significant bits, so the delta is not rounded to bf16 precision before it is added.
+template <class C>
+__device__ __forceinline__ void stage_t(uint4 *const (&xs)[4], const LoraEpilogue &ep,
+                                        const RowTable<C> &rows, int M, int tid) {
+    constexpr int kHalf = kBK / 2;
+    const int RM = ep.r_max;
+#pragma unroll 1
+    for (int q = 0; q * kHalf < RM; ++q) {
+        uint4 *const X = q == 0 ? xs[0] : q == 1 ? xs[1] : q == 2 ? xs[2] : xs[3];
+#pragma unroll 2
+        for (int c = tid; c < C::BM * 4; c += C::NT) {
+            const int row = c >> 2, lc = c & 3;
+            const int j = q * kHalf + (lc & 1) * 8;
+            uint4 v = make_uint4(0, 0, 0, 0);
+            if (rows.id[row] >= 0 && j < RM) {
+                // t[m, j .. j+7]: the shrink's chunk sums added in chunk order, four chunks'
+                // loads in flight at a time
+                const float *tp = ep.tpart + (size_t)rows.m[row] * RM + j;
+                const size_t cs = (size_t)M * RM;
+                float t[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
+#pragma unroll 1
+                for (int c0 = 0; c0 < ep.n_chunks; c0 += 4) {
+                    float4 p[4][2];
+#pragma unroll
+                    for (int k = 0; k < 4; ++k) {
+                        const bool in = c0 + k < ep.n_chunks;
+                        const float *src = tp + (size_t)(in ? c0 + k : 0) * cs;
+                        p[k][0] = in ? *reinterpret_cast<const float4 *>(src) : make_float4(0.f, 0.f, 0.f, 0.f);
+                        p[k][1] = in ? *reinterpret_cast<const float4 *>(src + 4) : make_float4(0.f, 0.f, 0.f, 0.f);
+                    }
+#pragma unroll
+                    for (int k = 0; k < 4; ++k) {
+                        if (c0 + k < ep.n_chunks) {
+                            t[0] += p[k][0].x; t[1] += p[k][0].y; t[2] += p[k][0].z; t[3] += p[k][0].w;
+                            t[4] += p[k][1].x; t[5] += p[k][1].y; t[6] += p[k][1].z; t[7] += p[k][1].w;
+                        }
+                    }
+                }
+                const float s = rows.lora[row];
+                float f[8];
+#pragma unroll
+                for (int e = 0; e < 8; ++e) f[e] = s * t[e];
+                if (lc >= 2) {  // the remainder after rounding to bf16
+#pragma unroll
+                    for (int e = 0; e < 8; ++e) f[e] -= __uint_as_float(f32_to_bf16_rne(f[e]) << 16);
+                }
+                v = make_uint4(pack_bf16x2(f[0], f[1]), pack_bf16x2(f[2], f[3]),
+                               pack_bf16x2(f[4], f[5]), pack_bf16x2(f[6], f[7]));
+            }
+            X[row * 4 + (lc ^ ((row >> 2) & 3))] = v;
+        }
+    }
+}
+
+// acc += T B_a for every run of one adapter among the tile's rows, in steps of 16 rank columns:
+// B_a's 16 rank rows twice (for T's two halves) in a W slot.  Four steps (the rank chunks of one,
+// two or four runs) share their two barriers and have their loads in flight together, a batch
+// ahead of their use.  Waves, and 32-row blocks, without a row of a run skip its step.
+//
+// A row outside a run still meets the run's B, times zero.  So that an adapter whose B holds an
+// infinity or a NaN spoils its own rows alone, such values are staged as zeros here, and a second
+// pass (ODD, only when there were any) stages them alone and adds their products by rows.  Returns
+// whether there were any.
+template <class C, bool ODD>
+__device__ __forceinline__ bool add_lora_steps(f32x16_t (&acc)[C::TM][C::TN], uint4 *const (&xs)[4],
+                                               uint4 *const (&ws)[4], const LoraEpilogue &ep,
+                                               const RowTable<C> &rows, int N, int n0, int tid,
+                                               int lane, int wm0, int wn0) {
+    constexpr int kHalf = kBK / 2;
+    const int RM = ep.r_max;
+    const int sh = RM <= 16 ? 0 : RM == 32 ? 1 : 2;  // 2^sh rank chunks per run
+    const int G = 4 >> sh;                            // runs per batch
+    auto slot = [](int u, uint4 *const (&v)[4]) { return u == 0 ? v[0] : u == 1 ? v[1] : u == 2 ? v[2] : v[3]; };
+    const int n_runs = rows.n_runs;
+    static_assert(kHalf * C::WCH <= C::NT, "one piece of B per thread and step");
+    const int br = tid / C::WCH, bc = tid % C::WCH, n = n0 + bc * 8;
+    uint4 bv[4];
+    // B_a's rank rows: all of a padded pool's stride (zero past the rank), the rank's in a
+    // compact one
+    auto load = [&](int R0) {
+#pragma unroll
+        for (int u = 0; u < 4; ++u) {
+            const int run = R0 + (u >> sh);
+            const int a = run < n_runs ? rows.id[rows.run[run]] : -1;
+            const int rank = (u & ((1 << sh) - 1)) * kHalf + br;
+            bv[u] = make_uint4(0, 0, 0, 0);
+            if (a >= 0 && br < kHalf && n < N) {
+                int ra = ep.roff ? min(max(ep.ranks[a], 0), RM) : ep.pstride;
+                const int brow0 = adapter_row0(ep.roff, ep.pool_rows, a, ep.pstride, ra);
+                if (rank < ra) bv[u] = ld16(ep.B + ((size_t)brow0 + rank) * N + n);
+            }
+        }
+    };
+    bool odd = false;
+    load(0);
+#pragma unroll 1
+    for (int R0 = 0; R0 < n_runs; R0 += G) {
+        if (ODD || R0 > 0) lds_barrier();  // every wave is done with the W slots
+        if (br < kHalf) {
+#pragma unroll
+            for (int u = 0; u < 4; ++u) {
+                uint32_t d[4] = {bv[u].x, bv[u].y, bv[u].z, bv[u].w};
+#pragma unroll
+                for (int e = 0; e < 4; ++e) {
+                    // the halves whose exponent is all ones
+                    const uint32_t m = ((d[e] & 0x7F80u) == 0x7F80u ? 0xFFFFu : 0u) |
+                                       ((d[e] & 0x7F800000u) == 0x7F800000u ? 0xFFFF0000u : 0u);
+                    odd |= m != 0;
+                    d[e] &= ODD ? m : ~m;
+                }
+                const uint4 v = make_uint4(d[0], d[1], d[2], d[3]);
+                ws[u][br * C::WCH + (bc ^ ((br & 3) << 2))] = v;
+                ws[u][(br + kHalf) * C::WCH + (bc ^ ((br & 3) << 2))] = v;
+            }
+        }
+        lds_barrier();
+        load(R0 + G);
+#pragma unroll 1
+        for (int u = 0; u < 4; ++u) {
+            const int run = R0 + (u >> sh);
+            if (run >= n_runs) break;
+            const int lo = rows.run[run], hi = rows.run[run + 1];
+            if (rows.id[lo] < 0 || hi <= wm0 || lo >= wm0 + C::WTM) continue;  // uniform in the wave
+            mfma_run<C, ODD>(acc, slot(u & ((1 << sh) - 1), xs), slot(u, ws), lane, wm0, wn0, lo, hi);
+        }
+    }
+    return __syncthreads_or(odd);
+}
+
+// The LoRA delta of one output tile (rows in segment order), after its K loop: acc += scale_a
+// t[rows, :] B_a[:, columns].  xs, ws: four slot pairs, free once every wave has passed the first
+// barrier here.  256 adapters on 4096 x 4096 x 11008 8-bit rows (17 runs per tile): 280 us per kernel,
+// 298 with T staged per batch, zeros outside its runs, and B loaded behind the barrier; 4096 x 4096
+// x 4096 bf16: 146 and 164; with 8 adapters (under two runs per tile) 230, and 131 bf16 with 4.
+template <class C>
+__device__ __forceinline__ void add_lora_runs(f32x16_t (&acc)[C::TM][C::TN], uint4 *const (&xs)[4],
+                                              uint4 *const (&ws)[4], const LoraEpilogue &ep,
+                                              RowTable<C> &rows, int M, int N, int n0, int tid,
+                                              int lane, int wm0, int wn0) {
+    lds_barrier();
+    if (tid < 64) fill_runs<C>(rows, lane);
+    stage_t<C>(xs, ep, rows, M, tid);
+    __syncthreads();
+    if (add_lora_steps<C, false>(acc, xs, ws, ep, rows, N, n0, tid, lane, wm0, wn0))
+        add_lora_steps<C, true>(acc, xs, ws, ep, rows, N, n0, tid, lane, wm0, wn0);
 }
 
 // Stores a wave's WTM x WTN block of the tile (first position row0 + wm0, first column c0) with

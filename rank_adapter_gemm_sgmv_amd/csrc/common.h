@@ -290,6 +290,7 @@ constexpr int kDecodeMaxRows = 128;
 constexpr int kDecodeGemmMaxRows = 256;
 bool decode_gemm_supported(int M, int K, int N);  // M <= kDecodeGemmMaxRows
 bool decode_fused_supported(int M, int K, int N);  // and M <= kDecodeMaxRows
+bool decode_act_supported(int M, int K, int N);  // with an epilogue: K in 8s (a padded pool)
 // Split partial floats of the decode GEMM at these sizes: the most any of its plans (with or
 // without adapter tiles) writes.
 size_t decode_gemm_partial_floats(int M, int K, int N, int r_max, int n_adapters);
@@ -418,6 +419,10 @@ hipError_t launch_rmsnorm(const NormArgs &a, hipStream_t s);
 
 // Records e as the error lora_last_hip_error() reports; LORA_ERR_HIP unless e is hipSuccess.
 lora_status_t hip_error_status(hipError_t e);
+
+// Workspace of lora_linear (act: what lora_linear_act may need too, lora_workspace_bytes()).
+size_t linear_workspace_bytes(int32_t M, int32_t d_in, int32_t d_out, int32_t r_max,
+                              int32_t n_adapters, bool act);
 
 // lora_linear on the workspace ws (validation, checked mode, launches).
 lora_status_t linear_on_workspace(const void *x, const void *W, const void *A, const void *B,

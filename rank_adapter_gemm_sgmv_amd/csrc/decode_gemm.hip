@@ -128,6 +128,57 @@ __device__ __forceinline__ void dec_x_src(S &src, const typename C::X *x, int M,
     }
 }
 
+// d_in an odd multiple of 8 (lora_linear_act): the K loop ends with the last whole 16-k step, and
+// the wave whose range ends at K adds the last 8 k here, from registers: as the first half
+// of one more step whose second half is zeros.  at(col) names W[K - 8, tile column col], whose k rows
+// are at(col).ld elements apart.
+struct TailCol {
+    const uint16_t *p;
+    size_t ld;
+};
+template <class C, class F>
+__device__ __forceinline__ void dec_tail(f32x16_t (&acc)[C::TM][C::TN], const uint16_t *x, int M, int K,
+                                         int m0, int lane, F at) {
+    const bool first = lane < 32;  // lanes holding the step's k 0 .. 7
+    bf16x8_t a[C::TM], b[C::TN];
+#pragma unroll
+    for (int i = 0; i < C::TM; ++i) {
+        const uint4 v = ld16(x + (size_t)min(m0 + 32 * i + (lane & 31), M - 1) * K + (K - 8));
+        a[i] = __builtin_bit_cast(bf16x8_t, first ? v : make_uint4(0, 0, 0, 0));
+    }
+#pragma unroll
+    for (int j = 0; j < C::TN; ++j) {
+        const TailCol c = at(32 * j + (lane & 31));
+        uint32_t w[4];
+#pragma unroll
+        for (int q = 0; q < 4; ++q)
+            w[q] = (uint32_t)c.p[2 * q * c.ld] | ((uint32_t)c.p[(2 * q + 1) * c.ld] << 16);
+        b[j] = __builtin_bit_cast(bf16x8_t, first ? make_uint4(w[0], w[1], w[2], w[3]) : make_uint4(0, 0, 0, 0));
+    }
+#pragma unroll
+    for (int i = 0; i < C::TM; ++i)
+#pragma unroll
+        for (int j = 0; j < C::TN; ++j)
+            acc[i][j] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(a[i], b[j], acc[i][j], 0, 0, 0);
+}
+
+// Column `col` of adapter tile lt at k (a padded pool; columns without an adapter read adapter 0's,
+// and columns past its rank rows its last: never used).
+template <int RM>
+__device__ __forceinline__ TailCol dec_adapter_col(const DecodeLora &lo, const uint16_t *A, int M,
+                                                   int K, int lt, int col, int k) {
+    constexpr int APT = AdapterTiles<RM>::APT;
+    const int sl = lt * APT + col / RM;
+    int a = 0;
+    if (lo.n_adapters <= M) {
+        a = sl < lo.n_adapters ? sl : 0;
+    } else if (sl < M) {
+        const int id = lo.ids[sl];
+        a = id >= 0 && id < lo.n_adapters ? id : 0;
+    }
+    return TailCol{A + ((size_t)a * K + k) * lo.pstride + min(col % RM, lo.pstride - 1), (size_t)lo.pstride};
+}
+
 // The reduction that follows a decode GEMM starts with dependent loads of the small tables (a
 // row's adapter, then its rank and scale, then B); left to it they come from HBM.  Touched at
 // the end of the GEMM's tiles, they are in every XCD's L2 by then.  One asm block issues the
@@ -254,6 +305,16 @@ __global__ __launch_bounds__(kThreads) void decode_gemm_kernel(
     const int kw1 = min(ks1, kw0 + per_wave);
     const int nst = (kw1 - kw0) / kBKW;
     dec_kloop<C>(acc, src, lds + wave * C::WAVE, kw0, nst, K, ldw, lane);
+    if ((K & 8) && kw1 == K && kw0 < K) {
+        if (tn < n_tn)
+            dec_tail<C>(acc, x, M, K, m0, lane, [&](int c) {
+                return TailCol{W + (size_t)(K - 8) * N + min(tn * kBN + c, N - 1), (size_t)N};
+            });
+        else
+            dec_tail<C>(acc, x, M, K, m0, lane, [&](int c) {
+                return dec_adapter_col<RM>(lo, A, M, K, tn - n_tn, c, K - 8);
+            });
+    }
     float *const mine = partial + ((size_t)split * n_tiles + tile) * C::TILE;
     if (n_lt > 0)  // a small-batch launch (adapter tiles)
         dec_tile_out<C, true>(acc, lds, lo, M, mine, tid, lane, wave);
@@ -970,14 +1031,14 @@ bool decode_fused_supported(int M, int K, int N) {
     return decode_gemm_supported(M, K, N) && M <= kDecodeMaxRows;
 }
 
-// The split plan itself and the 8-bit x (16-code chunks) need K in 16s only; the bf16 calls keep
-// decode_gemm_supported's 32.
-static bool decode_plan_ok(int M, int K, int N) {
-    return M >= 1 && M <= kDecodeGemmMaxRows && K % 16 == 0 && K >= 128 && N >= 8 && N % 4 == 0;
+// The kernels themselves take K in 8s (dec_tail), 8-bit x K in 16s; lora_linear keeps
+// decode_gemm_supported's 32 and its own tilings otherwise.
+bool decode_act_supported(int M, int K, int N) {
+    return M >= 1 && M <= kDecodeGemmMaxRows && K % 8 == 0 && K >= 128 && N >= 8 && N % 4 == 0;
 }
 
 bool decode_fp8_supported(int M, int K, int N) {
-    return decode_plan_ok(M, K, N) && M <= kFp8DecodeMaxRows && N % 8 == 0;
+    return decode_act_supported(M, K, N) && M <= kFp8DecodeMaxRows && K % 16 == 0 && N % 8 == 0;
 }
 
 size_t decode_fp8_partial_floats(int M, int K, int N, int r_max, int n_adapters) {
@@ -993,14 +1054,14 @@ size_t decode_fp8_partial_floats(int M, int K, int N, int r_max, int n_adapters)
 }
 
 size_t decode_gemm_partial_floats(int M, int K, int N, int r_max, int n_adapters) {
-    if (!decode_gemm_supported(M, K, N)) return 0;
+    if (!decode_act_supported(M, K, N)) return 0;
     // every plan a call of these sizes may run: without adapter tiles (batches of 129-256
     // rows, rank-compact pools, strides that are not a rank bucket, the fp8 base), and with
     // them (the fused small-batch path); the latter has more tiles but may have fewer splits
     const DecPlan p0 = dec_plan(M, K, N, 0);
     size_t f = (size_t)p0.ks * p0.n_tm * p0.n_tn * p0.bm * kBN;
     // (adapter slots r_max wide, the fp8 base's, or fused_tile_rank(r_max) wide, the bf16's)
-    if (rank_ok(r_max) && decode_fused_supported(M, K, N)) {
+    if (rank_ok(r_max) && M <= kDecodeMaxRows) {
         for (const int rs : {r_max, fused_tile_rank(r_max)}) {
             const DecPlan p = dec_plan(M, K, N, adapter_tiles(M, rs, n_adapters));
             const size_t fa = (size_t)p.ks * p.n_tm * (p.n_tn + p.n_lt) * p.bm * kBN;
@@ -1013,7 +1074,8 @@ size_t decode_gemm_partial_floats(int M, int K, int N, int r_max, int n_adapters
 hipError_t launch_decode_gemm(const uint16_t *x, const uint16_t *W, const uint16_t *A, int M,
                               int K, int N, const DecodeLora &lo, bool adapters, float *partial,
                               const SegBuild *build, hipStream_t s) {
-    if (!decode_gemm_supported(M, K, N) || partial == nullptr || !rank_ok(lo.r_max) ||
+    if (!decode_act_supported(M, K, N) || partial == nullptr || !rank_ok(lo.r_max) ||
+        ((K & 8) && lo.roff != nullptr) ||
         (adapters && (M > kDecodeMaxRows || A == nullptr || lo.ids == nullptr ||
                       (lo.roff == nullptr && (lo.pstride % 8 != 0 || lo.pstride < 8 ||
                                               lo.pstride > lo.r_max)))))
@@ -1146,7 +1208,7 @@ hipError_t launch_decode_gemm_fp8_lora_x8(const uint8_t *x8, const uint8_t *W8, 
 hipError_t launch_decode_reduce(const float *partial, int M, int K, int N, void *y, bool y_f32,
                                 const DecodeLora &lo, bool adapters, const Seg *seg,
                                 hipStream_t s, const Epilogue *epi) {
-    if (!decode_plan_ok(M, K, N) || partial == nullptr || !rank_ok(lo.r_max) ||
+    if (!decode_act_supported(M, K, N) || partial == nullptr || !rank_ok(lo.r_max) ||
         (!adapters && (lo.tpart == nullptr || lo.n_chunks < 1)))
         return hipErrorInvalidValue;
     const int n_lt = adapters ? adapter_tiles(M, lo.r_max, lo.n_adapters) : 0;

@@ -202,9 +202,10 @@ __device__ __forceinline__ void dec_kloop(f32x16_t (&acc)[C::TM][C::TN], const S
                  *const W3 = W2 + C::WSLOT;
     // W stage s holds k = KW(s) .. +15, x stage u holds k = KX(u) .. + KX - 1; stages past the
     // last reload the last one (an empty range loads k = 0), and an x stage that would run past K
-    // starts at K - KX instead, its later quarters then holding the wave's last steps
+    // starts at K - KX instead (K rounded down to whole steps), its later quarters then holding
+    // the wave's last steps
     constexpr int XS = C::KX / kBKW;  // steps per x stage: 4, or 8 with X8
-    const int kxl = nst > 0 ? min(kw0 + (nst - 1) / XS * C::KX, K - C::KX) : 0;
+    const int kxl = nst > 0 ? min(kw0 + (nst - 1) / XS * C::KX, (K & ~(kBKW - 1)) - C::KX) : 0;
 #define KW(S) (nst > 0 ? kw0 + min((S), nst - 1) * kBKW : 0)
 #define KX(U) (nst > 0 ? min(kw0 + (U) * C::KX, kxl) : 0)
     // Issue order: x(0), W(0), W(1), W(2); then step s issues x(s / XS + 1) when s % XS == 0,

@@ -125,7 +125,7 @@ __device__ __forceinline__ void fill_stage(uint4 *xs, uint4 *ws, const uint16_t 
 // O32: DMA sources as 32-bit byte offsets (x and W each below 4 GiB).
 // EPI: the epilogue of epilogue.h follows the delta, before the only rounding.
 template <class C, bool SEGROWS, bool LORA, bool YF32, bool O32, bool EPI>
-__global__ __launch_bounds__(C::NT) void gemm_big_kernel(const uint16_t *__restrict__ x,
+__global__ __launch_bounds__(C::NT, C::BM == 256 && C::BN == 128 ? 1 : 2) void gemm_big_kernel(const uint16_t *__restrict__ x,
                                                             const uint16_t *__restrict__ W,
                                                             int M, int K, int N,
                                                             void *y, int n_tm, int n_tn,
@@ -197,7 +197,7 @@ __global__ __launch_bounds__(C::NT) void gemm_big_kernel(const uint16_t *__restr
         issue_stage<C>(src, X0, W0, wave, 0, N);
         issue_stage<C>(src, X1, W1, wave, min(1, nmain - 1) * kBK, N);
         issue_stage<C>(src, X2, W2, wave, min(2, nmain - 1) * kBK, N);
-        if constexpr (LORA) fill_row<C>(rows, my_row, ep.ids, epi.row_scale, tid);
+        if constexpr (LORA) fill_row<C>(rows, my_row, ep, seg, epi.row_scale, row0, tid);
         wait_vm<2 * C::PER>();
         lds_barrier();
         read_frags<C>(fa, X0, W0, lane, wm0, wn0);
@@ -218,7 +218,7 @@ __global__ __launch_bounds__(C::NT) void gemm_big_kernel(const uint16_t *__restr
 #undef LORA_BIG_STEP
         wait_vm<0>();
     } else if constexpr (LORA) {
-        fill_row<C>(rows, my_row, ep.ids, epi.row_scale, tid);
+        fill_row<C>(rows, my_row, ep, seg, epi.row_scale, row0, tid);
     }
     // remaining steps (K not a multiple of 128), the last one possibly partial: through
     // registers into slot 0, zero beyond K
@@ -229,8 +229,10 @@ __global__ __launch_bounds__(C::NT) void gemm_big_kernel(const uint16_t *__restr
         mfma_stage<C>(acc, X0, W0, lane, wm0, wn0);
     }
 
-    if constexpr (LORA)
-        add_lora_runs<C>(acc, X0, W0, ep, seg, rows, M, N, row0, n0, tid, lane, wm0, wn0);
+    if constexpr (LORA) {
+        uint4 *const xs[4] = {X0, X1, X2, X3}, *const ws[4] = {W0, W1, W2, W3};
+        add_lora_runs<C>(acc, xs, ws, ep, rows, M, N, n0, tid, lane, wm0, wn0);
+    }
 
     // store: accumulator element v of a 32 x 32 block is row (v/4)*8 + (lane/32)*4 + v%4,
     // column lane%32.

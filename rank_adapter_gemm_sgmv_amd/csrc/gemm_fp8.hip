@@ -167,7 +167,7 @@ __device__ __forceinline__ void fill8(uint4 *slot, const uint8_t *__restrict__ s
 // WIDE: y is fp32 (see the top).  FUSED: whole K, rows in segment order, delta and epilogue; else slice blockIdx.y of K, rows in
 // their own order, into partial[blockIdx.y][M][N].
 template <class C, bool FUSED, bool WIDE, bool O32>
-__global__ __launch_bounds__(C::NT) void gemm_fp8_kernel(
+__global__ __launch_bounds__(C::NT, 2) void gemm_fp8_kernel(
     const uint8_t *__restrict__ x8, const uint8_t *__restrict__ W8,
     const float *__restrict__ w_scale, int M, int K, int N, int k_per_split,
     float *__restrict__ partial, void *y, int n_tm, int n_tn, Seg seg, LoraEpilogue ep,
@@ -226,7 +226,7 @@ __global__ __launch_bounds__(C::NT) void gemm_fp8_kernel(
     if (n > 0) {
         Frags8<C> fa, fb;
         issue8<C>(src, X0, W0, wave, k_lo);
-        if constexpr (FUSED) fill_row<C>(rows, my_row, ep.ids, epi.row_scale, tid);
+        if constexpr (FUSED) fill_row<C>(rows, my_row, ep, seg, epi.row_scale, row0, tid);
         wait_vm<0>();
         lds_barrier();
         issue8<C>(src, X1, W1, wave, k_lo + min(1, n - 1) * kK8);
@@ -249,7 +249,7 @@ __global__ __launch_bounds__(C::NT) void gemm_fp8_kernel(
 #undef LORA_FP8_STAGE
         wait_vm<0>();
     } else if constexpr (FUSED) {
-        fill_row<C>(rows, my_row, ep.ids, epi.row_scale, tid);
+        fill_row<C>(rows, my_row, ep, seg, epi.row_scale, row0, tid);
     }
     // the last stage, where it is partial: through registers, zero beyond k_hi
     if (const int k0 = k_lo + n * kK8; k0 < k_hi) {
@@ -278,7 +278,10 @@ __global__ __launch_bounds__(C::NT) void gemm_fp8_kernel(
     }
 
     if constexpr (FUSED) {
-        add_lora_runs<C>(acc, X0, W0, ep, seg, rows, M, N, row0, n0, tid, lane, wm0, wn0);
+        // (a stage's slot holds two of the bf16 steps')
+        uint4 *const xs[4] = {X0, X0 + C::XSLOT, X1, X1 + C::XSLOT};
+        uint4 *const ws[4] = {W0, W0 + C::WSLOT, W1, W1 + C::WSLOT};
+        add_lora_runs<C>(acc, xs, ws, ep, rows, M, N, n0, tid, lane, wm0, wn0);
         lds_barrier();
         // two waves per slot with eight waves, one with four
         constexpr int H = C::NW / 4;

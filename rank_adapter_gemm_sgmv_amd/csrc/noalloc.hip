@@ -45,7 +45,7 @@ lora_status_t lora_linear_noalloc(const void *x, const void *W, const void *A, c
                                   int32_t M, int32_t d_in, int32_t d_out, int32_t r_max,
                                   int32_t n_adapters, const lora_segments_t *segs, void *y,
                                   lora_dtype_t y_dtype, lora_mode_t mode, void *stream) {
-    const size_t need = lora_workspace_bytes(M, d_in, d_out, r_max, n_adapters);
+    const size_t need = lora::linear_workspace_bytes(M, d_in, d_out, r_max, n_adapters, false);
     if (need == 0)  // M = 0, or sizes lora_linear rejects: its status, nothing enqueued
         return lora::linear_on_workspace(x, W, A, B, scale, ranks, ids, M, d_in, d_out, r_max,
                                          n_adapters, segs, y, y_dtype, mode, nullptr, 0, stream);

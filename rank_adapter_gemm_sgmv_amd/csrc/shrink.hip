@@ -95,10 +95,12 @@ __device__ __forceinline__ void shrink_mfma_fill(f32x4_t (&acc)[C::NB], const XV
 //   kVarW    rows not RM wide but a multiple of 8: a rank-compact pool (roff names each
 //            adapter's first rank row; an adapter of rank r occupies round_up(r, 8) rows) or a
 //            padded pool whose stride pstride (< RM) is a multiple of 8;
-//   kFlat    a padded pool whose stride is not a multiple of 8: its k rows cannot be read in
-//            16-byte groups, so each chunk of A_a is read element by element (eight 2-byte
-//            loads in flight per lane) and scattered into the zeroed LDS rows.  A separate
-//            instantiation, so that the other layouts keep their registers and occupancy.
+//   kFlat    a padded pool whose stride is not a multiple of 8: its k rows do not start 16-byte
+//            aligned, but a chunk of A_a is one contiguous run that does, so it is read in
+//            16-byte pieces (eight in flight per lane) and scattered into the zeroed LDS rows
+//            element by element, or two at a time for an even stride (r_max 58, 35 rows x 464:
+//            9.8 us, and 18.0 with a 2-byte load per element).  A separate instantiation,
+//            so that the other layouts keep their registers and occupancy.
 enum { kPadRM = 0, kVarW = 1, kFlat = 2 };
 // Several pools of one x (lora_linear_multi): item it belongs to pool it / (tiles x chunks),
 // which reads A.p[pool] and writes partial.p[pool].
@@ -231,27 +233,39 @@ __global__ __launch_bounds__(64 * kWavesPerBlock) void shrink_mfma_kernel(
                     for (int v = lane; v < C::KS * C::LROW / 16; v += 64)
                         *reinterpret_cast<uint4 *>(wg + v * 16) = make_uint4(0, 0, 0, 0);
                     __builtin_amdgcn_s_waitcnt(0xC07F);  // lgkmcnt(0)
+                    // (the run starts 16-byte aligned and holds a multiple of 8 elements, as kb and
+                    // d_in are multiples of 8)
                     const int n_el = min(C::KS, k_hi - kb) * rs;
-                    const int step_k = 64 / rs, step_j = 64 - step_k * rs;
                     const uint16_t *src = Aa + (size_t)kb * rs;
+                    constexpr int NV = C::KS * RM / 8 / 64;  // 16-byte pieces per lane at most
+                    constexpr int U = NV < 8 ? NV : 8;       // loads in flight
+                    static_assert(NV % U == 0, "whole batches");
 #pragma unroll 1
-                    for (int e0 = 0; e0 < n_el; e0 += 64 * 8) {
-                        uint16_t h[8];
+                    for (int e0 = lane * 8; e0 < n_el; e0 += U * 512) {
+                        uint4 v[U];
 #pragma unroll
-                        for (int q = 0; q < 8; ++q) {
-                            const int e = e0 + lane + 64 * q;
-                            h[q] = e < n_el ? src[e] : (uint16_t)0;
-                        }
-                        // element e0 + lane + 64 q sits at k row kr, column j: one division per
-                        // batch, then steps of 64 elements
-                        int kr = (e0 + lane) / rs, j = (e0 + lane) - kr * rs;
+                        for (int u = 0; u < U; ++u)
+                            v[u] = e0 + u * 512 < n_el ? ld16(src + e0 + u * 512) : make_uint4(0, 0, 0, 0);
 #pragma unroll
-                        for (int q = 0; q < 8; ++q) {
-                            if (e0 + lane + 64 * q < n_el)
-                                *reinterpret_cast<uint16_t *>(wg + kr * C::LROW + j * 2) = h[q];
-                            j += step_j;
-                            kr += step_k;
-                            if (j >= rs) { j -= rs; ++kr; }
+                        for (int u = 0; u < U; ++u) {
+                            const int e = e0 + u * 512;
+                            if (e >= n_el) break;
+                            int kr = e / rs, j = e - kr * rs;
+                            const uint32_t w[4] = {v[u].x, v[u].y, v[u].z, v[u].w};
+                            if ((rs & 1) == 0) {  // pairs stay in one k row, 4-byte aligned
+#pragma unroll
+                                for (int q = 0; q < 4; ++q) {
+                                    *reinterpret_cast<uint32_t *>(wg + kr * C::LROW + j * 2) = w[q];
+                                    if ((j += 2) >= rs) { j -= rs; ++kr; }
+                                }
+                            } else {
+#pragma unroll
+                                for (int q = 0; q < 8; ++q) {
+                                    *reinterpret_cast<uint16_t *>(wg + kr * C::LROW + j * 2) =
+                                        (uint16_t)(q & 1 ? w[q / 2] >> 16 : w[q / 2]);
+                                    if (++j >= rs) { j -= rs; ++kr; }
+                                }
+                            }
                         }
                     }
                 }

@@ -29,7 +29,7 @@ class Call:
         out = torch.float32 if f32 else torch.bfloat16
         rk = torch.randint(1, r + 1, (n,), device="cuda", generator=g, dtype=torch.int32)
         self.ranks = rk if ranks == "mixed" else None
-        kept = torch.arange(r, device="cuda") < (rk[:, None] if ranks == "mixed" else r)
+        kept = torch.arange(r, device="cuda") < (rk[:, None] if ranks == "mixed" else torch.full_like(rk, r)[:, None])
         self.x = normal(M, K).bfloat16()
         self.W = normal(K, N, std=K ** -0.5).bfloat16()
         self.A = (normal(n, K, r, std=K ** -0.5) * kept[:, None, :]).bfloat16()
@@ -255,3 +255,36 @@ def test_graph_replays(M, K, mode):
         assert torch.equal(c.y, want), rep
         call()
         torch.cuda.synchronize()
+
+
+@pytest.mark.parametrize("M,K,N,n,r,mode", [
+    (9, 256, 264, 6, 16, DEC), (9, 256, 264, 40, 8, DEC), (150, 256, 264, 6, 16, DEC),
+    (300, 16384, 264, 6, 16, DEC), (300, 1032, 264, 6, 16, DEC), (800, 256, 264, 6, 16, PRE),
+    (800, 256, 264, 6, 64, PRE), (4100, 128, 3080, 40, 32, PRE), (3000, 264, 2056, 9, 8, PRE)])
+def test_an_adapter_with_nan_spoils_its_own_rows_alone(M, K, N, n, r, mode):
+    log(f"NaN adapter M={M} K={K} n={n} r={r}")
+    ids = np.arange(M) * 7 % (n + 1) - 1
+    c = Call(37, M, K, N, n, r, act="silu", bias=True, mode=mode, ids=ids, ranks=None)
+    base = c.run().clone()
+    c.B[1, 0, 3] = float("nan")
+    c.B[2, r - 1, N - 1] = float("inf")
+    c.A[3, K - 1, 0] = float("nan")
+    got = c.run()
+    hit = torch.zeros(M, N, dtype=torch.bool, device="cuda")
+    hit[c.ids == 1, 3] = True
+    hit[c.ids == 2, N - 1] = True
+    hit[c.ids == 3] = True
+    assert torch.equal(got[~hit], base[~hit])
+    assert torch.isnan(got[c.ids == 1, 3]).all() and torch.isnan(got[c.ids == 3]).all()
+    # (silu of minus infinity is NaN by its formula, of plus infinity infinity)
+    assert not torch.isfinite(got[c.ids == 2, N - 1]).any()
+
+
+@pytest.mark.parametrize("M,K,N,n,r", [(800, 256, 520, 700, 16), (1300, 520, 264, 121, 3), (4100, 128, 3080, 512, 8),
+                                       (4100, 128, 3080, 90, 64), (1024, 264, 1032, 64, 32), (777, 136, 264, 1, 40)])
+def test_prefill_with_many_adapters(M, K, N, n, r):
+    """Tiles of many short runs, each rank bucket."""
+    log(f"prefill M={M} n={n} r={r}")
+    for f32 in (False, True):
+        c = Call(41, M, K, N, n, r, act="gelu", residual=True, f32=f32, mode=PRE)
+        c.check(c.run(), f"M={M} n={n} r={r}")

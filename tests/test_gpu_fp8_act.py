@@ -47,7 +47,7 @@ class Call:
         out = torch.float32 if f32 else torch.bfloat16
         rk = torch.randint(1, r + 1, (n,), device="cuda", generator=g, dtype=torch.int32)
         self.ranks = rk if ranks == "mixed" else None
-        kept = torch.arange(r, device="cuda") < (rk[:, None] if ranks == "mixed" else r)
+        kept = torch.arange(r, device="cuda") < (rk[:, None] if ranks == "mixed" else torch.full_like(rk, r)[:, None])
         if codes == "normal":
             self.x8, self.x_scale = quantised(normal(M, K))
             self.W8, self.w_scale = quantised(normal(N, K, std=K ** -0.5))
@@ -283,3 +283,30 @@ def test_norm_gate_up_down_together():
         up.check(up.y, "up")
         gate.check(gate.y, "gate")
         down.check(y, "down")
+
+
+@pytest.mark.parametrize("M,K,N", BATCHES)
+def test_an_adapter_with_nan_spoils_its_own_rows_alone(M, K, N):
+    n, r = 6, 16
+    c = Call(37, M, K, N, n, r, act="silu", bias=True, ids=np.arange(M) * 5 % (n + 1) - 1, ranks=None)
+    base = c.run().clone()
+    c.B[1, 0, 3] = float("nan")
+    c.B[2, r - 1, N - 1] = float("inf")
+    c.A[3, K - 1, 0] = float("nan")
+    got = c.run()
+    hit = torch.zeros(M, N, dtype=torch.bool, device="cuda")
+    hit[c.ids == 1, 3] = True
+    hit[c.ids == 2, N - 1] = True
+    hit[c.ids == 3] = True
+    assert torch.equal(got[~hit], base[~hit])
+    assert torch.isnan(got[c.ids == 1, 3]).all() and torch.isnan(got[c.ids == 3]).all()
+    assert not torch.isfinite(got[c.ids == 2, N - 1]).any()
+
+
+@pytest.mark.parametrize("M,K,N,n,r", [(900, 304, 8200, 700, 16), (4100, 144, 3080, 512, 3),
+                                       (4100, 144, 3080, 90, 64), (2000, 256, 6408, 64, 32)])
+def test_tiles_of_many_short_runs(M, K, N, n, r):
+    log(f"linear_fp8 M={M} n={n} r={r}")
+    for f32 in (False, True):
+        c = Call(41, M, K, N, n, r, act="gelu", residual=True, f32=f32)
+        c.check(c.run(), f"M={M} n={n} r={r}")
