@@ -173,7 +173,8 @@ __device__ __forceinline__ void fill_row(RowTable<C> &t, int m, const LoraEpilog
     }
 }
 
-// The runs of the table's rows, by one wave (which must see the whole table).
+// The runs of the table's rows, by one wave behind the barrier that completes the table (the K loop's
+// barriers then lie before their use).
 template <class C>
 __device__ __forceinline__ void fill_runs(RowTable<C> &t, int lane) {
     int n = 0;
@@ -299,8 +300,8 @@ __device__ __forceinline__ void stage_t(uint4 *const (&xs)[4], const LoraEpilogu
 template <class C, bool ODD>
 __device__ __forceinline__ bool add_lora_steps(f32x16_t (&acc)[C::TM][C::TN], uint4 *const (&xs)[4],
                                                uint4 *const (&ws)[4], const LoraEpilogue &ep,
-                                               const RowTable<C> &rows, int N, int n0, int tid,
-                                               int lane, int wm0, int wn0) {
+                                               const RowTable<C> &rows, int M, int N, int n0,
+                                               int tid, int lane, int wm0, int wn0) {
     constexpr int kHalf = kBK / 2;
     const int RM = ep.r_max;
     const int sh = RM <= 16 ? 0 : RM == 32 ? 1 : 2;  // 2^sh rank chunks per run
@@ -328,6 +329,7 @@ __device__ __forceinline__ bool add_lora_steps(f32x16_t (&acc)[C::TM][C::TN], ui
     };
     bool odd = false;
     load(0);
+    if constexpr (!ODD) stage_t<C>(xs, ep, rows, M, tid);  // (the first batch's barrier covers T too)
 #pragma unroll 1
     for (int R0 = 0; R0 < n_runs; R0 += G) {
         if (ODD || R0 > 0) lds_barrier();  // every wave is done with the W slots
@@ -370,14 +372,11 @@ __device__ __forceinline__ bool add_lora_steps(f32x16_t (&acc)[C::TM][C::TN], ui
 template <class C>
 __device__ __forceinline__ void add_lora_runs(f32x16_t (&acc)[C::TM][C::TN], uint4 *const (&xs)[4],
                                               uint4 *const (&ws)[4], const LoraEpilogue &ep,
-                                              RowTable<C> &rows, int M, int N, int n0, int tid,
+                                              const RowTable<C> &rows, int M, int N, int n0, int tid,
                                               int lane, int wm0, int wn0) {
     lds_barrier();
-    if (tid < 64) fill_runs<C>(rows, lane);
-    stage_t<C>(xs, ep, rows, M, tid);
-    __syncthreads();
-    if (add_lora_steps<C, false>(acc, xs, ws, ep, rows, N, n0, tid, lane, wm0, wn0))
-        add_lora_steps<C, true>(acc, xs, ws, ep, rows, N, n0, tid, lane, wm0, wn0);
+    if (add_lora_steps<C, false>(acc, xs, ws, ep, rows, M, N, n0, tid, lane, wm0, wn0))
+        add_lora_steps<C, true>(acc, xs, ws, ep, rows, M, N, n0, tid, lane, wm0, wn0);
 }
 
 // Stores a wave's WTM x WTN block of the tile (first position row0 + wm0, first column c0) with

@@ -202,6 +202,7 @@ __global__ __launch_bounds__(C::NT, C::BM == 256 && C::BN == 128 ? 1 : 2) void g
         lds_barrier();
         read_frags<C>(fa, X0, W0, lane, wm0, wn0);
         issue_stage<C>(src, X3, W3, wave, min(3, nmain - 1) * kBK, N);
+        if (LORA && wave == C::NW - 1) fill_runs<C>(rows, lane);
 #define LORA_BIG_STEP(SS, FC, FN, XN, WN, XF, WF)                                 \
         wait_vm<2 * C::PER>();                                                   \
         lds_barrier();                                                           \
@@ -219,6 +220,8 @@ __global__ __launch_bounds__(C::NT, C::BM == 256 && C::BN == 128 ? 1 : 2) void g
         wait_vm<0>();
     } else if constexpr (LORA) {
         fill_row<C>(rows, my_row, ep, seg, epi.row_scale, row0, tid);
+        lds_barrier();
+        if (wave == C::NW - 1) fill_runs<C>(rows, lane);
     }
     // remaining steps (K not a multiple of 128), the last one possibly partial: through
     // registers into slot 0, zero beyond K

@@ -230,6 +230,7 @@ __global__ __launch_bounds__(C::NT, 2) void gemm_fp8_kernel(
         wait_vm<0>();
         lds_barrier();
         issue8<C>(src, X1, W1, wave, k_lo + min(1, n - 1) * kK8);
+        if (FUSED && wave == C::NW - 1) fill_runs<C>(rows, lane);
         read_frags8<C>(fa, X0, W0, 0, lane, wm0, wn0);
 #define LORA_FP8_STAGE(XP, WP, XQ, WQ)                                           \
         read_frags8<C>(fb, XP, WP, 1, lane, wm0, wn0);                           \
@@ -254,6 +255,7 @@ __global__ __launch_bounds__(C::NT, 2) void gemm_fp8_kernel(
     // the last stage, where it is partial: through registers, zero beyond k_hi
     if (const int k0 = k_lo + n * kK8; k0 < k_hi) {
         lds_barrier();
+        if (FUSED && n == 0 && wave == C::NW - 1) fill_runs<C>(rows, lane);
         fill8<C::BM, C::NT>(X0, x8, M, K, row0, k0, k_hi, FUSED ? seg.perm : nullptr, tid);
         fill8<C::BN, C::NT>(W0, W8, N, K, n0, k0, k_hi, nullptr, tid);
         __syncthreads();
