@@ -338,6 +338,12 @@ hipError_t launch_fp8_cfg(const Fp8Gemm &g, const Fp8Plan &p, void *y, bool y_f3
 // A slice of K is a multiple of two stages.
 constexpr int kMinK = 2 * kK8;
 
+// Up to 256 small tiles split K, into as many slices as two workgroups per CU hold at once: a
+// tile per CU leaves its loads and its epilogue without a neighbour to fill their waits.  Whole
+// call at d_out 4096, rank 64, fp32 residual, one slice -> split: 1024 x 512 52.5 -> 42.3 us,
+// 1024 x 4096 76.4 -> 65.3, 1024 x 11008 140 -> 115; 768 x 11008, two slices or (a second, short
+// round) three: 97 or 118.  Above 256 the slices cost more than they bring: 1280 x 4096 80 ->
+// 88 us, 1536 x 11008 144 -> 164 with three slices.
 Fp8Plan fp8_plan(int M, int K, int N, bool y_f32) {
     Fp8Plan p{};
     p.ks = 1;
@@ -345,9 +351,9 @@ Fp8Plan fp8_plan(int M, int K, int N, bool y_f32) {
     const long t256 = (long)((M + 255) / 256) * ((N + 255) / 256);
     const long t128 = (long)((M + 127) / 128) * ((N + 127) / 128);
     p.big = t256 >= 192 && !y_f32;
-    if (t256 < 192 && t128 < 256) {
+    if (t256 < 192 && t128 <= 256) {
         const int steps = (K + kMinK - 1) / kMinK;
-        int ks = (int)((512 + t128 - 1) / t128);           // two workgroups per CU
+        int ks = (int)(512 / t128);  // two workgroups per CU, one round
         if (ks > 16) ks = 16;
         if (ks > steps) ks = steps;
         const int per = (steps + ks - 1) / ks;
