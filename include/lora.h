@@ -276,8 +276,9 @@ typedef struct {
 
 /* lora_linear with an epilogue: z = x W + (x A_i) B_i scale_i (rows with id -1: x W), then epi
  * as above.  epi: a HOST struct read during the call; NULL gives lora_linear's result.  The
- * other arguments, the workspace (lora_workspace_bytes()), modes and errors are lora_linear's;
- * also LORA_ERR_VALUE for an unknown activation and LORA_ERR_ALIGN for the epilogue's operands. */
+ * other arguments, the workspace (lora_workspace_bytes()), modes and errors are lora_linear's
+ * (with epi, AUTO also weighs d_in, d_out and the adapters a tile meets against M); also
+ * LORA_ERR_VALUE for an unknown activation and LORA_ERR_ALIGN for the epilogue's operands. */
 lora_status_t lora_linear_act(const void *x, const void *W, const void *A, const void *B,
                               const float *scale, const int32_t *ranks, const int32_t *ids,
                               int32_t M, int32_t d_in, int32_t d_out, int32_t r_max,

@@ -357,11 +357,20 @@ hipError_t run_linear(const void *x, const void *W, const void *A, const void *B
     const bool flat = epi && !dec && gemm_splits_k(M, d_in, d_out);
     const bool splits = flat || (epi && sk_plan(M, d_in, d_out).use);
     if (epi && !splits && !dec) prefill = true;
-    // AUTO batches whose 128 x 128 tiles would leave most CUs idle split K instead (decode and
-    // prefill sequence: 22 tiles 32.9 and 43.7 us, 28 tiles 38.9 and 52.9, 64 tiles 47.1 and 61.8,
-    // 52.1 and 55.6; 96 tiles 39.4 and 28.9, 112 tiles 47.0 and 37.1)
-    if (prefill && mode == LORA_MODE_AUTO && splits && (long)((M + 127) / 128) * ((d_out + 127) / 128) <= 64)
-        prefill = false;
+    // AUTO with an epilogue weighs the sequences where both exist.  Prefill has one workgroup per
+    // 128 x 128 tile go through all of K and then through the tile's adapter runs; split K fills
+    // the chip but writes and adds partial sums in proportion to the tiles (in plain slices, where
+    // stream-K does not apply, it also reads its operands once per small tile: a longer K then
+    // no longer speaks for it).  Microseconds for split K and prefill, d_out 4096: 300 x 1024 rank
+    // 16 of 4 adapters 33.6 and 26.6, 300 x 11008 68.8 and 91.1, 1024 x 4096 71.7 and 55.8,
+    // 1024 x 11008 118 and 116; rank 64 of 256 adapters 300 x 1024 46.7 and 278, 1024 x 1024 72.9
+    // and 154; in slices, d_out 2760, rank 16 of 4, 1300 x 11008 213 and 132.
+    if (mode == LORA_MODE_AUTO && splits && !dec) {
+        const long tiles = (long)((M + 127) / 128) * ((d_out + 127) / 128);
+        const long runs = 128L * (n_adapters < M ? n_adapters : M) / (M > 128 ? M : 128);
+        const long k = flat && d_in > 4096 ? 4096 : d_in;
+        prefill = k + 12L * r_max * runs < 42L * (tiles < 256 ? tiles : 256);
+    }
     char *p = static_cast<char *>(ws);
     lora_segments_t own = carve_segments(p, M, n_adapters);
     float *t = reinterpret_cast<float *>(p); p += t_bytes(M, r_max);

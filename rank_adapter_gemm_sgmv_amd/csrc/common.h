@@ -212,6 +212,7 @@ hipError_t launch_gemm(const uint16_t *x, const uint16_t *W, int M, int K, int N
 // Large-batch MFMA GEMM (csrc/gemm_big.hip): with lora != nullptr, rows in segment order and
 // the LoRA delta of each adapter run added before the only store (prefill); otherwise plain
 // y = x W in natural row order.
+bool wide_tiles(int M, int N);  // 256 x 256 tiles (else 128 x 128)
 hipError_t launch_gemm_big(const uint16_t *x, const uint16_t *W, int M, int K, int N, void *y,
                            bool y_f32, Seg seg, const LoraEpilogue *lora, hipStream_t s,
                            const Epilogue *epi = nullptr);

@@ -7,7 +7,7 @@
 // delta is small next to x W).
 //
 // gfx950 design
-//  * Tile BM x BN (256 x 256, 256 x 128 or 128 x 128).  256 x 256 tiles use eight waves in a
+//  * Tile BM x BN (256 x 256 or 128 x 128).  256 x 256 tiles use eight waves in a
 //    2 x 4 grid (each owns 128 x 64 of the output: 128 accumulator registers, so two waves
 //    share a SIMD and one issues MFMAs while the other waits on LDS or the barrier); the
 //    smaller tiles use four waves in a 2 x 2 grid.  Accumulators are 32 x 32
@@ -617,22 +617,29 @@ hipError_t launch_big_cfg(const uint16_t *x, const uint16_t *W, int M, int K, in
 
 }  // namespace
 
+// 256 x 256 tiles (one workgroup per CU) or 128 x 128 (two): the large ones where they fill most
+// of a round of 256 CUs, or several rounds; the small ones below that and where a short second
+// round would follow.  d_in 4096, rank 16, bias and residual, large and small tiles: 208 of the
+// large ones 119 and 151 us, 256 of them 135 and 163; 288 of them 219 and 194.  fp8 (lora_linear_fp8)
+// 75.6 and 84.6, 82.8 and 92.6; 138 and 122.  Tiles of 256 x 128, one per CU, lost everywhere: 192 of
+// them 225 us for 124 with small tiles, 256 122 for 92, 320 218 for 121.
+bool wide_tiles(int M, int N) {
+    const long t = (long)((M + 255) / 256) * ((N + 255) / 256);
+    return t >= 192 && (t <= 256 || t > 304);
+}
+
 // Large-batch GEMM: prefill (segment-ordered rows, LoRA epilogue) when lora != nullptr,
 // else plain y = x W in natural row order.  Needs N >= 8 (N % 8 == 0) and M >= 1.
 hipError_t launch_gemm_big(const uint16_t *x, const uint16_t *W, int M, int K, int N, void *y,
                            bool y_f32, Seg seg, const LoraEpilogue *lora, hipStream_t s,
                            const Epilogue *epi) {
     if (epi && !lora) return hipErrorInvalidValue;
-    const long t256 = (long)((M + 255) / 256) * ((N + 255) / 256);
+    const bool wide = wide_tiles(M, N);
     if (lora) {
-        if (t256 >= 192) return launch_big_cfg<Big<256, 256, 2, 4>, true, true>(x, W, M, K, N, y, y_f32, seg, lora, s, epi);
-        if ((long)((M + 255) / 256) * ((N + 127) / 128) >= 192)
-            return launch_big_cfg<Big<256, 128>, true, true>(x, W, M, K, N, y, y_f32, seg, lora, s, epi);
+        if (wide) return launch_big_cfg<Big<256, 256, 2, 4>, true, true>(x, W, M, K, N, y, y_f32, seg, lora, s, epi);
         return launch_big_cfg<Big<128, 128>, true, true>(x, W, M, K, N, y, y_f32, seg, lora, s, epi);
     }
-    if (t256 >= 192) return launch_big_cfg<Big<256, 256, 2, 4>, false, false>(x, W, M, K, N, y, y_f32, seg, nullptr, s, nullptr);
-    if ((long)((M + 255) / 256) * ((N + 127) / 128) >= 192)
-        return launch_big_cfg<Big<256, 128>, false, false>(x, W, M, K, N, y, y_f32, seg, nullptr, s, nullptr);
+    if (wide) return launch_big_cfg<Big<256, 256, 2, 4>, false, false>(x, W, M, K, N, y, y_f32, seg, nullptr, s, nullptr);
     return launch_big_cfg<Big<128, 128>, false, false>(x, W, M, K, N, y, y_f32, seg, nullptr, s, nullptr);
 }
 

@@ -348,10 +348,9 @@ Fp8Plan fp8_plan(int M, int K, int N, bool y_f32) {
     Fp8Plan p{};
     p.ks = 1;
     p.k_per_split = K;
-    const long t256 = (long)((M + 255) / 256) * ((N + 255) / 256);
     const long t128 = (long)((M + 127) / 128) * ((N + 127) / 128);
-    p.big = t256 >= 192 && !y_f32;
-    if (t256 < 192 && t128 <= 256) {
+    p.big = wide_tiles(M, N) && !y_f32;
+    if (t128 <= 256) {
         const int steps = (K + kMinK - 1) / kMinK;
         int ks = (int)(512 / t128);  // two workgroups per CU, one round
         if (ks > 16) ks = 16;

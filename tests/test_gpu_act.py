@@ -82,11 +82,16 @@ SEQUENCES = [
     (300, 4128, 1032, 50, 64, DEC), (700, 2088, 136, 5, 8, AUTO),
     # too short to split
     (7, 8, 8, 2, 1, DEC), (3, 200, 72, 5, 3, AUTO), (300, 64, 520, 4, 16, DEC),
-    # prefill: 128 x 128, 256 x 128 and 256 x 256 tiles, ragged rows and columns, odd d_in
+    # prefill: 128 x 128 and 256 x 256 tiles, ragged rows and columns, odd d_in
     (768, 512, 520, 8, 16, AUTO), (1500, 1032, 264, 30, 64, AUTO), (3000, 264, 2056, 5, 8, AUTO),
     (4100, 520, 3080, 3, 16, AUTO), (12, 96, 40, 4, 16, PRE), (2000, 256, 6408, 700, 40, PRE),
     # decode asked for where only a large-tile launch runs
     (1300, 4096, 4104, 4, 16, DEC), (900, 256, 8200, 4, 16, DEC),
+    # AUTO's choice between splitting K and whole tiles, both sides of it below and above 768 rows
+    (300, 512, 4096, 4, 16, AUTO), (300, 512, 4096, 300, 64, AUTO), (768, 4096, 1024, 4, 16, AUTO),
+    (1024, 256, 2056, 1024, 40, AUTO), (1300, 1032, 1032, 700, 64, AUTO), (1300, 4104, 2056, 3, 8, AUTO),
+    # a few more tiles than one round of 256 x 256 ones
+    (4500, 128, 4096, 9, 16, PRE),
 ]
 
 

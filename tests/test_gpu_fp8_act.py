@@ -112,6 +112,7 @@ SHAPES = [
     (129, 512, 512, 7, 16), (200, 1040, 520, 40, 32), (256, 4096, 264, 256, 64), (131, 176, 1096, 300, 5),
     (257, 4096, 2056, 50, 64), (509, 11008, 1024, 100, 24), (300, 4128, 1032, 50, 33), (300, 64, 520, 4, 16),
     (700, 2096, 136, 5, 8), (1000, 2048, 520, 600, 16), (1500, 1040, 264, 30, 64), (900, 304, 8200, 4, 16),
+    (1024, 512, 4096, 70, 64), (768, 1040, 4096, 4, 16), (4500, 144, 4096, 9, 16),
     (3000, 272, 2056, 5, 8), (4100, 528, 3080, 3, 16), (4100, 1024, 3080, 700, 40), (2000, 256, 6408, 9, 16),
 ]
 
