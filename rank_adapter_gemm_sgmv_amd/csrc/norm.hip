@@ -52,18 +52,21 @@ __device__ __forceinline__ void norm_h8(float h[8], uint4 x, uint4 res, bool has
     }
 }
 
-// Row statistics -> factors of the outputs: y = h w r, code = h w f, scale s.
+// Row statistics -> factors of the outputs: y = (h r) w, code = ((h q) w) f, scale s.
 struct NormFactors {
-    float r, f, s;
+    float r, q, f, s;
 };
-__device__ __forceinline__ NormFactors norm_factors(float r, float top) {
+// top: max|h w|, or (nw: that overflowed) max|n| itself
+__device__ __forceinline__ NormFactors norm_factors(float r, float top, bool nw) {
     NormFactors o;
+    const float q = nw ? 1.0f : r, mx = q * top;
     o.r = r;
-    o.s = fmaxf(r * top, kFloor8) / kTop8;
+    o.q = nw ? r : 1.0f;
+    o.s = fmaxf(mx, kFloor8) / kTop8;
     // (below the floor the codes are n / s with the floor's s; above it r cancels)
-    o.f = r * top > kFloor8 ? kTop8 / top : r / o.s;
-    // a row with an infinity or a NaN has no scale: all its codes are NaN
-    if (!(r * top < __builtin_inff()) || r != r) o.s = o.f = __builtin_nanf("");
+    o.f = mx > kFloor8 ? kTop8 / top : q / o.s;
+    // a row with an infinity (r = 0) or a NaN has no scale: all its codes are NaN
+    if (!(mx < __builtin_inff()) || !(r > 0.0f)) o.s = o.f = __builtin_nanf("");
     return o;
 }
 
@@ -72,22 +75,26 @@ __device__ __forceinline__ NormFactors norm_factors(float r, float top) {
 // outputs at d 4096, plain stores -> these: 10.7 -> 8.3 us at 1024 rows, 54.0 -> 51.8 us at
 // 8192 (5.8 TB/s; a large copy reaches 5.5), the same at 64 rows and below.
 typedef uint32_t u32x2_t __attribute__((ext_vector_type(2)));
-__device__ __forceinline__ void st_bf16x8(uint16_t *p, const float f[8], float k) {
-    st16_nt(p, make_uint4(cvt_bf16x2(f[0] * k, f[1] * k), cvt_bf16x2(f[2] * k, f[3] * k),
-                          cvt_bf16x2(f[4] * k, f[5] * k), cvt_bf16x2(f[6] * k, f[7] * k)));
+__device__ __forceinline__ void st_bf16x8(uint16_t *p, const float f[8]) {
+    st16_nt(p, make_uint4(cvt_bf16x2(f[0], f[1]), cvt_bf16x2(f[2], f[3]), cvt_bf16x2(f[4], f[5]),
+                          cvt_bf16x2(f[6], f[7])));
 }
 
 __device__ __forceinline__ void norm_store8(const NormArgs &a, size_t at, const float h[8],
                                             uint4 w, const NormFactors &nf) {
-    if (a.sum) st_bf16x8(a.sum + at, h, 1.0f);
-    float g[8];
+    if (a.sum) st_bf16x8(a.sum + at, h);
+    float g[8], n[8];
     unpack8(w, g);
+    if (a.y) {
+        // |h r| is at most sqrt(d), so that no product overflows where n does not
 #pragma unroll
-    for (int e = 0; e < 8; ++e) g[e] *= h[e];
-    if (a.y) st_bf16x8(a.y + at, g, nf.r);
+        for (int e = 0; e < 8; ++e) n[e] = h[e] * nf.r * g[e];
+        st_bf16x8(a.y + at, n);
+    }
     if (a.y8) {
-        const u32x2_t v = {pack_e4m3x4(g[0] * nf.f, g[1] * nf.f, g[2] * nf.f, g[3] * nf.f),
-                           pack_e4m3x4(g[4] * nf.f, g[5] * nf.f, g[6] * nf.f, g[7] * nf.f)};
+#pragma unroll
+        for (int e = 0; e < 8; ++e) n[e] = h[e] * nf.q * g[e] * nf.f;
+        const u32x2_t v = {pack_e4m3x4(n[0], n[1], n[2], n[3]), pack_e4m3x4(n[4], n[5], n[6], n[7])};
         __builtin_nontemporal_store(v, reinterpret_cast<u32x2_t *>(a.y8 + at));
     }
 }
@@ -119,7 +126,7 @@ template <int WPR, int VPL>
 __global__ __launch_bounds__(WPR > 4 ? WPR * 64 : 256) void rmsnorm_kernel(NormArgs a) {
     constexpr int NW = WPR > 4 ? WPR : 4;  // waves per block
     constexpr int RPB = NW / WPR;          // rows per block
-    __shared__ float red[NW][2], red2[NW][2];
+    __shared__ float red[NW][2], red2[NW][2], red3[NW][2];
     const int wave = threadIdx.x >> 6;
     const int row = blockIdx.x * RPB + wave / WPR;
     const bool live = row < a.M;
@@ -155,11 +162,12 @@ __global__ __launch_bounds__(WPR > 4 ? WPR * 64 : 256) void rmsnorm_kernel(NormA
         }
     }
     row_reduce<WPR>(ss, top, red, wave);
-    float r = 1.0f / sqrtf(ss / (float)a.d + a.eps);
-    if (!(ss < __builtin_inff())) {
-        // some square overflowed: once more on h 2^-80 (eps is far below what remains).  The
-        // branch is uniform in the row, so in the wave (WPR == 1) or the block (its barrier).
-        static_assert(WPR == 1 || RPB == 1, "a block with barriers holds one row");
+    const float ms = ss / (float)a.d + a.eps;
+    float r = 1.0f / sqrtf(ms);
+    // Rows at the ends of the range go on: their branches are uniform in the row, so in the wave
+    // (WPR == 1) or the block (its barriers).
+    static_assert(WPR == 1 || RPB == 1, "a block with barriers holds one row");
+    if (!(ms < __builtin_inff())) {  // some square overflowed: once more on h 2^-80
         float s2 = 0.0f, t2 = 0.0f;
 #pragma unroll
         for (int i = 0; i < VPL; ++i)
@@ -167,10 +175,24 @@ __global__ __launch_bounds__(WPR > 4 ? WPR * 64 : 256) void rmsnorm_kernel(NormA
 #pragma unroll
                 for (int e = 0; e < 8; ++e) s2 = fmaf(h[i][e] * kShrink, h[i][e] * kShrink, s2);
         row_reduce<WPR>(s2, t2, red2, wave);
-        r = kShrink / sqrtf(s2 / (float)a.d);
+        r = kShrink / sqrtf(s2 / (float)a.d + a.eps * kShrink * kShrink);
+    }
+    const bool nw = !(top < __builtin_inff());
+    if (nw) {  // some h w did: max|n| instead
+        float s3 = 0.0f;
+        top = 0.0f;
+#pragma unroll
+        for (int i = 0; i < VPL; ++i)
+            if (c0 + i * (WPR * 512) < a.d) {
+                float g[8];
+                unpack8(wv[i], g);
+#pragma unroll
+                for (int e = 0; e < 8; ++e) top = fmaxf(top, fabsf(h[i][e] * r * g[e]));
+            }
+        row_reduce<WPR>(s3, top, red3, wave);
     }
     if (!live) return;
-    const NormFactors nf = norm_factors(r, top);
+    const NormFactors nf = norm_factors(r, top, nw);
 #pragma unroll
     for (int i = 0; i < VPL; ++i) {
         const int c = c0 + i * (WPR * 512);
@@ -182,14 +204,14 @@ __global__ __launch_bounds__(WPR > 4 ? WPR * 64 : 256) void rmsnorm_kernel(NormA
 // Rows too long for registers: one block of 16 waves per row, which it reads twice (the second
 // time mostly from L2).
 __global__ __launch_bounds__(1024) void rmsnorm_long_kernel(NormArgs a) {
-    __shared__ float red[16][2], red2[16][2];
+    __shared__ float red[16][2], red2[16][2], red3[16][2];
     const int wave = threadIdx.x >> 6;
     const size_t base = (size_t)blockIdx.x * a.d;
     const bool has_res = a.residual != nullptr;
     const uint4 one = make_uint4(kOneBf16x2, kOneBf16x2, kOneBf16x2, kOneBf16x2);
     const uint4 zero = make_uint4(0, 0, 0, 0);
-    // the row's sum of (h k)^2 and max|h w|
-    auto stats = [&](float k, float &ss, float &top) {
+    // the row's sum of (h k)^2 and max|h q w|
+    auto stats = [&](float k, float q, float &ss, float &top) {
         ss = top = 0.0f;
         for (int c = threadIdx.x * 8; c < a.d; c += 8192) {
             float h[8], g[8];
@@ -198,21 +220,26 @@ __global__ __launch_bounds__(1024) void rmsnorm_long_kernel(NormArgs a) {
 #pragma unroll
             for (int e = 0; e < 8; ++e) {
                 ss = fmaf(h[e] * k, h[e] * k, ss);
-                top = fmaxf(top, fabsf(h[e] * g[e]));
+                top = fmaxf(top, fabsf(h[e] * q * g[e]));
             }
         }
     };
-    float ss, top;
-    stats(1.0f, ss, top);
+    float ss, top, spare;
+    stats(1.0f, 1.0f, ss, top);
     row_reduce<16>(ss, top, red, wave);
-    float r = 1.0f / sqrtf(ss / (float)a.d + a.eps);
-    if (!(ss < __builtin_inff())) {  // uniform in the block
-        float s2, t2;
-        stats(kShrink, s2, t2);
-        row_reduce<16>(s2, t2, red2, wave);
-        r = kShrink / sqrtf(s2 / (float)a.d);
+    const float ms = ss / (float)a.d + a.eps;
+    float r = 1.0f / sqrtf(ms);
+    if (!(ms < __builtin_inff())) {  // uniform in the block, as the next one
+        stats(kShrink, 1.0f, ss, spare);
+        row_reduce<16>(ss, spare, red2, wave);
+        r = kShrink / sqrtf(ss / (float)a.d + a.eps * kShrink * kShrink);
     }
-    const NormFactors nf = norm_factors(r, top);
+    const bool nw = !(top < __builtin_inff());
+    if (nw) {
+        stats(1.0f, r, spare, top);
+        row_reduce<16>(spare, top, red3, wave);
+    }
+    const NormFactors nf = norm_factors(r, top, nw);
     for (int c = threadIdx.x * 8; c < a.d; c += 8192) {
         float h[8];
         norm_h8(h, ld16(a.x + base + c), has_res ? ld16(a.residual + base + c) : zero, has_res);

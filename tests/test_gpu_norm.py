@@ -96,6 +96,30 @@ def test_small_and_large_magnitudes(d, std):
     check(run(x, r, wt), x, r, wt)
 
 
+@pytest.mark.parametrize("d", [64, 1032, 4096, 11008, 16400])
+@pytest.mark.parametrize("x2,w2,eps", [(100, 60, EPS), (100, -60, EPS), (3, 125, EPS), (66, 0, 1e38),
+                                       (62.5, 0, 3e38), (-40, 0, 3e38)])
+def test_ends_of_the_range(d, x2, w2, eps):
+    """Finite n whose h w overflows fp32, and an eps that counts next to squares that do."""
+    log(f"rmsnorm d={d} x 2^{x2} w 2^{w2} eps {eps}")
+    x, _, wt = inputs(3, d, False, True, 12, 2.0 ** x2)
+    wt = (wt.double() * 2.0 ** (w2 - x2)).bfloat16()
+    got = run(x, None, wt, eps=eps)
+    # rows whose n itself leaves fp32 (8 sigma at w 2^125): y is infinite there, no scale exists
+    n = formula(x, None, wt, eps)[0].abs()
+    lim, t = 2.0 ** 128, slack(d)
+    off = n.amax(1) >= lim * (1 - t)
+    keep = ~off
+    check((got[0][keep], got[1][keep], got[2][keep], got[3][keep]), x[keep], None, wt, eps)
+    y, no = got[1][off], n[off]
+    assert torch.isinf(y[no >= lim * (1 + t)]).all()
+    fine = no < lim * (1 - 2.0 ** -8)
+    err = (y.double().abs() - no)[fine].abs()
+    assert (err <= no[fine] * (2.0 ** -8 * 1.01 + t)).all()
+    sure = n.amax(1) >= lim * (1 + t)
+    assert torch.isnan(got[3][sure]).all() and torch.isnan(got[2][sure].float()).all()
+
+
 @pytest.mark.parametrize("d", [512, 1024, 4096, 11008, 16392])
 def test_special_rows(d):
     """Zero rows, infinities and NaN touch their own row alone."""
