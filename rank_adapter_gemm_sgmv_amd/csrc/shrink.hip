@@ -187,12 +187,13 @@ __global__ __launch_bounds__(64 * kWavesPerBlock) void shrink_mfma_kernel(
 #pragma unroll
                 for (int st = 0; st < C::STEPS; ++st) xv[st] = load_x(kb + 32 * st + 8 * g);
             };
-            // At r_max <= 16 every fill's loads are issued before the first fill is used (one
+            // At r_max <= 32 every fill's loads are issued before the first fill is used (one
             // round trip per chunk instead of one per fill; at r_max 16, 30 more VGPRs and four
-            // workgroups per CU instead of five): prefill shrink 9.9 -> 9.4 us, the MLP's
-            // 11008-deep shrink 16.0 -> 15.7 us.  Above r_max 16 the registers would cost a
-            // wave per SIMD.
-            constexpr bool UPFRONT = RM <= 16;
+            // workgroups per CU instead of five): prefill shrink 9.86-9.90 -> 9.34-9.46 us, the MLP's
+            // 11008-deep shrink 16.0 -> 15.7 us; at r_max 32, where LDS holds three workgroups per
+            // CU either way, 509 x 11008 of 256 adapters 37.3 -> 35.9 us, 4096 x 4096 of 8 18.7 ->
+            // 16.7.  At r_max 64 it brought nothing (31.4 and 32.0, 16.7 and 16.3).
+            constexpr bool UPFRONT = RM <= 32;
             uint4 pav[UPFRONT ? C::FILLS : 1][C::AL];
             XV pxv[UPFRONT ? C::FILLS : 1][C::STEPS];
             if constexpr (UPFRONT) {
