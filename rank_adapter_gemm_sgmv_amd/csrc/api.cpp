@@ -83,7 +83,7 @@ size_t gemm_bytes(int32_t M, int32_t d_in, int32_t d_out, int32_t r_max, int32_t
 
 // The same of lora_linear_fp8: its tiles' K slices or, for decode batches, the decode plans'.
 size_t fp8_gemm_bytes(int32_t M, int32_t d_in, int32_t d_out, int32_t r_max, int32_t n_adapters) {
-    const size_t a = fp8_partial_floats(M, d_in, d_out),
+    const size_t a = fp8_partial_floats(M, d_in, d_out, r_max, n_adapters),
                  b = decode_fp8_partial_floats(M, d_in, d_out, rank_bucket(r_max), n_adapters);
     return round_up((a > b ? a : b) * sizeof(float));
 }
@@ -627,8 +627,8 @@ hipError_t run_fp8(const Fp8Gemm &g, const uint16_t *A, const uint16_t *B, const
                               s)) != hipSuccess)
         return e;
     const LoraEpilogue ep{spart, ksplit, B, scale, ids, rb, n_adapters, ranks, nullptr, 0, r_max};
-    const Fp8Plan pl = fp8_plan(g.M, g.K, g.N, y_f32);
-    if ((e = launch_gemm_fp8(g, pl, y, y_f32, sg, ep, epi, gpart, s)) != hipSuccess || pl.ks == 1)
+    const Fp8Plan pl = fp8_plan(g.M, g.K, g.N, y_f32, r_max, n_adapters);
+    if ((e = launch_gemm_fp8(g, pl, y, y_f32, sg, ep, epi, gpart, s)) != hipSuccess || !pl.split)
         return e;
     SkProj pj{};
     pj.B[0] = B;

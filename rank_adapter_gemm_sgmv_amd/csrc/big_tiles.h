@@ -289,9 +289,9 @@ __device__ __forceinline__ void stage_t(uint4 *const (&xs)[4], const LoraEpilogu
 }
 
 // acc += T B_a for every run of one adapter among the tile's rows, in steps of 16 rank columns:
-// B_a's 16 rank rows twice (for T's two halves) in a W slot.  Four steps (the rank chunks of one,
-// two or four runs) share their two barriers and have their loads in flight together, a batch
-// ahead of their use.  Waves, and 32-row blocks, without a row of a run skip its step.
+// B_a's 16 rank rows twice (for T's two halves) in a W slot.  Four steps share their two barriers and
+// have their loads in flight together, a batch ahead of their use (two more batches ahead changed
+// nothing).  Waves, and 32-row blocks, without a row of a run skip its step.
 //
 // A row outside a run still meets the run's B, times zero.  So that an adapter whose B holds an
 // infinity or a NaN spoils its own rows alone, such values are staged as zeros here, and a second
@@ -305,60 +305,85 @@ __device__ __forceinline__ bool add_lora_steps(f32x16_t (&acc)[C::TM][C::TN], ui
     constexpr int kHalf = kBK / 2;
     const int RM = ep.r_max;
     const int sh = RM <= 16 ? 0 : RM == 32 ? 1 : 2;  // 2^sh rank chunks per run
-    const int G = 4 >> sh;                            // runs per batch
     auto slot = [](int u, uint4 *const (&v)[4]) { return u == 0 ? v[0] : u == 1 ? v[1] : u == 2 ? v[2] : v[3]; };
-    const int n_runs = rows.n_runs;
-    static_assert(kHalf * C::WCH <= C::NT, "one piece of B per thread and step");
+    const int n_runs = __builtin_amdgcn_readfirstlane(rows.n_runs);
+    wm0 = __builtin_amdgcn_readfirstlane(wm0);
+    static_assert(kHalf * C::WCH == C::NT, "one piece of B per thread and step");
     const int br = tid / C::WCH, bc = tid % C::WCH, n = n0 + bc * 8;
     uint4 bv[4];
+    // Step t of the tile: the runs are taken in two halves in turn, whose rows mostly belong to
+    // different waves (in run order, half of the waves waited at each barrier for the other:
+    // 1024 x 1024 x 4096 of 256 adapters rank 64, 131 -> 111 us; 256 x 256 tiles spill over it, 4096 x
+    // 4096 x 4096 244 -> 262); a row meets its own run's rank chunks in ascending order.
+    constexpr bool SIDES = C::BM == 128;
+    const int two = SIDES && n_runs > 1 ? 1 : 0, half = two ? (n_runs + 1) / 2 : n_runs;
+    const int n_steps = half << (sh + two);
+    auto chunk_of = [&](int T0, int u) { return (SIDES && two ? (T0 + u) >> 1 : u) & ((1 << sh) - 1); };
+    // Lane l holds the first row (SIDES: and the end) and the adapter of step T0 + l's run (else:
+    // of the l-th run of the batch), which the steps take from there as scalars (read from LDS
+    // step by step, they were a chain of two reads in front of each: 154 -> 131 us).
+    int span, adapter;
+    auto runs_of = [&](int T0) {
+        if constexpr (SIDES) {
+            const int t = T0 + lane, run = (t & two) * half + (t >> (sh + two));
+            const int first = rows.run[min(run, n_runs)];
+            span = first | rows.run[min(run + 1, n_runs)] << 16;
+            adapter = t < n_steps && run < n_runs ? rows.id[first] : -1;
+        } else {
+            const int run = (T0 >> sh) + lane;
+            span = rows.run[min(run, n_runs)];
+            adapter = run < n_runs ? rows.id[span] : -1;
+        }
+    };
+    auto lane_of = [&](int u) { return SIDES ? u : u >> sh; };
     // B_a's rank rows: all of a padded pool's stride (zero past the rank), the rank's in a
     // compact one
-    auto load = [&](int R0) {
+    auto load = [&](int T0) {
 #pragma unroll
         for (int u = 0; u < 4; ++u) {
-            const int run = R0 + (u >> sh);
-            const int a = run < n_runs ? rows.id[rows.run[run]] : -1;
-            const int rank = (u & ((1 << sh) - 1)) * kHalf + br;
+            const int a = __builtin_amdgcn_readlane(adapter, lane_of(u));
+            const int rank = chunk_of(T0, u) * kHalf + br;
             bv[u] = make_uint4(0, 0, 0, 0);
-            if (a >= 0 && br < kHalf && n < N) {
+            if (a >= 0) {
                 int ra = ep.roff ? min(max(ep.ranks[a], 0), RM) : ep.pstride;
                 const int brow0 = adapter_row0(ep.roff, ep.pool_rows, a, ep.pstride, ra);
-                if (rank < ra) bv[u] = ld16(ep.B + ((size_t)brow0 + rank) * N + n);
+                if (rank < ra && n < N) bv[u] = ld16(ep.B + ((size_t)brow0 + rank) * N + n);
             }
         }
     };
     bool odd = false;
+    runs_of(0);
     load(0);
     if constexpr (!ODD) stage_t<C>(xs, ep, rows, M, tid);  // (the first batch's barrier covers T too)
 #pragma unroll 1
-    for (int R0 = 0; R0 < n_runs; R0 += G) {
-        if (ODD || R0 > 0) lds_barrier();  // every wave is done with the W slots
-        if (br < kHalf) {
+    for (int T0 = 0; T0 < n_steps; T0 += 4) {
+        if (ODD || T0 > 0) lds_barrier();  // every wave is done with the W slots
 #pragma unroll
-            for (int u = 0; u < 4; ++u) {
-                uint32_t d[4] = {bv[u].x, bv[u].y, bv[u].z, bv[u].w};
+        for (int u = 0; u < 4; ++u) {
+            uint32_t d[4] = {bv[u].x, bv[u].y, bv[u].z, bv[u].w};
 #pragma unroll
-                for (int e = 0; e < 4; ++e) {
-                    // the halves whose exponent is all ones
-                    const uint32_t m = ((d[e] & 0x7F80u) == 0x7F80u ? 0xFFFFu : 0u) |
-                                       ((d[e] & 0x7F800000u) == 0x7F800000u ? 0xFFFF0000u : 0u);
-                    odd |= m != 0;
-                    d[e] &= ODD ? m : ~m;
-                }
-                const uint4 v = make_uint4(d[0], d[1], d[2], d[3]);
-                ws[u][br * C::WCH + (bc ^ ((br & 3) << 2))] = v;
-                ws[u][(br + kHalf) * C::WCH + (bc ^ ((br & 3) << 2))] = v;
+            for (int e = 0; e < 4; ++e) {
+                // the halves whose exponent is all ones
+                const uint32_t m = ((d[e] & 0x7F80u) == 0x7F80u ? 0xFFFFu : 0u) |
+                                   ((d[e] & 0x7F800000u) == 0x7F800000u ? 0xFFFF0000u : 0u);
+                odd |= m != 0;
+                d[e] &= ODD ? m : ~m;
             }
+            const uint4 v = make_uint4(d[0], d[1], d[2], d[3]);
+            ws[u][br * C::WCH + (bc ^ ((br & 3) << 2))] = v;
+            ws[u][(br + kHalf) * C::WCH + (bc ^ ((br & 3) << 2))] = v;
         }
         lds_barrier();
-        load(R0 + G);
+        const int rows_of = span, of = adapter;  // this batch's
+        runs_of(T0 + 4);
+        load(T0 + 4);
 #pragma unroll 1
         for (int u = 0; u < 4; ++u) {
-            const int run = R0 + (u >> sh);
-            if (run >= n_runs) break;
-            const int lo = rows.run[run], hi = rows.run[run + 1];
-            if (rows.id[lo] < 0 || hi <= wm0 || lo >= wm0 + C::WTM) continue;  // uniform in the wave
-            mfma_run<C, ODD>(acc, slot(u & ((1 << sh) - 1), xs), slot(u, ws), lane, wm0, wn0, lo, hi);
+            const int k = lane_of(u), span_k = __builtin_amdgcn_readlane(rows_of, k);
+            const int lo = SIDES ? span_k & 0xFFFF : span_k;
+            const int hi = SIDES ? span_k >> 16 : __builtin_amdgcn_readlane(rows_of, k + 1);
+            if (__builtin_amdgcn_readlane(of, k) < 0 || hi <= wm0 || lo >= wm0 + C::WTM) continue;  // uniform
+            mfma_run<C, ODD>(acc, slot(chunk_of(T0, u), xs), slot(u, ws), lane, wm0, wn0, lo, hi);
         }
     }
     return __syncthreads_or(odd);
@@ -366,9 +391,10 @@ __device__ __forceinline__ bool add_lora_steps(f32x16_t (&acc)[C::TM][C::TN], ui
 
 // The LoRA delta of one output tile (rows in segment order), after its K loop: acc += scale_a
 // t[rows, :] B_a[:, columns].  xs, ws: four slot pairs, free once every wave has passed the first
-// barrier here.  256 adapters on 4096 x 4096 x 11008 8-bit rows (17 runs per tile): 280 us per kernel,
-// 298 with T staged per batch, zeros outside its runs, and B loaded behind the barrier; 4096 x 4096
-// x 4096 bf16: 146 and 164; with 8 adapters (under two runs per tile) 230, and 131 bf16 with 4.
+// barrier here.  Whole call, 1, 8, 64 and 256 adapters of rank 16, us: 4096 x 4096 x 11008 8-bit rows
+// 206, 205, 216, 258 (17 runs per tile in the last; the kernel alone 298 before T was staged once
+// for every row and B loaded ahead); 4096 x 4096 x 4096 bf16 143, 142, 148, 161; 1300 x 1024 x 4096
+// bf16 40, 41, 44, 57.
 template <class C>
 __device__ __forceinline__ void add_lora_runs(f32x16_t (&acc)[C::TM][C::TN], uint4 *const (&xs)[4],
                                               uint4 *const (&ws)[4], const LoraEpilogue &ep,

@@ -396,12 +396,12 @@ struct Fp8Gemm {
 };
 // big: 256 x 256 tiles (bf16 y), else 128 x 128; ks > 1 slices of k_per_split of K.
 struct Fp8Plan {
-    bool big;
+    bool big, split;
     int ks, k_per_split;
 };
-Fp8Plan fp8_plan(int M, int K, int N, bool y_f32);
-size_t fp8_partial_floats(int M, int K, int N);
-// p.ks == 1: y from rows in segment order, with the delta and the epilogue.  p.ks > 1: slices
+Fp8Plan fp8_plan(int M, int K, int N, bool y_f32, int r_max, int n_adapters);
+size_t fp8_partial_floats(int M, int K, int N, int r_max, int n_adapters);
+// !p.split: y from rows in segment order, with the delta and the epilogue.  p.split: slices
 // partial[ks][M][N] of x8 W8^T w_scale (launch_splitk_reduce_lora must follow).
 hipError_t launch_gemm_fp8(const Fp8Gemm &g, const Fp8Plan &p, void *y, bool y_f32, Seg seg,
                            const LoraEpilogue &ep, const Epilogue &epi, float *partial,

@@ -338,19 +338,25 @@ hipError_t launch_fp8_cfg(const Fp8Gemm &g, const Fp8Plan &p, void *y, bool y_f3
 // A slice of K is a multiple of two stages.
 constexpr int kMinK = 2 * kK8;
 
-// Up to 256 small tiles split K, into as many slices as two workgroups per CU hold at once: a
-// tile per CU leaves its loads and its epilogue without a neighbour to fill their waits.  Whole
-// call at d_out 4096, rank 64, fp32 residual, one slice -> split: 1024 x 512 52.5 -> 42.3 us,
-// 1024 x 4096 76.4 -> 65.3, 1024 x 11008 140 -> 115; 768 x 11008, two slices or (a second, short
-// round) three: 97 or 118.  Above 256 the slices cost more than they bring: 1280 x 4096 80 ->
-// 88 us, 1536 x 11008 144 -> 164 with three slices.
-Fp8Plan fp8_plan(int M, int K, int N, bool y_f32) {
+// Up to 256 small tiles may split K, into as many slices as two workgroups per CU hold at once. That
+// costs the slices' way through memory and a launch (the more, the more tiles); whole tiles cost a
+// walk through K at a workgroup or two per CU and, behind it, one through the adapter runs of the
+// tile's rows, at every rank chunk (one slice is worth it for the latter alone).  us split and whole,
+// d_out 4096: rank 16 of 4 adapters 520 x 1040 39.8 and 28.9, 520 x 4112 48.5 and 52.2, 520 x 11008
+// 62.0 and 79.2, 1024 x 4112 61.5 and 56.1; rank 64 of 64 260 x 512 37.0 and 96.9, 1024 x 512 53.5 and 54.5,
+// 1024 x 4112 85.5 and 98.9; d_out 264, rank 16 of 4: 260 x 2048 28.6 and 28.3, 260 x 4112 30.0
+// and 36.7.  Rounds: 768 x 11008 x 4096 97 us in two slices, 118 in three (a second, short
+// round).  Above 256 tiles the slices cost more than they bring: 1280 x 4096 x 4096 80 -> 88 us,
+// 1536 x 11008 144 -> 164 with three.
+Fp8Plan fp8_plan(int M, int K, int N, bool y_f32, int r_max, int n_adapters) {
     Fp8Plan p{};
     p.ks = 1;
     p.k_per_split = K;
     const long t128 = (long)((M + 127) / 128) * ((N + 127) / 128);
+    const long runs = 128L * (n_adapters < M ? n_adapters : M) / (M > 128 ? M : 128);
     p.big = wide_tiles(M, N) && !y_f32;
-    if (t128 <= 256) {
+    p.split = t128 <= 256 && K + 10L * r_max * runs > 2600 + 9 * t128;
+    if (p.split) {
         const int steps = (K + kMinK - 1) / kMinK;
         int ks = (int)(512 / t128);  // two workgroups per CU, one round
         if (ks > 16) ks = 16;
@@ -362,16 +368,17 @@ Fp8Plan fp8_plan(int M, int K, int N, bool y_f32) {
     return p;
 }
 
-size_t fp8_partial_floats(int M, int K, int N) {
-    const Fp8Plan p = fp8_plan(M, K, N, true);  // (the split does not depend on y's type)
-    return p.ks > 1 ? (size_t)p.ks * M * N : 0;
+size_t fp8_partial_floats(int M, int K, int N, int r_max, int n_adapters) {
+    // (the split does not depend on y's type)
+    const Fp8Plan p = fp8_plan(M, K, N, true, r_max, n_adapters);
+    return p.split ? (size_t)p.ks * M * N : 0;
 }
 
 hipError_t launch_gemm_fp8(const Fp8Gemm &g, const Fp8Plan &p, void *y, bool y_f32, Seg seg,
                            const LoraEpilogue &ep, const Epilogue &epi, float *partial,
                            hipStream_t s) {
     if (g.M < 1 || g.K < 16 || g.K % 16 != 0 || g.N < 8 || g.N % 8 != 0) return hipErrorInvalidValue;
-    if (p.ks > 1) {
+    if (p.split) {
         if (partial == nullptr || p.k_per_split % kMinK != 0) return hipErrorInvalidValue;
         return launch_fp8_cfg<Big<128, 128>, false>(g, p, y, y_f32, seg, ep, epi, partial, s);
     }
