@@ -359,16 +359,17 @@ hipError_t run_linear(const void *x, const void *W, const void *A, const void *B
     if (epi && !splits && !dec) prefill = true;
     // AUTO with an epilogue weighs the sequences where both exist.  Prefill has one workgroup per
     // 128 x 128 tile go through all of K and then through the tile's adapter runs; split K fills
-    // the chip but writes and adds partial sums in proportion to the tiles (in plain slices, where
-    // stream-K does not apply, it also reads its operands once per small tile: a longer K then
-    // no longer speaks for it).  Microseconds for split K and prefill, d_out 4096: 300 x 1024 rank
-    // 16 of 4 adapters 33.6 and 26.6, 300 x 11008 68.8 and 91.1, 1024 x 4096 71.7 and 55.8,
-    // 1024 x 11008 118 and 116; rank 64 of 256 adapters 300 x 1024 46.7 and 278, 1024 x 1024 72.9
-    // and 154; in slices, d_out 2760, rank 16 of 4, 1300 x 11008 213 and 132.
+    // the chip but writes and adds partial sums in proportion to the tiles.  In plain slices,
+    // where stream-K does not apply, it also reads its operands once per small tile: a K above
+    // 4096 then no longer speaks for it, and with many tiles against it.  us for split K and prefill,
+    // d_out 4096: rank 16 of 4 adapters 300 x 512 27.7 and 24.0, 300 x 11008 73.3 and 97.0, 1000 x
+    // 2048 60.5 and 41.6, 1000 x 11008 123 and 121; rank 32 of 256 300 x 512 36.3 and 106, 768 x 2048
+    // 61.9 and 86.5, 1000 x 2048 71.3 and 84.4; in slices, d_out 2760, rank 16 of 4, 1300 x 11008
+    // 215 and 133, rank 32 of 256 248 and 192.
     if (mode == LORA_MODE_AUTO && splits && !dec) {
         const long tiles = (long)((M + 127) / 128) * ((d_out + 127) / 128);
         const long runs = 128L * (n_adapters < M ? n_adapters : M) / (M > 128 ? M : 128);
-        const long k = flat && d_in > 4096 ? 4096 : d_in;
+        const long k = !flat || d_in <= 4096 ? d_in : tiles > 128 ? 0 : 4096;
         prefill = k + 12L * r_max * runs < 42L * (tiles < 256 ? tiles : 256);
     }
     char *p = static_cast<char *>(ws);
