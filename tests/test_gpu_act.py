@@ -92,6 +92,9 @@ SEQUENCES = [
     (1024, 256, 2056, 1024, 40, AUTO), (1300, 1032, 1032, 700, 64, AUTO), (1300, 4104, 2056, 3, 8, AUTO),
     # a few more tiles than one round of 256 x 256 ones
     (4500, 128, 4096, 9, 16, PRE),
+    # small tiles over one, two, an odd number and very many runs, at each number of rank chunks
+    (140, 128, 136, 1, 64, PRE), (129, 128, 136, 2, 64, PRE), (900, 128, 520, 33, 32, PRE),
+    (900, 136, 520, 51, 8, PRE), (300, 128, 264, 300, 48, PRE), (131, 64, 72, 3, 17, PRE),
 ]
 
 

@@ -114,6 +114,9 @@ SHAPES = [
     (700, 2096, 136, 5, 8), (1000, 2048, 520, 600, 16), (1500, 1040, 264, 30, 64), (900, 304, 8200, 4, 16),
     (1024, 512, 4096, 70, 64), (768, 1040, 4096, 4, 16), (4500, 144, 4096, 9, 16),
     (3000, 272, 2056, 5, 8), (4100, 528, 3080, 3, 16), (4100, 1024, 3080, 700, 40), (2000, 256, 6408, 9, 16),
+    # one slice of K for the adapters' sake, less than a stage and with a rest; whole tiles below
+    (260, 64, 264, 200, 64), (300, 272, 520, 300, 32), (260, 16, 264, 200, 33), (520, 1040, 1032, 4, 16),
+    (2000, 512, 264, 40, 64), (4096, 400, 376, 150, 1),
 ]
 
 
