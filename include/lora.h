@@ -389,8 +389,9 @@ lora_status_t lora_linear_fp8(const void *x8, const float *x_scale, const void *
  * and y8 16-byte aligned, y_scale 4-byte.  d a positive multiple of 8, at most 2^20.  sum and
  * y may each be x or residual itself (in place); outputs must not overlap each other or an input
  * otherwise.  A row that holds an infinity or a NaN gives NaN wherever the formula does in y,
- * and NaN for its scale and every code; so does, for scale and codes, a row with an n beyond
- * fp32's range (infinite in y).  Rows are independent; no workspace.
+ * and NaN for its scale and every code; so does, for scale and codes, a row with an n that is NaN
+ * (a NaN in weight, or an infinite weight on h = 0) or beyond fp32's range (infinite in y).  Rows
+ * are independent; no workspace.
  * Errors: LORA_ERR_SHAPE (M, d), LORA_ERR_VALUE (eps not finite or below 1e-30), LORA_ERR_NULL
  * (x; y and y8 both NULL; one of y8 and y_scale alone), LORA_ERR_ALIGN, LORA_ERR_HIP. */
 lora_status_t lora_rmsnorm(const void *x, const void *residual, const void *weight, float eps,

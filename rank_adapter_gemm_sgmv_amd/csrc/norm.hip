@@ -10,7 +10,9 @@
 //  * A row is read once and stays in registers between its statistics and its output, as
 //    fp32 h (never rounded to the bf16 sum first).
 //  * Both statistics come from one reduction: r > 0 is the same for the whole row, so
-//    max|n| = r max|h w|, and the sum of squares and max|h w| are reduced side by side.
+//    max|n| = r max|h w|, and the sum of squares and max|h w| are reduced side by side.  The
+//    maximum keeps a NaN (v_maximum3_f32 takes no more instructions than the one that drops it),
+//    so that a NaN in weight, or an infinite weight on a zero h, reaches the row's scale.
 //  * The 8-bit codes are h w (448 / max|h w|): r cancels, and with it its rounding.
 //  * WPR waves share a row, so that a lane holds one to three 16-byte pieces of it and all of
 //    the row's loads are in flight at once (one row alone is one round trip to memory).
@@ -35,9 +37,11 @@ __device__ __forceinline__ float wave_sum(float v) {
     for (int d = 1; d < 64; d <<= 1) v += __shfl_xor(v, d, 64);
     return v;
 }
+// the larger of a and b, NaN if either is
+__device__ __forceinline__ float max_nan(float a, float b) { return __builtin_elementwise_maximum(a, b); }
 __device__ __forceinline__ float wave_max(float v) {
 #pragma unroll
-    for (int d = 1; d < 64; d <<= 1) v = fmaxf(v, __shfl_xor(v, d, 64));
+    for (int d = 1; d < 64; d <<= 1) v = max_nan(v, __shfl_xor(v, d, 64));
     return v;
 }
 
@@ -65,7 +69,7 @@ __device__ __forceinline__ NormFactors norm_factors(float r, float top, bool nw)
     o.s = fmaxf(mx, kFloor8) / kTop8;
     // (below the floor the codes are n / s with the floor's s; above it r cancels)
     o.f = mx > kFloor8 ? kTop8 / top : q / o.s;
-    // a row with an infinity (r = 0) or a NaN has no scale: all its codes are NaN
+    // a row with an infinity (r = 0) or a NaN, in h or in h w, has no scale: all its codes are NaN
     if (!(mx < __builtin_inff()) || !(r > 0.0f)) o.s = o.f = __builtin_nanf("");
     return o;
 }
@@ -116,7 +120,7 @@ __device__ __forceinline__ void row_reduce(float &ss, float &top, float (*red)[2
 #pragma unroll
         for (int i = 1; i < WPR; ++i) {
             ss += red[w0 + i][0];
-            top = fmaxf(top, red[w0 + i][1]);
+            top = max_nan(top, red[w0 + i][1]);
         }
     }
 }
@@ -157,7 +161,7 @@ __global__ __launch_bounds__(WPR > 4 ? WPR * 64 : 256) void rmsnorm_kernel(NormA
 #pragma unroll
             for (int e = 0; e < 8; ++e) {
                 ss = fmaf(h[i][e], h[i][e], ss);
-                top = fmaxf(top, fabsf(h[i][e] * g[e]));
+                top = max_nan(top, fabsf(h[i][e] * g[e]));
             }
         }
     }
@@ -187,7 +191,7 @@ __global__ __launch_bounds__(WPR > 4 ? WPR * 64 : 256) void rmsnorm_kernel(NormA
                 float g[8];
                 unpack8(wv[i], g);
 #pragma unroll
-                for (int e = 0; e < 8; ++e) top = fmaxf(top, fabsf(h[i][e] * r * g[e]));
+                for (int e = 0; e < 8; ++e) top = max_nan(top, fabsf(h[i][e] * r * g[e]));
             }
         row_reduce<WPR>(s3, top, red3, wave);
     }
@@ -220,7 +224,7 @@ __global__ __launch_bounds__(1024) void rmsnorm_long_kernel(NormArgs a) {
 #pragma unroll
             for (int e = 0; e < 8; ++e) {
                 ss = fmaf(h[e] * k, h[e] * k, ss);
-                top = fmaxf(top, fabsf(h[e] * q * g[e]));
+                top = max_nan(top, fabsf(h[e] * q * g[e]));
             }
         }
     };

@@ -224,3 +224,31 @@ def test_other_stream_and_graph():
             assert torch.equal(a.view(torch.uint8), b.view(torch.uint8)), rep
         call()
         torch.cuda.synchronize()
+
+
+@pytest.mark.parametrize("d", [64, 512, 1024, 1032, 4096, 11008, 16384, 16392])
+@pytest.mark.parametrize("kind", ["nan", "inf times zero", "inf", "none"])
+def test_special_weights(d, kind):
+    """n that is NaN or infinite in one column leaves its row without a scale: NaN in y_scale and
+    every code, as max|n| of the formula; y is spoilt in that column alone."""
+    log(f"special weights d={d} {kind}")
+    x, r, wt = inputs(5, d, True, True, 71)
+    base = run(x, r, wt)
+    at = d - 3
+    hit = [0, 1, 2, 3, 4]
+    if kind == "nan":
+        wt[at] = float("nan")
+    elif kind == "inf":
+        wt[at] = float("-inf")
+        x[:, at], r[:, at] = 2.0, 1.0
+    elif kind == "inf times zero":
+        wt[at] = float("inf")
+        x[:, at], r[:, at] = 1.0, -1.0
+    else:
+        hit = []
+    n, _ = formula(x, r, wt)
+    _, y, y8, sc = run(x, r, wt)
+    assert torch.equal(torch.isnan(y), torch.isnan(n)) and torch.equal(torch.isinf(y), torch.isinf(n))
+    assert torch.isnan(sc[hit]).all() and torch.isnan(y8[hit].float()).all()
+    if not hit:
+        assert torch.equal(sc, base[3]) and torch.equal(y8.view(torch.uint8), base[2].view(torch.uint8))
