@@ -272,7 +272,7 @@ void launch_one(const NormArgs &a, hipStream_t s) {
 //   d 11008 8 x 3: 4.43 at 1 row, 75.9 at 4096;  16 x 2: 4.58, 92.1
 // so eight waves share a row wherever it has a piece for each of their lanes, and only rows of
 // 513-1024 elements go by the number of rows.
-hipError_t launch_rmsnorm(const NormArgs &a, hipStream_t s) {
+static void launch_rows(const NormArgs &a, hipStream_t s) {
     if (a.d <= 512) launch_one<1, 1>(a, s);
     else if (a.d <= 1024 && a.M >= 1024) launch_one<1, 2>(a, s);
     else if (a.d <= 2048) launch_one<4, 1>(a, s);
@@ -281,6 +281,26 @@ hipError_t launch_rmsnorm(const NormArgs &a, hipStream_t s) {
     else if (a.d <= 12288) launch_one<8, 3>(a, s);
     else if (a.d <= 16384) launch_one<16, 2>(a, s);
     else launch(rmsnorm_long_kernel, dim3((unsigned)a.M), dim3(1024), 0, s, a);
+}
+
+// A launch holds fewer than 2^32 threads: LORA_MAX_ROWS = 2^22 rows on blocks of 1024 are one too
+// many, so rows go in parts of 2^21 (rows are independent).
+hipError_t launch_rmsnorm(const NormArgs &a, hipStream_t s) {
+    constexpr int kPart = 1 << 21;
+    for (int m = 0; m < a.M; m += kPart) {
+        NormArgs p = a;
+        const size_t at = (size_t)m * a.d;
+        p.M = a.M - m < kPart ? a.M - m : kPart;
+        p.x = a.x + at;
+        if (a.residual) p.residual = a.residual + at;
+        if (a.sum) p.sum = a.sum + at;
+        if (a.y) p.y = a.y + at;
+        if (a.y8) {
+            p.y8 = a.y8 + at;
+            p.y_scale = a.y_scale + m;
+        }
+        launch_rows(p, s);
+    }
     return hipGetLastError();
 }
 

@@ -252,3 +252,30 @@ def test_special_weights(d, kind):
     assert torch.isnan(sc[hit]).all() and torch.isnan(y8[hit].float()).all()
     if not hit:
         assert torch.equal(sc, base[3]) and torch.equal(y8.view(torch.uint8), base[2].view(torch.uint8))
+
+
+@pytest.mark.parametrize("d", [8, 12296])
+def test_most_rows(d):
+    """LORA_MAX_ROWS rows in place, also of a d whose blocks hold 1024 threads (2^32 in all)."""
+    M = L.LORA_MAX_ROWS
+    if torch.cuda.mem_get_info()[0] < M * d * 2 + (8 << 30):
+        pytest.skip("not enough memory")
+    log(f"rmsnorm M={M} d={d}")
+    x = torch.zeros(M, d, dtype=torch.bfloat16, device="cuda")
+    at = [0, 1, 2 ** 21 - 1, 2 ** 21, 2 ** 21 + 1, M - 2, M - 1]
+    tail, _, wt = inputs(len(at), d, False, True, 81)
+    for i, m in enumerate(at):
+        x[m] = tail[i]
+    sc = torch.full((M,), 7.0, device="cuda")
+    y8 = torch.full((M * d,), 0x55, dtype=torch.uint8, device="cuda") if d == 8 else None
+    L.lora_rmsnorm(x, None, wt, EPS, M, d, None, x, y8, None if y8 is None else sc)
+    torch.cuda.synchronize()
+    if y8 is not None:
+        y8 = y8.view(M, d).view(torch.float8_e4m3fn)
+        check((None, x[at], y8[at], sc[at]), tail, None, wt)
+        assert (sc == 2.0 ** -60 / 448).sum() == M - len(at)
+    else:
+        check((None, x[at], None, None), tail, None, wt)
+    assert (x[3:2 ** 21 - 1] == 0).all()
+    del x, y8, sc
+    torch.cuda.empty_cache()
