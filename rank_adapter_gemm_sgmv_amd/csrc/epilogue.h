@@ -7,10 +7,10 @@
 // is still in registers, so the four optional operands cost their own bytes and nothing else.
 //
 // Activations use the hardware's exp2 and reciprocal (about 1 ulp each); exp2's argument is
-// rounded once or twice, a relative error of |z| 2^-23 in e^z where e^z matters (|z| of a few).
-// GELU's Gaussian is Abramowitz and Stegun 7.1.26 in its erfc form, |error| <= 1.5e-7: the
-// library's erf costs three times the instructions, which a prefill tile cannot hide behind
-// MFMAs (its epilogue runs after the last of them).
+// rounded once or twice, a relative error of |z| 2^-23 in e^z.
+// GELU's Gaussian tail is a polynomial fitted here (epi_gelu): the library's erf costs three times
+// the instructions, which a prefill tile cannot hide behind MFMAs (its epilogue runs after the last of
+// them).
 #pragma once
 
 #include "common.h"
@@ -48,14 +48,23 @@ __device__ __forceinline__ float epi_gelu_tanh(float z) {
     return z * __builtin_amdgcn_rcpf(1.0f + e);
 }
 
-// z Phi(z) = max(z, 0) - |z| erfc(|z| / sqrt(2)) / 2, with erfc(u) = t (a1 + t (a2 + ...)) e^-u^2,
-// t = 1 / (1 + p u); |z| is kept finite against 0 (it is inf - inf 0 otherwise)
+// z Phi(z) = max(z, 0) - |z| Phi(-|z|), with Phi(-a) = t P(t) e^(-a^2 / 2), t = 1 / (1 + 0.275 a).
+// P is the polynomial of degree 8 whose t P(t) has the smallest largest relative error against
+// erfcx(a / sqrt(2)) / 2 over 0 <= a <= 40 (4.3e-8; a linear programme over its values), so that
+// the tail of a negative z is right to its own size: the result is within (24 + 1.5 z^2) 2^-24 of it
+// (t 3 units, up to 2.9 times in P; P 4; products and exp2 6; exp2's argument 1.25 z^2).  One term less
+// is off by 6.4e-7, one of five terms with an absolute bound (1.5e-7) was off by 5e-5 at z = -3 and 4e-3
+// at -6.  |z| is kept finite against 0 (it is inf - inf 0 otherwise).
 __device__ __forceinline__ float epi_gelu(float z) {
-    const float t = __builtin_amdgcn_rcpf(fmaf(0.3275911f * 0.70710678118654752f, fabsf(z), 1.0f));
-    float p = fmaf(0.5f * 1.061405429f, t, 0.5f * -1.453152027f);
-    p = fmaf(p, t, 0.5f * 1.421413741f);
-    p = fmaf(p, t, 0.5f * -0.284496736f);
-    p = fmaf(p, t, 0.5f * 0.254829592f);
+    const float t = __builtin_amdgcn_rcpf(fmaf(0.275f, fabsf(z), 1.0f));
+    float p = fmaf(0.027061667f, t, -0.110292655f);
+    p = fmaf(p, t, 0.129608795f);
+    p = fmaf(p, t, -0.0347237383f);
+    p = fmaf(p, t, 0.0878079468f);
+    p = fmaf(p, t, 0.0789904468f);
+    p = fmaf(p, t, 0.102181808f);
+    p = fmaf(p, t, 0.109655047f);
+    p = fmaf(p, t, 0.109710667f);
     const float tail = p * t * __builtin_amdgcn_exp2f(-0.5f * kLog2e * z * z);
     return fmaf(-fminf(fabsf(z), 3e38f), tail, fmaxf(z, 0.0f));
 }
