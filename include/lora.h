@@ -258,8 +258,8 @@ lora_status_t lora_linear_compact(const void *x, const void *W, const void *A, c
  * read before it is written) and must not overlap it otherwise.  Activations: RELU max(z, 0);
  * SILU z / (1 + e^-z); GELU z Phi(z) with the normal distribution Phi; GELU_TANH its tanh form,
  * z / 2 (1 + tanh(sqrt(2 / pi) (z + 0.044715 z^3))).  Each is within a few fp32 steps of
- * itself, plus its exponential's: |z| steps (SILU), z^2 (GELU), 5 |v| for tanh(v)
- * (GELU_TANH).  With silu and mul, a gate projection
+ * itself, plus its exponential's: |z| steps (SILU), z^2 (GELU), 5 |v| for tanh(v) (GELU_TANH);
+ * these three give NaN at -infinity, as their formulas do.  With silu and mul, a gate projection
  * ([P1], "How much memory does one LoRA adapter actually cost?", gate_proj) writes the MLP's
  * silu(gate) * up. */
 typedef enum LORA_ENUM_INT {

@@ -54,7 +54,7 @@ __device__ __forceinline__ float epi_gelu_tanh(float z) {
 // the tail of a negative z is right to its own size: the result is within (24 + 1.5 z^2) 2^-24 of it
 // (t 3 units, up to 2.9 times in P; P 4; products and exp2 6; exp2's argument 1.25 z^2).  One term less
 // is off by 6.4e-7, one of five terms with an absolute bound (1.5e-7) was off by 5e-5 at z = -3 and 4e-3
-// at -6.  |z| is kept finite against 0 (it is inf - inf 0 otherwise).
+// at -6.  +infinity keeps a finite factor against e^-inf = 0; -infinity gives NaN, as z Phi(z) does.
 __device__ __forceinline__ float epi_gelu(float z) {
     const float t = __builtin_amdgcn_rcpf(fmaf(0.275f, fabsf(z), 1.0f));
     float p = fmaf(0.027061667f, t, -0.110292655f);
@@ -66,7 +66,7 @@ __device__ __forceinline__ float epi_gelu(float z) {
     p = fmaf(p, t, 0.109655047f);
     p = fmaf(p, t, 0.109710667f);
     const float tail = p * t * __builtin_amdgcn_exp2f(-0.5f * kLog2e * z * z);
-    return fmaf(-fminf(fabsf(z), 3e38f), tail, fmaxf(z, 0.0f));
+    return fmaf(-fabsf(fminf(z, 3e38f)), tail, fmaxf(z, 0.0f));
 }
 
 // The activation of V elements (one branch for all of them).
