@@ -279,7 +279,9 @@ typedef struct {
 /* lora_linear with an epilogue: z = x W + (x A_i) B_i scale_i (rows with id -1: x W), then epi
  * as above.  epi: a HOST struct read during the call; NULL gives lora_linear's result.  The
  * other arguments, the workspace (lora_workspace_bytes()), modes and errors are lora_linear's
- * (with epi, AUTO also weighs d_in, d_out and the adapters a tile meets against M); also
+ * (with epi, AUTO also weighs d_in, d_out and the adapters a tile meets against M).  With y in fp32
+ * and an epilogue of anything, scale t keeps its fp32 bits in every mode (PREFILL carries it as three
+ * bf16 values instead of lora_linear's two; an epilogue of nothing is lora_linear there).  Also
  * LORA_ERR_VALUE for an unknown activation and LORA_ERR_ALIGN for the epilogue's operands. */
 lora_status_t lora_linear_act(const void *x, const void *W, const void *A, const void *B,
                               const float *scale, const int32_t *ranks, const int32_t *ids,
@@ -362,7 +364,8 @@ lora_status_t lora_linear_fp8w_profiled(const void *x, const void *W8, const flo
  * lora_linear_act; NULL: y = z).  x8: E4M3 codes [M][d_in]; x_scale fp32 [M]; W8: E4M3 codes
  * [d_out][d_in]; w_scale fp32 [d_out].  Sums are fp32; with y in bf16,
  * products below 2^-13 of the largest in their octet of k may be dropped from them (the 8-bit
- * matrix instruction's own adder), with y in fp32 none are.  A NaN code gives NaN in its row (x8) or
+ * matrix instruction's own adder) and scale t may enter as a pair of bf16 values (16 bits); with y in
+ * fp32 neither happens.  A NaN code gives NaN in its row (x8) or
  * column (W8).  A, B, scale, ranks, ids, y and segs as for lora_linear.  Any number of rows;
  * d_in a multiple of 16 (else LORA_ERR_SHAPE).  mode: LORA_MODE_AUTO (else LORA_ERR_MODE; the
  * launches follow from the sizes), LORA_MODE_CHECKED may be OR-ed in.  ws:

@@ -63,30 +63,34 @@ struct Frags {
 };
 
 template <class C>
-__device__ __forceinline__ void read_frags(Frags<C> &f, const uint4 *__restrict__ xs,
-                                           const uint4 *__restrict__ ws, int lane, int wm0,
-                                           int wn0) {
+__device__ __forceinline__ bf16x8_t read_a(const uint4 *__restrict__ xs, int kk, int i, int lane, int wm0) {
+    const int row = wm0 + 32 * i + (lane & 31);
+    const int lc = 2 * kk + (lane >> 5);
+    return *reinterpret_cast<const bf16x8_t *>(&xs[row * 4 + (lc ^ ((row >> 2) & 3))]);
+}
+template <class C>
+__device__ __forceinline__ bf16x8_t read_b(const uint4 *__restrict__ ws, int kk, int j, int lane, int wn0) {
     const lds_char_t *wsb = (const lds_char_t *)(ws);
     const int g = lane >> 4, li = lane & 15;
     const int rsw = (li >> 2) << 2;  // (row % 4) * 4 for every W row this lane names
+    const int col = wn0 + 32 * j + 16 * (g & 1) + 4 * (li & 3);
+    const int lc = col >> 3, half = (col >> 2) & 1;
+    const int r = 16 * kk + 8 * (g >> 1) + (li >> 2);
+    const lds_char_t *p = wsb + r * (C::BN * 2) + ((lc ^ rsw) << 4) + half * 8;
+    const bf16x4_t lo = __builtin_amdgcn_ds_read_tr16_b64_v4bf16((lds_bf16x4_t *)p);
+    const bf16x4_t hi = __builtin_amdgcn_ds_read_tr16_b64_v4bf16((lds_bf16x4_t *)(p + 4 * C::BN * 2));
+    return __builtin_shufflevector(lo, hi, 0, 1, 2, 3, 4, 5, 6, 7);
+}
+template <class C>
+__device__ __forceinline__ void read_frags(Frags<C> &f, const uint4 *__restrict__ xs,
+                                           const uint4 *__restrict__ ws, int lane, int wm0,
+                                           int wn0) {
 #pragma unroll
     for (int kk = 0; kk < 2; ++kk) {
 #pragma unroll
-        for (int i = 0; i < C::TM; ++i) {
-            const int row = wm0 + 32 * i + (lane & 31);
-            const int lc = 2 * kk + (lane >> 5);
-            f.a[kk][i] = *reinterpret_cast<const bf16x8_t *>(&xs[row * 4 + (lc ^ ((row >> 2) & 3))]);
-        }
+        for (int i = 0; i < C::TM; ++i) f.a[kk][i] = read_a<C>(xs, kk, i, lane, wm0);
 #pragma unroll
-        for (int j = 0; j < C::TN; ++j) {
-            const int col = wn0 + 32 * j + 16 * (g & 1) + 4 * (li & 3);
-            const int lc = col >> 3, half = (col >> 2) & 1;
-            const int r = 16 * kk + 8 * (g >> 1) + (li >> 2);
-            const lds_char_t *p = wsb + r * (C::BN * 2) + ((lc ^ rsw) << 4) + half * 8;
-            const bf16x4_t lo = __builtin_amdgcn_ds_read_tr16_b64_v4bf16((lds_bf16x4_t *)p);
-            const bf16x4_t hi = __builtin_amdgcn_ds_read_tr16_b64_v4bf16((lds_bf16x4_t *)(p + 4 * C::BN * 2));
-            f.b[kk][j] = __builtin_shufflevector(lo, hi, 0, 1, 2, 3, 4, 5, 6, 7);
-        }
+        for (int j = 0; j < C::TN; ++j) f.b[kk][j] = read_b<C>(ws, kk, j, lane, wn0);
     }
 }
 
@@ -192,22 +196,38 @@ __device__ __forceinline__ void fill_runs(RowTable<C> &t, int lane) {
     }
 }
 
-// One bf16 step of the delta: T (xs) holds every row's own, so rows outside lo <= row < hi (tile
-// rows) are taken as zeros.  BY_ROW: and the products are added to the rows inside alone, so that
-// 0 x infinity and 0 x NaN reach no other row.
-template <class C, bool BY_ROW>
+// T's third part (EXACT) of a rank chunk: 16 k of every tile row, in the second half of a W slot
+// (whose first half holds a step's 16 rows of B).  Chunk c of row r lies at c ^ ((r / 8) % 2), so that
+// 16 rows of one chunk meet all banks once.
+template <class C>
+__device__ __forceinline__ uint4 *t3_of(uint4 *ws) {
+    static_assert(kBK / 2 * C::WCH >= 2 * C::BM, "T's third part fits half a W slot");
+    return ws + kBK / 2 * C::WCH;
+}
+__device__ __forceinline__ int t3_at(int row, int c) { return 2 * row + (c ^ ((row >> 3) & 1)); }
+
+// One bf16 step of the delta (T's parts, 16 k each, times the same 16 rows of B): T (xs, t3) holds every
+// row's own, so rows outside lo <= row < hi (tile rows) are taken as zeros.  BY_ROW: and the products
+// are added to the rows inside alone, so that 0 x infinity and 0 x NaN reach no other row.
+template <class C, bool BY_ROW, bool EXACT>
 __device__ __forceinline__ void mfma_run(f32x16_t (&acc)[C::TM][C::TN], const uint4 *__restrict__ xs,
-                                         const uint4 *__restrict__ ws, int lane, int wm0, int wn0,
+                                         const uint4 *t3, const uint4 *ws, int lane, int wm0, int wn0,
                                          int lo, int hi) {
-    Frags<C> f;
-    read_frags<C>(f, xs, ws, lane, wm0, wn0);
+    constexpr int PARTS = EXACT ? 3 : 2;
+    bf16x8_t b[C::TN];
+#pragma unroll
+    for (int j = 0; j < C::TN; ++j) b[j] = read_b<C>(ws, 0, j, lane, wn0);
 #pragma unroll
     for (int i = 0; i < C::TM; ++i) {
         const int r0 = wm0 + 32 * i, row = r0 + (lane & 31);
         if (hi <= r0 || lo >= r0 + 32) continue;  // uniform: a block without a row of the run
+        bf16x8_t a[PARTS];
 #pragma unroll
-        for (int kk = 0; kk < 2; ++kk)
-            if (row < lo || row >= hi) f.a[kk][i] = __builtin_bit_cast(bf16x8_t, make_uint4(0, 0, 0, 0));
+        for (int kk = 0; kk < 2; ++kk) a[kk] = read_a<C>(xs, kk, i, lane, wm0);
+        if constexpr (EXACT) a[2] = *reinterpret_cast<const bf16x8_t *>(&t3[t3_at(row, lane >> 5)]);
+#pragma unroll
+        for (int kk = 0; kk < PARTS; ++kk)
+            if (row < lo || row >= hi) a[kk] = __builtin_bit_cast(bf16x8_t, make_uint4(0, 0, 0, 0));
 #pragma unroll
         for (int j = 0; j < C::TN; ++j) {
             if constexpr (BY_ROW) {
@@ -215,8 +235,8 @@ __device__ __forceinline__ void mfma_run(f32x16_t (&acc)[C::TM][C::TN], const ui
 #pragma unroll
                 for (int v = 0; v < 16; ++v) p[v] = 0.0f;
 #pragma unroll
-                for (int kk = 0; kk < 2; ++kk)
-                    p = __builtin_amdgcn_mfma_f32_32x32x16_bf16(f.a[kk][i], f.b[kk][j], p, 0, 0, 0);
+                for (int kk = 0; kk < PARTS; ++kk)
+                    p = __builtin_amdgcn_mfma_f32_32x32x16_bf16(a[kk], b[j], p, 0, 0, 0);
 #pragma unroll
                 for (int v = 0; v < 16; ++v) {
                     const int rv = r0 + (v / 4) * 8 + (lane >> 5) * 4 + (v % 4);
@@ -224,8 +244,8 @@ __device__ __forceinline__ void mfma_run(f32x16_t (&acc)[C::TM][C::TN], const ui
                 }
             } else {
 #pragma unroll
-                for (int kk = 0; kk < 2; ++kk)
-                    acc[i][j] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(f.a[kk][i], f.b[kk][j], acc[i][j], 0, 0, 0);
+                for (int kk = 0; kk < PARTS; ++kk)
+                    acc[i][j] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(a[kk], b[j], acc[i][j], 0, 0, 0);
             }
         }
     }
@@ -234,20 +254,23 @@ __device__ __forceinline__ void mfma_run(f32x16_t (&acc)[C::TM][C::TN], const ui
 // T = scale_a * t of the tile's rows, every row with its own adapter: rank chunk q (16 columns) in
 // slot q's x layout, as a pair of bf16 values per element -- k slots 0..15 the value rounded to
 // bf16, slots 16..31 the remainder (exact in fp32) rounded to bf16.  The pair carries scale * t to
-// about 16 significant bits, so the delta is not rounded to bf16 precision before it is added.
-template <class C>
-__device__ __forceinline__ void stage_t(uint4 *const (&xs)[4], const LoraEpilogue &ep,
-                                        const RowTable<C> &rows, int M, int tid) {
+// about 16 significant bits, so the delta is not rounded to bf16 precision before it is added.  EXACT
+// (fp32 y): what the pair leaves, again rounded to bf16, in W slot q's second half: the three carry
+// all 24 bits.
+template <class C, bool EXACT>
+__device__ __forceinline__ void stage_t(uint4 *const (&xs)[4], uint4 *const (&ws)[4],
+                                        const LoraEpilogue &ep, const RowTable<C> &rows, int M, int tid) {
     constexpr int kHalf = kBK / 2;
     const int RM = ep.r_max;
 #pragma unroll 1
     for (int q = 0; q * kHalf < RM; ++q) {
         uint4 *const X = q == 0 ? xs[0] : q == 1 ? xs[1] : q == 2 ? xs[2] : xs[3];
+        uint4 *const T3 = t3_of<C>(q == 0 ? ws[0] : q == 1 ? ws[1] : q == 2 ? ws[2] : ws[3]);
 #pragma unroll 2
         for (int c = tid; c < C::BM * 4; c += C::NT) {
             const int row = c >> 2, lc = c & 3;
             const int j = q * kHalf + (lc & 1) * 8;
-            uint4 v = make_uint4(0, 0, 0, 0);
+            uint4 v = make_uint4(0, 0, 0, 0), v3 = v;
             if (rows.id[row] >= 0 && j < RM) {
                 // t[m, j .. j+7]: the shrink's chunk sums added in chunk order, four chunks'
                 // loads in flight at a time
@@ -282,14 +305,21 @@ __device__ __forceinline__ void stage_t(uint4 *const (&xs)[4], const LoraEpilogu
                 }
                 v = make_uint4(pack_bf16x2(f[0], f[1]), pack_bf16x2(f[2], f[3]),
                                pack_bf16x2(f[4], f[5]), pack_bf16x2(f[6], f[7]));
+                if (EXACT && lc >= 2) {
+#pragma unroll
+                    for (int e = 0; e < 8; ++e) f[e] -= __uint_as_float(f32_to_bf16_rne(f[e]) << 16);
+                    v3 = make_uint4(pack_bf16x2(f[0], f[1]), pack_bf16x2(f[2], f[3]),
+                                    pack_bf16x2(f[4], f[5]), pack_bf16x2(f[6], f[7]));
+                }
             }
             X[row * 4 + (lc ^ ((row >> 2) & 3))] = v;
+            if (EXACT && lc >= 2) T3[t3_at(row, lc & 1)] = v3;
         }
     }
 }
 
 // acc += T B_a for every run of one adapter among the tile's rows, in steps of 16 rank columns:
-// B_a's 16 rank rows twice (for T's two halves) in a W slot.  Four steps share their two barriers and
+// B_a's 16 rank rows (for each of T's parts) in the first half of a W slot.  Four steps share their two barriers and
 // have their loads in flight together, a batch ahead of their use (two more batches ahead changed
 // nothing).  Waves, and 32-row blocks, without a row of a run skip its step.
 //
@@ -297,7 +327,7 @@ __device__ __forceinline__ void stage_t(uint4 *const (&xs)[4], const LoraEpilogu
 // infinity or a NaN spoils its own rows alone, such values are staged as zeros here, and a second
 // pass (ODD, only when there were any) stages them alone and adds their products by rows.  Returns
 // whether there were any.
-template <class C, bool ODD>
+template <class C, bool ODD, bool EXACT>
 __device__ __forceinline__ bool add_lora_steps(f32x16_t (&acc)[C::TM][C::TN], uint4 *const (&xs)[4],
                                                uint4 *const (&ws)[4], const LoraEpilogue &ep,
                                                const RowTable<C> &rows, int M, int N, int n0,
@@ -354,7 +384,7 @@ __device__ __forceinline__ bool add_lora_steps(f32x16_t (&acc)[C::TM][C::TN], ui
     bool odd = false;
     runs_of(0);
     load(0);
-    if constexpr (!ODD) stage_t<C>(xs, ep, rows, M, tid);  // (the first batch's barrier covers T too)
+    if constexpr (!ODD) stage_t<C, EXACT>(xs, ws, ep, rows, M, tid);  // (the first batch's barrier covers T too)
 #pragma unroll 1
     for (int T0 = 0; T0 < n_steps; T0 += 4) {
         if (ODD || T0 > 0) lds_barrier();  // every wave is done with the W slots
@@ -369,9 +399,7 @@ __device__ __forceinline__ bool add_lora_steps(f32x16_t (&acc)[C::TM][C::TN], ui
                 odd |= m != 0;
                 d[e] &= ODD ? m : ~m;
             }
-            const uint4 v = make_uint4(d[0], d[1], d[2], d[3]);
-            ws[u][br * C::WCH + (bc ^ ((br & 3) << 2))] = v;
-            ws[u][(br + kHalf) * C::WCH + (bc ^ ((br & 3) << 2))] = v;
+            ws[u][br * C::WCH + (bc ^ ((br & 3) << 2))] = make_uint4(d[0], d[1], d[2], d[3]);
         }
         lds_barrier();
         const int rows_of = span, of = adapter;  // this batch's
@@ -383,7 +411,8 @@ __device__ __forceinline__ bool add_lora_steps(f32x16_t (&acc)[C::TM][C::TN], ui
             const int lo = SIDES ? span_k & 0xFFFF : span_k;
             const int hi = SIDES ? span_k >> 16 : __builtin_amdgcn_readlane(rows_of, k + 1);
             if (__builtin_amdgcn_readlane(of, k) < 0 || hi <= wm0 || lo >= wm0 + C::WTM) continue;  // uniform
-            mfma_run<C, ODD>(acc, slot(chunk_of(T0, u), xs), slot(u, ws), lane, wm0, wn0, lo, hi);
+            const int q = chunk_of(T0, u);
+            mfma_run<C, ODD, EXACT>(acc, slot(q, xs), t3_of<C>(slot(q, ws)), slot(u, ws), lane, wm0, wn0, lo, hi);
         }
     }
     return __syncthreads_or(odd);
@@ -395,14 +424,14 @@ __device__ __forceinline__ bool add_lora_steps(f32x16_t (&acc)[C::TM][C::TN], ui
 // 206, 205, 216, 258 (17 runs per tile in the last; the kernel alone 298 before T was staged once
 // for every row and B loaded ahead); 4096 x 4096 x 4096 bf16 143, 142, 148, 161; 1300 x 1024 x 4096
 // bf16 40, 41, 44, 57.
-template <class C>
+template <class C, bool EXACT>
 __device__ __forceinline__ void add_lora_runs(f32x16_t (&acc)[C::TM][C::TN], uint4 *const (&xs)[4],
                                               uint4 *const (&ws)[4], const LoraEpilogue &ep,
                                               const RowTable<C> &rows, int M, int N, int n0, int tid,
                                               int lane, int wm0, int wn0) {
     lds_barrier();
-    if (add_lora_steps<C, false>(acc, xs, ws, ep, rows, M, N, n0, tid, lane, wm0, wn0))
-        add_lora_steps<C, true>(acc, xs, ws, ep, rows, M, N, n0, tid, lane, wm0, wn0);
+    if (add_lora_steps<C, false, EXACT>(acc, xs, ws, ep, rows, M, N, n0, tid, lane, wm0, wn0))
+        add_lora_steps<C, true, EXACT>(acc, xs, ws, ep, rows, M, N, n0, tid, lane, wm0, wn0);
 }
 
 // Stores a wave's WTM x WTN block of the tile (first position row0 + wm0, first column c0) with

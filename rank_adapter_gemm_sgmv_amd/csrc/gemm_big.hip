@@ -123,7 +123,8 @@ __device__ __forceinline__ void fill_stage(uint4 *xs, uint4 *ws, const uint16_t 
 }
 
 // O32: DMA sources as 32-bit byte offsets (x and W each below 4 GiB).
-// EPI: the epilogue of epilogue.h follows the delta, before the only rounding.
+// EPI: the epilogue of epilogue.h follows the delta, before the only rounding; with fp32 y the delta
+// then carries all 24 bits of scale t (lora_linear's carries 16).
 template <class C, bool SEGROWS, bool LORA, bool YF32, bool O32, bool EPI>
 __global__ __launch_bounds__(C::NT, C::BM == 256 && C::BN == 128 ? 1 : 2) void gemm_big_kernel(const uint16_t *__restrict__ x,
                                                             const uint16_t *__restrict__ W,
@@ -234,7 +235,7 @@ __global__ __launch_bounds__(C::NT, C::BM == 256 && C::BN == 128 ? 1 : 2) void g
 
     if constexpr (LORA) {
         uint4 *const xs[4] = {X0, X1, X2, X3}, *const ws[4] = {W0, W1, W2, W3};
-        add_lora_runs<C>(acc, xs, ws, ep, rows, M, N, n0, tid, lane, wm0, wn0);
+        add_lora_runs<C, YF32 && EPI>(acc, xs, ws, ep, rows, M, N, n0, tid, lane, wm0, wn0);
     }
 
     // store: accumulator element v of a 32 x 32 block is row (v/4)*8 + (lane/32)*4 + v%4,
@@ -634,6 +635,8 @@ hipError_t launch_gemm_big(const uint16_t *x, const uint16_t *W, int M, int K, i
                            bool y_f32, Seg seg, const LoraEpilogue *lora, hipStream_t s,
                            const Epilogue *epi) {
     if (epi && !lora) return hipErrorInvalidValue;
+    // an epilogue of nothing stores what lora_linear does
+    if (epi && !epi->bias && !epi->mul && !epi->residual && epi->act == LORA_ACT_NONE) epi = nullptr;
     const bool wide = wide_tiles(M, N);
     if (lora) {
         if (wide) return launch_big_cfg<Big<256, 256, 2, 4>, true, true>(x, W, M, K, N, y, y_f32, seg, lora, s, epi);

@@ -283,7 +283,7 @@ __global__ __launch_bounds__(C::NT, 2) void gemm_fp8_kernel(
         // (a stage's slot holds two of the bf16 steps')
         uint4 *const xs[4] = {X0, X0 + C::XSLOT, X1, X1 + C::XSLOT};
         uint4 *const ws[4] = {W0, W0 + C::WSLOT, W1, W1 + C::WSLOT};
-        add_lora_runs<C>(acc, xs, ws, ep, rows, M, N, n0, tid, lane, wm0, wn0);
+        add_lora_runs<C, WIDE>(acc, xs, ws, ep, rows, M, N, n0, tid, lane, wm0, wn0);
         lds_barrier();
         // two waves per slot with eight waves, one with four
         constexpr int H = C::NW / 4;
