@@ -206,14 +206,46 @@ __device__ __forceinline__ uint4 *t3_of(uint4 *ws) {
 }
 __device__ __forceinline__ int t3_at(int row, int c) { return 2 * row + (c ^ ((row >> 3) & 1)); }
 
+// 8 bf16 values -> -1, 0 or 1 by their sign, a NaN kept
+__device__ __forceinline__ bf16x8_t signs8(bf16x8_t v) {
+    const uint4 u = __builtin_bit_cast(uint4, v);
+    uint32_t d[4] = {u.x, u.y, u.z, u.w};
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+        uint32_t o = 0;
+#pragma unroll
+        for (int s = 0; s < 32; s += 16) {
+            const uint32_t h = (d[e] >> s) & 0xFFFFu, m = h & 0x7FFFu;
+            o |= (m == 0 ? 0u : m > 0x7F80u ? h : (h & 0x8000u) | 0x3F80u) << s;
+        }
+        d[e] = o;
+    }
+    return __builtin_bit_cast(bf16x8_t, make_uint4(d[0], d[1], d[2], d[3]));
+}
+
+// Two bf16 values: infinities and NaN alone, others zeros (ODD), or the others alone, an infinity
+// as 1 of its sign.
+template <bool ODD>
+__device__ __forceinline__ uint32_t odd_bf16x2(uint32_t d) {
+    uint32_t o = 0;
+#pragma unroll
+    for (int s = 0; s < 32; s += 16) {
+        const uint32_t h = (d >> s) & 0xFFFFu, m = h & 0x7FFFu;
+        o |= (ODD ? (m >= 0x7F80u ? h : 0u)
+                  : m < 0x7F80u ? h : m == 0x7F80u ? (h & 0x8000u) | 0x3F80u : 0u) << s;
+    }
+    return o;
+}
+
 // One bf16 step of the delta (T's parts, 16 k each, times the same 16 rows of B): T (xs, t3) holds every
-// row's own, so rows outside lo <= row < hi (tile rows) are taken as zeros.  BY_ROW: and the products
-// are added to the rows inside alone, so that 0 x infinity and 0 x NaN reach no other row.
+// row's own, so rows outside lo <= row < hi (tile rows) are taken as zeros.  BY_ROW (the pass over
+// infinities and NaN): T is its sign alone, and the products are added to the rows inside alone, so
+// that 0 x infinity and 0 x NaN reach no other row.
 template <class C, bool BY_ROW, bool EXACT>
 __device__ __forceinline__ void mfma_run(f32x16_t (&acc)[C::TM][C::TN], const uint4 *__restrict__ xs,
                                          const uint4 *t3, const uint4 *ws, int lane, int wm0, int wn0,
                                          int lo, int hi) {
-    constexpr int PARTS = EXACT ? 3 : 2;
+    constexpr int PARTS = BY_ROW ? 1 : EXACT ? 3 : 2;
     bf16x8_t b[C::TN];
 #pragma unroll
     for (int j = 0; j < C::TN; ++j) b[j] = read_b<C>(ws, 0, j, lane, wn0);
@@ -223,8 +255,9 @@ __device__ __forceinline__ void mfma_run(f32x16_t (&acc)[C::TM][C::TN], const ui
         if (hi <= r0 || lo >= r0 + 32) continue;  // uniform: a block without a row of the run
         bf16x8_t a[PARTS];
 #pragma unroll
-        for (int kk = 0; kk < 2; ++kk) a[kk] = read_a<C>(xs, kk, i, lane, wm0);
-        if constexpr (EXACT) a[2] = *reinterpret_cast<const bf16x8_t *>(&t3[t3_at(row, lane >> 5)]);
+        for (int kk = 0; kk < min(PARTS, 2); ++kk) a[kk] = read_a<C>(xs, kk, i, lane, wm0);
+        if constexpr (BY_ROW) a[0] = signs8(a[0]);
+        if constexpr (PARTS == 3) a[2] = *reinterpret_cast<const bf16x8_t *>(&t3[t3_at(row, lane >> 5)]);
 #pragma unroll
         for (int kk = 0; kk < PARTS; ++kk)
             if (row < lo || row >= hi) a[kk] = __builtin_bit_cast(bf16x8_t, make_uint4(0, 0, 0, 0));
@@ -249,6 +282,23 @@ __device__ __forceinline__ void mfma_run(f32x16_t (&acc)[C::TM][C::TN], const ui
             }
         }
     }
+}
+
+// f's leading bf16 part: rounded to nearest, but a finite f stays finite (the largest ones are cut off
+// instead).  What it leaves of f: nothing of an infinity or a NaN.
+__device__ __forceinline__ uint32_t bf16_part(float f) {
+    const uint32_t h = f32_to_bf16_rne(f);
+    return (h & 0x7FFFu) == 0x7F80u ? __float_as_uint(f) >> 16 : h;
+}
+__device__ __forceinline__ float bf16_rest(float f) {
+    const uint32_t h = bf16_part(f);
+    return (h & 0x7F80u) == 0x7F80u ? 0.0f : f - __uint_as_float(h << 16);
+}
+__device__ __forceinline__ uint4 bf16_parts8(const float (&f)[8]) {
+    uint32_t w[4];
+#pragma unroll
+    for (int e = 0; e < 4; ++e) w[e] = bf16_part(f[2 * e]) | (bf16_part(f[2 * e + 1]) << 16);
+    return make_uint4(w[0], w[1], w[2], w[3]);
 }
 
 // T = scale_a * t of the tile's rows, every row with its own adapter: rank chunk q (16 columns) in
@@ -301,15 +351,13 @@ __device__ __forceinline__ void stage_t(uint4 *const (&xs)[4], uint4 *const (&ws
                 for (int e = 0; e < 8; ++e) f[e] = s * t[e];
                 if (lc >= 2) {  // the remainder after rounding to bf16
 #pragma unroll
-                    for (int e = 0; e < 8; ++e) f[e] -= __uint_as_float(f32_to_bf16_rne(f[e]) << 16);
+                    for (int e = 0; e < 8; ++e) f[e] = bf16_rest(f[e]);
                 }
-                v = make_uint4(pack_bf16x2(f[0], f[1]), pack_bf16x2(f[2], f[3]),
-                               pack_bf16x2(f[4], f[5]), pack_bf16x2(f[6], f[7]));
+                v = bf16_parts8(f);
                 if (EXACT && lc >= 2) {
 #pragma unroll
-                    for (int e = 0; e < 8; ++e) f[e] -= __uint_as_float(f32_to_bf16_rne(f[e]) << 16);
-                    v3 = make_uint4(pack_bf16x2(f[0], f[1]), pack_bf16x2(f[2], f[3]),
-                                    pack_bf16x2(f[4], f[5]), pack_bf16x2(f[6], f[7]));
+                    for (int e = 0; e < 8; ++e) f[e] = bf16_rest(f[e]);
+                    v3 = bf16_parts8(f);
                 }
             }
             X[row * 4 + (lc ^ ((row >> 2) & 3))] = v;
@@ -324,9 +372,10 @@ __device__ __forceinline__ void stage_t(uint4 *const (&xs)[4], uint4 *const (&ws
 // nothing).  Waves, and 32-row blocks, without a row of a run skip its step.
 //
 // A row outside a run still meets the run's B, times zero.  So that an adapter whose B holds an
-// infinity or a NaN spoils its own rows alone, such values are staged as zeros here, and a second
-// pass (ODD, only when there were any) stages them alone and adds their products by rows.  Returns
-// whether there were any.
+// infinity or a NaN spoils its own rows alone, a second pass (ODD, only when there are any) stages
+// them alone, against the sign of T, and adds their products by rows: T of several parts, whose
+// signs may differ, would make NaN of an infinite product.  Here such an infinity stands as 1 of its
+// sign (an infinite T keeps its own) and a NaN as 0.  Returns whether there were any.
 template <class C, bool ODD, bool EXACT>
 __device__ __forceinline__ bool add_lora_steps(f32x16_t (&acc)[C::TM][C::TN], uint4 *const (&xs)[4],
                                                uint4 *const (&ws)[4], const LoraEpilogue &ep,
@@ -391,13 +440,14 @@ __device__ __forceinline__ bool add_lora_steps(f32x16_t (&acc)[C::TM][C::TN], ui
 #pragma unroll
         for (int u = 0; u < 4; ++u) {
             uint32_t d[4] = {bv[u].x, bv[u].y, bv[u].z, bv[u].w};
+            // an exponent of all ones, plus one, carries into its half's sign bit
+            uint32_t ones = 0;
 #pragma unroll
-            for (int e = 0; e < 4; ++e) {
-                // the halves whose exponent is all ones
-                const uint32_t m = ((d[e] & 0x7F80u) == 0x7F80u ? 0xFFFFu : 0u) |
-                                   ((d[e] & 0x7F800000u) == 0x7F800000u ? 0xFFFF0000u : 0u);
-                odd |= m != 0;
-                d[e] &= ODD ? m : ~m;
+            for (int e = 0; e < 4; ++e) ones |= (d[e] & 0x7F807F80u) + 0x00800080u;
+            if (ODD || (ones & 0x80008000u)) {
+                odd = true;
+#pragma unroll
+                for (int e = 0; e < 4; ++e) d[e] = odd_bf16x2<ODD>(d[e]);
             }
             ws[u][br * C::WCH + (bc ^ ((br & 3) << 2))] = make_uint4(d[0], d[1], d[2], d[3]);
         }

@@ -85,3 +85,61 @@ def test_fp32_delta_keeps_24_bits(op, shape):
     want = c.t64()[:, None] * c.B[i, c.j[i]].double()
     off = (c.run().double() - want).abs()
     assert (off <= 6 * 2.0 ** -23 * want.abs()).all(), float((off / (want.abs() + 1e-30)).max() * 2 ** 23)
+
+
+@pytest.mark.parametrize("op", ["act", "fp8"])
+@pytest.mark.parametrize("f32", [True, False])
+@pytest.mark.parametrize("shape", SHAPES, ids=lambda s: "x".join(map(str, s)))
+def test_infinite_b(op, f32, shape):
+    """An infinity in B gives its adapter's rows t times it: an infinity of the product's sign, NaN
+    for t = 0.  Other rows and columns keep their bits."""
+    log(f"infinite B {op} {shape} f32={f32}")
+    c = Case(op, *shape, f32=f32, seed=sum(shape))
+    M, K, N, r, n = c.dims
+    c.x.view(torch.uint8).view(M, -1)[M - 2] = 0  # t = 0
+    base = c.run()
+    i = c.ids.long().clamp_min(0)
+    c.B[0, c.j[0], 3] = float("inf")
+    c.B[n - 1, c.j[n - 1], N - 1] = float("-inf")
+    c.B[n // 2, c.j[n // 2], 8] = float("inf")
+    want = c.t64()[:, None] * c.B[i, c.j[i]].double()
+    want[c.ids < 0] = 0
+    got = c.run()
+    assert torch.equal(torch.isnan(got), torch.isnan(want))
+    inf = torch.isinf(want)
+    assert torch.equal(torch.isinf(got), inf) and torch.equal(got[inf].sign(), want[inf].sign().to(got.dtype))
+    fine = torch.isfinite(want)
+    assert inf.sum() > 0 and torch.equal(got[fine], base[fine])
+
+
+@pytest.mark.parametrize("op", ["act", "fp8"])
+@pytest.mark.parametrize("f32", [True, False])
+@pytest.mark.parametrize("shape", [(300, 128, 264, 9, 1), (4100, 128, 3080, 50, 1)], ids=lambda s: "x".join(map(str, s)))
+def test_ends_of_the_range(op, f32, shape):
+    """scale t between the largest bf16 and the largest fp32 value stays finite; an infinite one
+    gives an infinity of the product's sign, also times an infinite B, and NaN times 0."""
+    log(f"ends of the range {op} {shape} f32={f32}")
+    c = Case(op, *shape, f32=f32, seed=3)
+    M, K, N, r, n = c.dims
+    c.A.zero_()
+    c.A[:, 0] = float.fromhex("0x1.fep127")  # the largest bf16
+    c.A[:, 40] = float.fromhex("0x1.8p127")  # times 2^-8
+    c.A[1, 0] = c.A[1, 40] = float.fromhex("-0x1.8p127")
+    c.scale.fill_(1.0)
+    c.scale[1] = 2.0  # t beyond fp32
+    c.B[:] = (c.B.float() * 2.0 ** -20).bfloat16()
+    c.B[1, 0, 1] = float("inf")
+    c.B[1, 0, 2] = 0.0
+    got = c.run().double()
+    t = c.t64()
+    one = c.ids == 1
+    i = c.ids.long().clamp_min(0)
+    want = t[:, None] * c.B[i, 0].double()
+    rest = want[~one]
+    step = 6 * 2.0 ** -23 if f32 else 2.0 ** -8 + 2.0 ** -15
+    assert t.abs().max() > float.fromhex("0x1.ffp127")
+    assert ((got[~one] - rest).abs() <= step * rest.abs()).all()
+    assert torch.isnan(got[one][:, 2]).all()
+    keep = torch.arange(N, device="cuda") != 2
+    assert torch.isinf(got[one][:, keep]).all()
+    assert torch.equal(got[one][:, keep].sign(), want[one][:, keep].sign())
