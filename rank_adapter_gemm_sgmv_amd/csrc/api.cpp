@@ -101,7 +101,8 @@ void clear_stale_error() { (void)hipGetLastError(); }
 
 }  // namespace
 
-// Workspace of lora_linear, or (act) of lora_linear_act and every other call.
+// Workspace of lora_linear and lora_linear_multi per projection, or (act) of lora_linear_act and every
+// other call.
 size_t lora::linear_workspace_bytes(int32_t M, int32_t d_in, int32_t d_out, int32_t r_max, int32_t n_adapters, bool act) {
     if (check_common(M, r_max, n_adapters) != LORA_OK || !dim_ok(d_in) || !dim_ok(d_out)) return 0;
     if (M == 0) return 0;
@@ -833,7 +834,7 @@ extern "C" {
 size_t lora_workspace_bytes_multi(int32_t M, int32_t d_in, int32_t d_out, int32_t r_max,
                                   int32_t n_adapters, int32_t n_proj) {
     if (n_proj < 1 || n_proj > LORA_MAX_PROJ) return 0;
-    const size_t one = lora_workspace_bytes(M, d_in, d_out, r_max, n_adapters);
+    const size_t one = linear_workspace_bytes(M, d_in, d_out, r_max, n_adapters, false);
     if (one == 0) return 0;
     const size_t merged = multi_sk_bytes(M, d_in, d_out, r_max, n_adapters, n_proj);
     return merged > one ? merged : one;

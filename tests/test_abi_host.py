@@ -284,3 +284,17 @@ def test_linear_multi_rejects(over, code):
 
 def test_linear_multi_empty_batch_is_noop():
     _multi(M=0, x=None, ys=[None, None], ws=None)
+
+
+@pytest.mark.parametrize("M,d_in,d_out,need", [(1, 4104, 4096, 133120), (64, 1032, 520, 546048),
+                                               (200, 1160, 520, 1704448), (128, 200, 264, 17920),
+                                               (256, 4104, 1024, 13731840)])
+def test_multi_needs_no_more_than_its_projections(M, d_in, d_out, need):
+    """A d_in that is no multiple of 32: lora_linear_multi runs lora_linear's launches, which need
+    less than the lora_linear_act that lora_workspace_bytes() also covers."""
+    for n_proj in (1, 2, L.LORA_MAX_PROJ):
+        assert L.lora_workspace_bytes_multi(M, d_in, d_out, 16, 8, n_proj) == need
+    assert L.lora_workspace_bytes(M, d_in, d_out, 16, 8) >= need
+    with pytest.raises(L.LoraError) as e:
+        _multi(M=M, d_in=d_in, d_out=d_out, n_adapters=8, ws_bytes=need - 1)
+    assert e.value.status == 5

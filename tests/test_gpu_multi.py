@@ -217,3 +217,34 @@ def test_multi_random_shapes(i):
     out, singles = run_multi(base, projs, L.LORA_MODE_DECODE)
     for p, (y, ref) in enumerate(zip(out, refs(base, projs))):
         assert_parity(y, ref, f"case {i} projection {p} (group {g})")
+
+
+@pytest.mark.parametrize("case", [(611, 1, 4104, 4096, 8, 16, 2), (612, 64, 1032, 520, 8, 16, 3),
+                                  (613, 200, 1160, 520, 8, 16, 2), (614, 128, 200, 264, 8, 16, 2)],
+                         ids=lambda c: "x".join(map(str, c)))
+def test_multi_odd_d_in(case):
+    """d_in no multiple of 32: the workspace holds lora_linear's launches, the bits are its own, and
+    nothing behind the workspace is written."""
+    import torch
+
+    from rank_adapter_gemm_sgmv_amd import lora as L
+
+    seed, M, d_in, d_out, n, r, n_proj = case
+    log(f"multi odd d_in {case}")
+    base, projs = multi_case(*case)
+    nb = L.lora_workspace_bytes_multi(M, d_in, d_out, base.r_max, base.n_adapters, n_proj)
+    ws = torch.full((nb + 4096,), 0x5A, dtype=torch.uint8, device="cuda")
+    x = bf16_dev(projs[0].x)
+    Ws, As, Bs = ([bf16_dev(getattr(p, k)) for p in projs] for k in "WAB")
+    ids = torch.from_numpy(base.ids.astype(np.int32)).cuda()
+    ranks = torch.from_numpy(base.ranks.astype(np.int32)).cuda()
+    scale = torch.from_numpy(scale_of(base)).cuda()
+    ys = [torch.empty((M, d_out), dtype=torch.bfloat16, device="cuda") for _ in projs]
+    L.lora_linear_multi(x, Ws, As, Bs, scale, ranks, ids, M, d_in, d_out, base.r_max, base.n_adapters,
+                        None, ys, L.LORA_BF16, L.LORA_MODE_DECODE, ws, nb)
+    torch.cuda.synchronize()
+    assert (ws[nb:] == 0x5A).all()
+    _, singles = run_multi(base, projs, L.LORA_MODE_DECODE)
+    for y, s, want in zip(ys, singles, refs(base, projs)):
+        assert np.array_equal(bf16_host(y), s)
+        assert_parity(s, want, str(case))
