@@ -185,9 +185,11 @@ def _check(status: int, where: str) -> None:
 
 
 # torch.cuda.current_device() and current_stream() without their Python objects: a decode
-# call's launch costs the host about as much as these do
-_current_device = torch._C._cuda_getDevice
-_current_stream = torch._C._cuda_getCurrentRawStream
+# call's launch costs the host about as much as these do.  A torch without those names (one
+# built without GPU support, for host-only calls) has the public calls.
+_current_device = getattr(torch._C, "_cuda_getDevice", torch.cuda.current_device)
+_current_stream = getattr(torch._C, "_cuda_getCurrentRawStream",
+                          lambda device: torch.cuda.current_stream(device).cuda_stream)
 
 _BF16 = (torch.bfloat16,)
 _F32 = (torch.float32,)
