@@ -214,6 +214,14 @@ def _buf(a, name: str, n: int, dtypes) -> Optional[int]:
     return a.data_ptr()
 
 
+def _stream_here(stream) -> Optional[int]:
+    """_stream of a call whose buffers _buf checks: a torch stream must be of the current device
+    too (its kernels would run on the stream's device), else ValueError."""
+    if stream is not None and not isinstance(stream, int) and stream.device_index != _current_device():
+        raise ValueError(f"stream: one of the current device wanted, got one of device {stream.device_index}")
+    return _stream(stream)
+
+
 def _seg_struct(seg) -> lora_segments_t:
     if isinstance(seg, lora_segments_t):
         return seg
@@ -474,7 +482,7 @@ def lora_linear_act(x, W, A, B, scale, ranks, ids, M: int, d_in: int, d_out: int
         _buf(ids, "ids", M, _I32), M, d_in, d_out, r_max, n_adapters,
         None if segs is None else _seg_struct(segs), _epi_struct(epi, M, d_out, y_types),
         _buf(y, "y", M * d_out, y_types), y_dtype, mode, _buf(ws, "ws", ws_bytes, _U8), ws_bytes,
-        _stream(stream)), "lora_linear_act")
+        _stream_here(stream)), "lora_linear_act")
 
 
 def lora_fp8_workspace_bytes(M: int, d_in: int, d_out: int, r_max: int, n_adapters: int) -> int:
@@ -501,7 +509,7 @@ def lora_linear_fp8(x8, x_scale, W8, w_scale, A, B, scale, ranks, ids, M: int, d
         _buf(ids, "ids", M, _I32), M, d_in, d_out, r_max, n_adapters,
         None if segs is None else _seg_struct(segs), _epi_struct(epi, M, d_out, y_types),
         _buf(y, "y", M * d_out, y_types), y_dtype, mode, _buf(ws, "ws", ws_bytes, _U8), ws_bytes,
-        _stream(stream)), "lora_linear_fp8")
+        _stream_here(stream)), "lora_linear_fp8")
 
 
 def lora_rmsnorm(x, residual, weight, eps: float, M: int, d: int, sum, y, y8, y_scale,
@@ -513,7 +521,7 @@ def lora_rmsnorm(x, residual, weight, eps: float, M: int, d: int, sum, y, y8, y_
         _buf(x, "x", el, _BF16), _buf(residual, "residual", el, _BF16),
         _buf(weight, "weight", d, _BF16), eps, M, d, _buf(sum, "sum", el, _BF16),
         _buf(y, "y", el, _BF16), _buf(y8, "y8", el, _E4M3), _buf(y_scale, "y_scale", M, _F32),
-        _stream(stream)), "lora_rmsnorm")
+        _stream_here(stream)), "lora_rmsnorm")
 
 
 # ---- device buffers (torch is only the allocator here) ----------------------------------

@@ -52,3 +52,22 @@ def test_status_value():
 def test_rmsnorm_binding_rejects_tensors(bad):
     with pytest.raises(ValueError, match=next(iter(bad))):
         _norm(**bad)
+
+
+class _Stream:
+    """What the binding reads of a torch stream."""
+
+    def __init__(self, device_index):
+        self.device_index, self.cuda_stream = device_index, 0
+
+
+def test_binding_rejects_a_stream_of_another_device(monkeypatch):
+    monkeypatch.setattr(L, "_current_device", lambda: 0)
+    lora = dict(A=FAKE, B=FAKE, scale=FAKE, ranks=None, ids=FAKE, M=0, d_in=64, d_out=64, r_max=8, n_adapters=2,
+                segs=None, epi=None, y=FAKE, y_dtype=L.LORA_BF16, mode=L.LORA_MODE_AUTO, ws=FAKE, ws_bytes=0)
+    calls = [lambda s: _norm(M=0, stream=s), lambda s: L.lora_linear_act(x=FAKE, W=FAKE, **lora, stream=s),
+             lambda s: L.lora_linear_fp8(x8=FAKE, x_scale=FAKE, W8=FAKE, w_scale=FAKE, **lora, stream=s)]
+    for call in calls:
+        call(_Stream(0))
+        with pytest.raises(ValueError, match="stream"):
+            call(_Stream(1))
