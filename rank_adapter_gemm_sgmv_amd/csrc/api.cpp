@@ -326,11 +326,11 @@ lora_status_t check_tables(const int32_t *ids, int32_t M, const int32_t *ranks,
 }
 
 // The launch sequence of lora_linear (arguments already validated, M > 0).
-//   decode, M <= 128 and d_in % 32 == 0: one split-K GEMM over W and the batch's adapters'
-//            A laid side by side (the shrink as extra column tiles), then the ordered
-//            reduction that adds scale_a t B_a (no segment-building launch: adapters are
-//            numbered by id or grouped in LDS; segs is not needed)
-//   decode, 128 < M <= 256 and d_in % 32 == 0: the split-K GEMM with build_segments in one
+//   decode, M <= 128 and d_in % 32 == 0 (with an epilogue % 8): one split-K GEMM over W and
+//            the batch's adapters' A laid side by side (the shrink as extra column tiles), then
+//            the ordered reduction that adds scale_a t B_a (no segment-building launch: adapters
+//            are numbered by id, or one slot per row; segs is not needed)
+//   decode, 128 < M <= 256 and d_in as above: the split-K GEMM with build_segments in one
 //            extra workgroup, shrink (chunk sums), the ordered reduction with the expand
 //   decode, 256 < M <= 1024, d_in % 128 == 0 and few 256 x 256 tiles: build_segments,
 //            shrink (chunk sums), the stream-K GEMM, one pass adding its partial tiles, t

@@ -201,7 +201,7 @@ struct LoraEpilogue {
     int pstride;           // padded pool: rank rows per adapter (<= r_max, the bucket)
 };
 
-// y = x W (+ LoRA epilogue when lora != nullptr).  `prefill` selects the 256x256 tiling
+// y = x W (+ LoRA epilogue when lora != nullptr).  `prefill` selects the large tilings (wide_tiles)
 // and segment-ordered rows; otherwise a decode tiling, which may split K: then the partial
 // sums go to ws_partial and *ksplit_out != 1: > 1 split-K slices (launch_splitk_reduce must
 // follow), or -1 stream-K partial tiles (launch_sk_reduce_lora must follow).
@@ -283,7 +283,8 @@ struct SegBuild {
 };
 
 // Decode batches up to this many rows take the fused path (x W and x A_i as tiles of one
-// split-K launch) when d_in % 32 == 0: beyond it the adapter tiles (up to one slot per row)
+// split-K launch) where the split-K GEMM serves their d_in (decode_gemm_supported: multiples of 32;
+// decode_act_supported: of 8; decode_fp8_supported: of 16): beyond it the adapter tiles (up to one slot per row)
 // cost more than the segment-path shrink.
 constexpr int kDecodeMaxRows = 128;
 // The split-K decode GEMM + LoRA reduction serve batches up to this many rows (beyond

@@ -390,7 +390,7 @@ __device__ __forceinline__ void f8_tile(uint4 *lds, const typename C::X *__restr
     const int m0 = tm * C::BM, n0 = tn * kBN;
     const int ks0 = split * k_per_split;
     const int ks1 = min(K, ks0 + k_per_split);
-    const int nst = (ks1 - ks0) / kBKW;        // 16-k steps (K % 32 == 0)
+    const int nst = (ks1 - ks0) / kBKW;        // 16-k steps (K % 16 == 0)
     const int nsg = (nst + 7) >> 3;             // 128-k stages
     const int klast = ks0 + (nst - 1) * kBKW;   // first k of the last step
 

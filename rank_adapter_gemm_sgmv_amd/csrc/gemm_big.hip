@@ -28,7 +28,7 @@
 //    four rows of one read hit distinct banks.
 //  * Prefill rows are taken in segment order (positions of perm), so a tile holds a few long
 //    runs of one adapter.  After the K loop, every run adds s_a * t[rows, :] B_a[:, cols]
-//    as extra 32-deep MFMA steps (the K-extension [x | s t] [W ; B_a]) before the only store.
+//    as extra MFMA steps (the K-extension [x | s t] [W ; B_a], big_tiles.h) before the only store.
 //  * Tiles are handed to XCDs in compact blocks (workgroup b runs on XCD b % 8), so the
 //    x and W panels a tile group shares are read once into that XCD's L2.
 #include <type_traits>
@@ -126,7 +126,7 @@ __device__ __forceinline__ void fill_stage(uint4 *xs, uint4 *ws, const uint16_t 
 // EPI: the epilogue of epilogue.h follows the delta, before the only rounding; with fp32 y the delta
 // then carries all 24 bits of scale t (lora_linear's carries 16).
 template <class C, bool SEGROWS, bool LORA, bool YF32, bool O32, bool EPI>
-__global__ __launch_bounds__(C::NT, C::BM == 256 && C::BN == 128 ? 1 : 2) void gemm_big_kernel(const uint16_t *__restrict__ x,
+__global__ __launch_bounds__(C::NT, 2) void gemm_big_kernel(const uint16_t *__restrict__ x,
                                                             const uint16_t *__restrict__ W,
                                                             int M, int K, int N,
                                                             void *y, int n_tm, int n_tn,
