@@ -342,9 +342,8 @@ lora_status_t check_tables(const int32_t *ids, int32_t M, const int32_t *ranks,
 // otherwise" then ends in one pass that adds the split-K slices, t from the chunk sums, the
 // expand and the epilogue, or, where K is not split, takes the prefill sequence.
 // A rank-compact pool (roff != nullptr, lora_linear_compact) takes the same sequences; a padded
-// pool whose r_max is not a rank bucket (8, 16, 32, 64) too, except that its decode batches of
-// at most 128 rows take the second one (the first lays adapters side by side at row stride
-// r_max = the bucket).
+// pool whose r_max is not a multiple of 8 too, except that its decode batches of at most 128
+// rows take the second one (the first reads an adapter's k rows in 16-byte pieces).
 hipError_t run_linear(const void *x, const void *W, const void *A, const void *B,
                       const float *scale, const int32_t *ranks, const int32_t *roff,
                       int32_t pool_rows, const int32_t *ids, int32_t M, int32_t d_in,
