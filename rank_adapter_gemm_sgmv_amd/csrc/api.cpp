@@ -362,10 +362,10 @@ hipError_t run_linear(const void *x, const void *W, const void *A, const void *B
     // the chip but writes and adds partial sums in proportion to the tiles.  In plain slices,
     // where stream-K does not apply, it also reads its operands once per small tile: a K above
     // 4096 then no longer speaks for it, and with many tiles against it.  us for split K and prefill,
-    // d_out 4096: rank 16 of 4 adapters 300 x 512 27.7 and 24.0, 300 x 11008 73.3 and 97.0, 1000 x
-    // 2048 60.5 and 41.6, 1000 x 11008 123 and 121; rank 32 of 256 300 x 512 36.3 and 106, 768 x 2048
-    // 61.9 and 86.5, 1000 x 2048 71.3 and 84.4; in slices, d_out 2760, rank 16 of 4, 1300 x 11008
-    // 215 and 133, rank 32 of 256 248 and 192.
+    // d_out 4096: rank 16 of 4 adapters 300 x 512 26.3 and 22.6, 300 x 11008 70.3 and 91.2, 1000 x
+    // 2048 56.7 and 38.3, 1000 x 11008 121 and 117; rank 32 of 256 300 x 512 34.3 and 90.7, 768 x 2048
+    // 61.9 and 80.7, 1000 x 2048 70.0 and 74.9; in slices, d_out 2760, rank 16 of 4, 1300 x 11008
+    // 198 and 128, rank 32 of 256 251 and 187.
     if (mode == LORA_MODE_AUTO && splits && !dec) {
         const long tiles = (long)((M + 127) / 128) * ((d_out + 127) / 128);
         const long runs = 128L * (n_adapters < M ? n_adapters : M) / (M > 128 ? M : 128);

@@ -471,9 +471,9 @@ __device__ __forceinline__ bool add_lora_steps(f32x16_t (&acc)[C::TM][C::TN], ui
 // The LoRA delta of one output tile (rows in segment order), after its K loop: acc += scale_a
 // t[rows, :] B_a[:, columns].  xs, ws: four slot pairs, free once every wave has passed the first
 // barrier here.  Whole call, 1, 8, 64 and 256 adapters of rank 16, us: 4096 x 4096 x 11008 8-bit rows
-// 206, 205, 216, 258 (17 runs per tile in the last; the kernel alone 298 before T was staged once
-// for every row and B loaded ahead); 4096 x 4096 x 4096 bf16 143, 142, 148, 161; 1300 x 1024 x 4096
-// bf16 40, 41, 44, 57.
+// 207, 209, 217, 251 (17 runs per tile in the last; the kernel alone 298 before T was staged once
+// for every row and B loaded ahead); 4096 x 4096 x 4096 bf16 145, 145, 150, 162; 1300 x 1024 x 4096
+// bf16 39, 39, 42, 54.
 template <class C, bool EXACT>
 __device__ __forceinline__ void add_lora_runs(f32x16_t (&acc)[C::TM][C::TN], uint4 *const (&xs)[4],
                                               uint4 *const (&ws)[4], const LoraEpilogue &ep,

@@ -621,8 +621,9 @@ hipError_t launch_big_cfg(const uint16_t *x, const uint16_t *W, int M, int K, in
 // 256 x 256 tiles (one workgroup per CU) or 128 x 128 (two): the large ones where they fill most
 // of a round of 256 CUs, or several rounds; the small ones below that and where a short second
 // round would follow.  d_in 4096, rank 16, bias and residual, large and small tiles: 208 of the
-// large ones 119 and 151 us, 256 of them 135 and 163; 288 of them 219 and 194.  fp8 (lora_linear_fp8)
-// 75.6 and 84.6, 82.8 and 92.6; 138 and 122.  Tiles of 256 x 128, one per CU, lost everywhere: 192 of
+// large ones 127 and 160 us, 256 of them 146 and 174; 288 of them 231 and 208.  fp8 (lora_linear_fp8)
+// 78.6 and 91.6, 87.5 and 102; 142 and 130.  (At 320, past the border, the small ones still lead: 236 and
+// 216, fp8 142 and 133.)  Tiles of 256 x 128, one per CU, lost everywhere: 192 of
 // them 225 us for 124 with small tiles, 256 122 for 92, 320 218 for 121.
 bool wide_tiles(int M, int N) {
     const long t = (long)((M + 255) / 256) * ((N + 255) / 256);

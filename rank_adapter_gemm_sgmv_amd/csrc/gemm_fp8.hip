@@ -342,10 +342,10 @@ constexpr int kMinK = 2 * kK8;
 // costs the slices' way through memory and a launch (the more, the more tiles); whole tiles cost a
 // walk through K at a workgroup or two per CU and, behind it, one through the adapter runs of the
 // tile's rows, at every rank chunk (one slice is worth it for the latter alone).  us split and whole,
-// d_out 4096: rank 16 of 4 adapters 520 x 1040 39.8 and 28.9, 520 x 4112 48.5 and 52.2, 520 x 11008
-// 62.0 and 79.2, 1024 x 4112 61.5 and 56.1; rank 64 of 64 260 x 512 37.0 and 96.9, 1024 x 512 53.5 and 54.5,
-// 1024 x 4112 85.5 and 98.9; d_out 264, rank 16 of 4: 260 x 2048 28.6 and 28.3, 260 x 4112 30.0
-// and 36.7.  Rounds: 768 x 11008 x 4096 97 us in two slices, 118 in three (a second, short
+// d_out 4096: rank 16 of 4 adapters 520 x 1024 36.5 and 26.1, 520 x 4112 46.0 and 49.4, 520 x 11008
+// 62.2 and 77.3, 1024 x 4112 59.6 and 54.2; rank 64 of 64 260 x 512 37.0 and 89.1, 1024 x 512 58.9 and 50.3
+// (the rule takes the slices), 1024 x 4112 90.4 and 95.2; d_out 264, rank 16 of 4: 260 x 2048 27.1 and
+// 27.2, 260 x 4112 28.7 and 36.2.  Rounds: 768 x 11008 x 4096 97 us in two slices, 118 in three (a second, short
 // round).  Above 256 tiles the slices cost more than they bring: 1280 x 4096 x 4096 80 -> 88 us,
 // 1536 x 11008 144 -> 164 with three.
 Fp8Plan fp8_plan(int M, int K, int N, bool y_f32, int r_max, int n_adapters) {
