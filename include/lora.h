@@ -69,7 +69,7 @@ extern "C" {
 #define LORA_MAX_ROWS (1 << 22)  /* rows per call */
 #define LORA_MAX_PROJ 4          /* projections per lora_linear_multi call */
 
-/* The three enums below are passed as int.  Any int value may reach the library (an
+/* The enums below are passed as int.  Any int value may reach the library (an
  * unknown status or dtype, a mode with LORA_MODE_CHECKED OR-ed in), so in C++ they are given
  * int as their fixed underlying type, which makes every int value a valid value of the type
  * and keeps the C representation. */
@@ -402,6 +402,68 @@ lora_status_t lora_linear_fp8(const void *x8, const float *x_scale, const void *
 lora_status_t lora_rmsnorm(const void *x, const void *residual, const void *weight, float eps,
                            int32_t M, int32_t d, void *sum, void *y, void *y8, float *y_scale,
                            void *stream);
+
+/* The same with 8-bit integers for the 8-bit output, the x operand of lora_linear_int8, and such
+ * integers of rows as they are (an output or down projection's input, which no norm stands before):
+ *     p = fp32(h * weight)                          (lora_quant_int8: p = x)
+ *     y8[m] = rint(127 p / max|p|)                  (exactly, ties to even; in [-127, 127])
+ *     y_scale[m] = max(max|n|, 2^-60) / 127         (lora_quant_int8: n = x)
+ * Below the floor of 2^-60 the integers are rint(n / y_scale); where some h * weight is beyond fp32's
+ * range, p is fp32(n).  y8: int8 [M][d], 16-byte aligned.  A row that has no scale (as for lora_rmsnorm)
+ * gets NaN for it and zeros for integers, so that what is multiplied from it is NaN.  lora_rmsnorm_int8's
+ * arguments, other outputs, limits and errors are lora_rmsnorm's, but y8 and y_scale are required
+ * (LORA_ERR_NULL) and y alone may be NULL; lora_quant_int8's are its x, M, d, y8 and y_scale. */
+lora_status_t lora_rmsnorm_int8(const void *x, const void *residual, const void *weight, float eps,
+                                int32_t M, int32_t d, void *sum, void *y, void *y8, float *y_scale,
+                                void *stream);
+lora_status_t lora_quant_int8(const void *x, int32_t M, int32_t d, void *y8, float *y_scale,
+                              void *stream);
+
+/* Rotary positions of a batch's queries and keys, between their projections and attention (the pages
+ * take the projections alone and define no such call).  Pair i of a head's first rot_dim elements,
+ * (i, i + rot_dim / 2) or, interleaved, (2 i, 2 i + 1), turns by its row's angle:
+ *     (a, b) -> factor * (a cos t - b sin t, a sin t + b cos t),
+ *     t = 2 pi positions[m] freqs[i]                (the turns and their fraction in 64 bits)
+ * Elements past rot_dim are copied.  inverse = 1 turns by -t: the gradient of q and k from that of
+ * q_out and k_out.  q: [M][q_heads][head_dim], rows q_stride elements apart (a slice of a row of q, k
+ * and v, say); k alike, or k_heads = 0 (k and k_out are then not read); q_out and k_out with strides of
+ * their own, in q's type (dtype: LORA_BF16 or LORA_F32; fp32 arithmetic, one rounding).  q_out may be
+ * q itself with the same stride, and k_out k; outputs overlap nothing otherwise.  Between the rows'
+ * heads nothing is read or written.  positions: int32 [M], any value.  freqs: double [rot_dim / 2],
+ * turns per position, as lora_rope_freqs writes them (device memory).
+ * Limits: 1 <= q_heads, k_heads <= LORA_ROPE_MAX_HEADS; head_dim a multiple of 8 up to
+ * LORA_ROPE_MAX_DIM; rot_dim even, 2 .. head_dim; strides multiples of 8 from heads * head_dim to
+ * LORA_ROPE_MAX_STRIDE (else LORA_ERR_SHAPE).  q, k, q_out, k_out 16-byte aligned, freqs 8.
+ * Errors: LORA_ERR_SHAPE (also: in place with two strides), _DTYPE, _MODE (layout), _VALUE (factor not
+ * finite or not positive, inverse not 0 or 1), _NULL, _ALIGN, _HIP. */
+typedef enum LORA_ENUM_INT { LORA_ROPE_HALF = 0, LORA_ROPE_INTERLEAVED = 1 } lora_rope_t;
+#define LORA_ROPE_MAX_HEADS 1024
+#define LORA_ROPE_MAX_DIM 1024
+#define LORA_ROPE_MAX_STRIDE (1 << 28)
+lora_status_t lora_rope(const void *q, const void *k, const int32_t *positions, const double *freqs,
+                        int32_t M, int32_t q_heads, int32_t k_heads, int32_t head_dim, int32_t rot_dim,
+                        int64_t q_stride, int64_t k_stride, lora_rope_t layout, float factor,
+                        int32_t inverse, void *q_out, int64_t q_out_stride, void *k_out,
+                        int64_t k_out_stride, lora_dtype_t dtype, void *stream);
+
+/* lora_rope's table, on the host: freqs[i] = base^(-2 i / rot_dim) / (2 pi) turns per position for pair
+ * i < rot_dim / 2, scaled for contexts `stretch` times as long as the `length` positions of training:
+ *   LINEAR  freqs / stretch (positions interpolated)
+ *   NTK     base * stretch^(rot_dim / (rot_dim - 2)) instead of base
+ *   YARN    pair i keeps the share g = clamp((length freqs[i] - 1) / 31, 0, 1) of its pace, the turns it
+ *           makes in `length` positions between 1 and 32, and is interpolated for the rest:
+ *           freqs[i] (g + (1 - g) / stretch); *factor = 0.1 ln(stretch) + 1
+ * *factor is 1 otherwise.  freqs (rot_dim / 2 doubles) and factor are HOST pointers.
+ * Errors: LORA_ERR_SHAPE (rot_dim odd or outside 2 .. LORA_ROPE_MAX_DIM), _MODE, _NULL, _VALUE (base not
+ * above 1, stretch below 1, YARN's length not positive, or any not finite). */
+typedef enum LORA_ENUM_INT {
+    LORA_ROPE_PLAIN = 0,
+    LORA_ROPE_LINEAR = 1,
+    LORA_ROPE_NTK = 2,
+    LORA_ROPE_YARN = 3
+} lora_rope_scaling_t;
+lora_status_t lora_rope_freqs(int32_t rot_dim, double base, lora_rope_scaling_t scaling, double stretch,
+                              double length, double *freqs, float *factor);
 
 /* For callers that cannot allocate (code under HIP graph capture, serving loops or
  * harnesses that forbid hipMalloc): lora_linear without a caller workspace.  The call uses a

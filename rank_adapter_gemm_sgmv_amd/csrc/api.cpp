@@ -2,6 +2,7 @@
 // workspace layout and the launch sequence of each call.  No call allocates device memory or
 // keeps state; only the checked mode and the measurement aids synchronise.
 #include <float.h>
+#include <math.h>
 #include <stdint.h>
 #include <string.h>
 
@@ -1218,21 +1219,104 @@ lora_status_t lora_linear_fp8(const void *x8, const float *x_scale, const void *
                               y_dtype == LORA_F32, ws, (hipStream_t)stream));
 }
 
-lora_status_t lora_rmsnorm(const void *x, const void *residual, const void *weight, float eps,
-                           int32_t M, int32_t d, void *sum, void *y, void *y8, float *y_scale,
-                           void *stream) {
+}  // extern "C"
+
+namespace {
+
+// lora_rmsnorm, lora_rmsnorm_int8 and (no norm) lora_quant_int8.
+lora_status_t rows_call(const void *x, const void *residual, const void *weight, float eps, int32_t M,
+                        int32_t d, void *sum, void *y, void *y8, float *y_scale, bool int8, bool norm,
+                        void *stream) {
     if (M < 0 || M > LORA_MAX_ROWS || !dim_ok(d)) return LORA_ERR_SHAPE;
     if (!(eps >= 1e-30f) || eps > FLT_MAX) return LORA_ERR_VALUE;
     if (M == 0) return LORA_OK;
-    if (!x || (!y && !y8) || !y8 != !y_scale) return LORA_ERR_NULL;
+    if (!x || (!y && !y8) || !y8 != !y_scale || (int8 && !y8)) return LORA_ERR_NULL;
     for (const void *p : {x, residual, weight, (const void *)sum, (const void *)y, (const void *)y8})
         if (!aligned(p, 16)) return LORA_ERR_ALIGN;
     if (!aligned(y_scale, 4)) return LORA_ERR_ALIGN;
     clear_stale_error();
     const NormArgs a{static_cast<const uint16_t *>(x), static_cast<const uint16_t *>(residual),
                      static_cast<const uint16_t *>(weight), static_cast<uint16_t *>(sum),
-                     static_cast<uint16_t *>(y), static_cast<uint8_t *>(y8), y_scale, eps, M, d};
+                     static_cast<uint16_t *>(y), static_cast<uint8_t *>(y8), y_scale, eps, M, d, int8, norm};
     return hip_status(launch_rmsnorm(a, (hipStream_t)stream));
+}
+
+}  // namespace
+
+extern "C" {
+
+lora_status_t lora_rmsnorm(const void *x, const void *residual, const void *weight, float eps,
+                           int32_t M, int32_t d, void *sum, void *y, void *y8, float *y_scale,
+                           void *stream) {
+    return rows_call(x, residual, weight, eps, M, d, sum, y, y8, y_scale, false, true, stream);
+}
+
+lora_status_t lora_rmsnorm_int8(const void *x, const void *residual, const void *weight, float eps,
+                                int32_t M, int32_t d, void *sum, void *y, void *y8, float *y_scale,
+                                void *stream) {
+    return rows_call(x, residual, weight, eps, M, d, sum, y, y8, y_scale, true, true, stream);
+}
+
+lora_status_t lora_quant_int8(const void *x, int32_t M, int32_t d, void *y8, float *y_scale,
+                              void *stream) {
+    return rows_call(x, nullptr, nullptr, 1.0f, M, d, nullptr, nullptr, y8, y_scale, true, false, stream);
+}
+
+lora_status_t lora_rope(const void *q, const void *k, const int32_t *positions, const double *freqs,
+                        int32_t M, int32_t q_heads, int32_t k_heads, int32_t head_dim, int32_t rot_dim,
+                        int64_t q_stride, int64_t k_stride, lora_rope_t layout, float factor,
+                        int32_t inverse, void *q_out, int64_t q_out_stride, void *k_out,
+                        int64_t k_out_stride, lora_dtype_t dtype, void *stream) {
+    if (M < 0 || M > LORA_MAX_ROWS || q_heads < 1 || q_heads > LORA_ROPE_MAX_HEADS || k_heads < 0 ||
+        k_heads > LORA_ROPE_MAX_HEADS || head_dim < 8 || head_dim > LORA_ROPE_MAX_DIM ||
+        head_dim % 8 != 0 || rot_dim < 2 || rot_dim > head_dim || rot_dim % 2 != 0)
+        return LORA_ERR_SHAPE;
+    if (dtype != LORA_BF16 && dtype != LORA_F32) return LORA_ERR_DTYPE;
+    if (layout != LORA_ROPE_HALF && layout != LORA_ROPE_INTERLEAVED) return LORA_ERR_MODE;
+    if (!(factor > 0.0f) || factor > FLT_MAX || inverse < 0 || inverse > 1) return LORA_ERR_VALUE;
+    const RopeArgs a{{q, q_out, q_stride, q_out_stride, q_heads}, {k, k_out, k_stride, k_out_stride, k_heads},
+                     positions, freqs, factor, M, head_dim, rot_dim, layout == LORA_ROPE_INTERLEAVED,
+                     inverse != 0, dtype == LORA_F32};
+    for (const RopeHeads *t : {&a.q, &a.k}) {
+        const int64_t row = (int64_t)t->heads * head_dim;
+        if (t->heads == 0) continue;
+        for (const int64_t s : {t->x_stride, t->y_stride})
+            if (s < row || s > LORA_ROPE_MAX_STRIDE || s % 8 != 0) return LORA_ERR_SHAPE;
+        if (t->x == t->y && t->x_stride != t->y_stride && t->x != nullptr) return LORA_ERR_SHAPE;
+    }
+    if (M == 0) return LORA_OK;
+    if (!q || !q_out || !positions || !freqs || (k_heads > 0 && (!k || !k_out))) return LORA_ERR_NULL;
+    if (!aligned(q, 16) || !aligned(q_out, 16) || !aligned(positions, 4) || !aligned(freqs, 8) ||
+        (k_heads > 0 && (!aligned(k, 16) || !aligned(k_out, 16))))
+        return LORA_ERR_ALIGN;
+    clear_stale_error();
+    return hip_status(launch_rope(a, (hipStream_t)stream));
+}
+
+lora_status_t lora_rope_freqs(int32_t rot_dim, double base, lora_rope_scaling_t scaling, double stretch,
+                              double length, double *freqs, float *factor) {
+    if (rot_dim < 2 || rot_dim > LORA_ROPE_MAX_DIM || rot_dim % 2 != 0) return LORA_ERR_SHAPE;
+    if (scaling < LORA_ROPE_PLAIN || scaling > LORA_ROPE_YARN) return LORA_ERR_MODE;
+    if (!freqs || !factor) return LORA_ERR_NULL;
+    if (!(base > 1.0) || !(base <= DBL_MAX)) return LORA_ERR_VALUE;
+    if (scaling != LORA_ROPE_PLAIN && (!(stretch >= 1.0) || !(stretch <= DBL_MAX))) return LORA_ERR_VALUE;
+    if (scaling == LORA_ROPE_YARN && (!(length > 0.0) || !(length <= DBL_MAX))) return LORA_ERR_VALUE;
+    constexpr double kTurn = 6.283185307179586476925286766559;  // 2 pi
+    // the base whose slowest pair turns `stretch` times slower and whose fastest keeps its pace
+    if (scaling == LORA_ROPE_NTK) base *= pow(stretch, rot_dim > 2 ? rot_dim / (rot_dim - 2.0) : 2.0);
+    for (int32_t i = 0; i < rot_dim / 2; ++i) {
+        double f = pow(base, -2.0 * i / rot_dim) / kTurn;
+        if (scaling == LORA_ROPE_LINEAR) f /= stretch;
+        if (scaling == LORA_ROPE_YARN) {
+            // kept: the share of a pair that turns often enough within `length` to stay as it is
+            double kept = (length * f - 1.0) / 31.0;
+            kept = kept < 0.0 ? 0.0 : kept > 1.0 ? 1.0 : kept;
+            f = f / stretch * (1.0 - kept) + f * kept;
+        }
+        freqs[i] = f;
+    }
+    *factor = scaling == LORA_ROPE_YARN ? (float)(0.1 * log(stretch) + 1.0) : 1.0f;
+    return LORA_OK;
 }
 
 const char *lora_status_string(lora_status_t status) {

@@ -408,7 +408,7 @@ hipError_t launch_gemm_fp8(const Fp8Gemm &g, const Fp8Plan &p, void *y, bool y_f
                            const LoraEpilogue &ep, const Epilogue &epi, float *partial,
                            hipStream_t s);
 
-// ---- residual addition + RMS norm (csrc/norm.hip) -------------------------------------------
+// ---- residual addition + RMS norm, rows in 8 bits (csrc/norm.hip) ----------------------------
 struct NormArgs {
     const uint16_t *x, *residual, *weight;  // [M][d], [M][d] or nullptr, [d] or nullptr (= 1)
     uint16_t *sum, *y;                      // [M][d] or nullptr
@@ -416,8 +416,27 @@ struct NormArgs {
     float *y_scale;                         // [M], with y8
     float eps;
     int M, d;
+    bool int8, norm;                        // 8-bit integers, of n or (no norm) of x itself; else E4M3 codes of n
 };
 hipError_t launch_rmsnorm(const NormArgs &a, hipStream_t s);
+
+// ---- rotary positions (csrc/rope.hip) ---------------------------------------------------------
+// One of the two tensors: heads of head_dim elements, rows `stride` elements apart.
+struct RopeHeads {
+    const void *x;
+    void *y;            // x itself (in place, the same stride) or apart from it
+    int64_t x_stride, y_stride;
+    int heads;
+};
+struct RopeArgs {
+    RopeHeads q, k;            // k.heads may be 0
+    const int32_t *positions;  // [M]
+    const double *freqs;       // [rot_dim / 2], turns per position
+    float factor;
+    int M, head_dim, rot_dim;
+    bool interleaved, inverse, f32;
+};
+hipError_t launch_rope(const RopeArgs &a, hipStream_t s);
 
 // Records e as the error lora_last_hip_error() reports; LORA_ERR_HIP unless e is hipSuccess.
 lora_status_t hip_error_status(hipError_t e);

@@ -1,10 +1,12 @@
 // norm.hip -- what a serving program runs in front of every adapted projection: the residual
 // addition and the root-mean-square norm of a batch's rows, written in bf16, in 8 bits with a
-// scale per row (the x operand of lora_linear_fp8), or both, in one pass over the data.
+// scale per row (the x operand of lora_linear_fp8 or lora_linear_int8), or both, in one pass over
+// the data; and rows in 8-bit integers as they are (lora_quant_int8: no norm).
 //
 //   h = x[m] + residual[m]             (fp32; sum[m] = bf16(h))
 //   r = 1 / sqrt(mean(h^2) + eps)      n = h r w
 //   y[m] = bf16(n);   s = max(max|n|, 2^-60) / 448;   y8[m] = E4M3(n / s);   y_scale[m] = s
+//   8-bit integers: s = max(max|n|, 2^-60) / 127;   y8[m] = rint(127 p / max|p|), p = fp32(h w)
 //
 // Bound: HBM bytes for many rows, one round trip to memory for few.
 //  * A row is read once and stays in registers between its statistics and its output, as
@@ -22,7 +24,11 @@ namespace lora {
 
 namespace {
 
-constexpr float kTop8 = 448.0f;                      // the largest E4M3 value
+// What the rows' 8-bit output is: E4M3 codes, integers, or integers of x itself (no norm).
+enum Rows8 { kE4m3, kInt8, kInt8Plain };
+
+template <Rows8 Q>
+constexpr float kTop8 = Q == kE4m3 ? 448.0f : 127.0f;  // the largest value of an 8-bit code
 constexpr float kFloor8 = 0x1p-60f;                  // rows of zeros still get a normal scale
 constexpr float kShrink = 0x1p-80f;                  // rescales rows whose squares overflow
 
@@ -30,6 +36,24 @@ constexpr float kShrink = 0x1p-80f;                  // rescales rows whose squa
 __device__ __forceinline__ uint32_t pack_e4m3x4(float a, float b, float c, float d) {
     int v = __builtin_amdgcn_cvt_pk_fp8_f32(a, b, 0, false);
     return (uint32_t)__builtin_amdgcn_cvt_pk_fp8_f32(c, d, v, true);
+}
+
+// rint(127 p / top), ties to even, exactly.  q0 = p (127 / top) is off by at most 2^-16 of it, so only
+// quotients that close to a border (a few in ten thousand, and the ties that short significands
+// like bf16's make) take the exact remainder.  p is not above top; a NaN gives 0.
+__device__ __forceinline__ int int8_code(float p, float f, float top) {
+    const float q0 = p * f;
+    float k = rintf(q0);
+    if (fabsf(q0 - k) > 0.4995f) {
+        const double e = 127.0 * (double)p - (double)k * (double)top, half = 0.5 * (double)top;
+        const bool odd = ((int)k & 1) != 0;
+        if (e > half || (e == half && odd)) k += 1.0f;
+        if (e < -half || (e == -half && odd)) k -= 1.0f;
+    }
+    return k == k ? (int)k : 0;
+}
+__device__ __forceinline__ uint32_t pack_int8x4(int a, int b, int c, int d) {
+    return (uint32_t)(a & 255) | (uint32_t)(b & 255) << 8 | (uint32_t)(c & 255) << 16 | (uint32_t)d << 24;
 }
 
 __device__ __forceinline__ float wave_sum(float v) {
@@ -56,20 +80,24 @@ __device__ __forceinline__ void norm_h8(float h[8], uint4 x, uint4 res, bool has
     }
 }
 
-// Row statistics -> factors of the outputs: y = (h r) w, code = ((h q) w) f, scale s.
+// Row statistics -> factors of the outputs: y = (h r) w, code = ((h q) w) f, scale s.  Integers are
+// rint(127 (h q) w / top).
 struct NormFactors {
-    float r, q, f, s;
+    float r, q, f, s, top;
 };
 // top: max|h w|, or (nw: that overflowed) max|n| itself
+template <Rows8 Q>
 __device__ __forceinline__ NormFactors norm_factors(float r, float top, bool nw) {
     NormFactors o;
     const float q = nw ? 1.0f : r, mx = q * top;
     o.r = r;
     o.q = nw ? r : 1.0f;
-    o.s = fmaxf(mx, kFloor8) / kTop8;
+    o.s = fmaxf(mx, kFloor8) / kTop8<Q>;
     // (below the floor the codes are n / s with the floor's s; above it r cancels)
-    o.f = mx > kFloor8 ? kTop8 / top : q / o.s;
+    o.f = mx > kFloor8 ? kTop8<Q> / top : q / o.s;
+    o.top = mx > kFloor8 ? top : kFloor8 / q;
     // a row with an infinity (r = 0) or a NaN, in h or in h w, has no scale: all its codes are NaN
+    // (integers 0)
     if (!(mx < __builtin_inff()) || !(r > 0.0f)) o.s = o.f = __builtin_nanf("");
     return o;
 }
@@ -84,6 +112,7 @@ __device__ __forceinline__ void st_bf16x8(uint16_t *p, const float f[8]) {
                           cvt_bf16x2(f[6], f[7])));
 }
 
+template <Rows8 Q>
 __device__ __forceinline__ void norm_store8(const NormArgs &a, size_t at, const float h[8],
                                             uint4 w, const NormFactors &nf) {
     if (a.sum) st_bf16x8(a.sum + at, h);
@@ -96,9 +125,17 @@ __device__ __forceinline__ void norm_store8(const NormArgs &a, size_t at, const 
         st_bf16x8(a.y + at, n);
     }
     if (a.y8) {
+        u32x2_t v;
+        if constexpr (Q == kE4m3) {
 #pragma unroll
-        for (int e = 0; e < 8; ++e) n[e] = h[e] * nf.q * g[e] * nf.f;
-        const u32x2_t v = {pack_e4m3x4(n[0], n[1], n[2], n[3]), pack_e4m3x4(n[4], n[5], n[6], n[7])};
+            for (int e = 0; e < 8; ++e) n[e] = h[e] * nf.q * g[e] * nf.f;
+            v = {pack_e4m3x4(n[0], n[1], n[2], n[3]), pack_e4m3x4(n[4], n[5], n[6], n[7])};
+        } else {
+            int c[8];
+#pragma unroll
+            for (int e = 0; e < 8; ++e) c[e] = int8_code(h[e] * nf.q * g[e], nf.f, nf.top);
+            v = {pack_int8x4(c[0], c[1], c[2], c[3]), pack_int8x4(c[4], c[5], c[6], c[7])};
+        }
         __builtin_nontemporal_store(v, reinterpret_cast<u32x2_t *>(a.y8 + at));
     }
 }
@@ -126,7 +163,7 @@ __device__ __forceinline__ void row_reduce(float &ss, float &top, float (*red)[2
 }
 
 // WPR waves per row, VPL 16-byte pieces per lane: rows of at most 512 WPR VPL elements.
-template <int WPR, int VPL>
+template <Rows8 Q, int WPR, int VPL>
 __global__ __launch_bounds__(WPR > 4 ? WPR * 64 : 256) void rmsnorm_kernel(NormArgs a) {
     constexpr int NW = WPR > 4 ? WPR : 4;  // waves per block
     constexpr int RPB = NW / WPR;          // rows per block
@@ -166,7 +203,7 @@ __global__ __launch_bounds__(WPR > 4 ? WPR * 64 : 256) void rmsnorm_kernel(NormA
         }
     }
     row_reduce<WPR>(ss, top, red, wave);
-    const float ms = ss / (float)a.d + a.eps;
+    const float ms = Q == kInt8Plain ? 1.0f : ss / (float)a.d + a.eps;
     float r = 1.0f / sqrtf(ms);
     // Rows at the ends of the range go on: their branches are uniform in the row, so in the wave
     // (WPR == 1) or the block (its barriers).
@@ -181,7 +218,7 @@ __global__ __launch_bounds__(WPR > 4 ? WPR * 64 : 256) void rmsnorm_kernel(NormA
         row_reduce<WPR>(s2, t2, red2, wave);
         r = kShrink / sqrtf(s2 / (float)a.d + a.eps * kShrink * kShrink);
     }
-    const bool nw = !(top < __builtin_inff());
+    const bool nw = Q != kInt8Plain && !(top < __builtin_inff());
     if (nw) {  // some h w did: max|n| instead
         float s3 = 0.0f;
         top = 0.0f;
@@ -196,17 +233,18 @@ __global__ __launch_bounds__(WPR > 4 ? WPR * 64 : 256) void rmsnorm_kernel(NormA
         row_reduce<WPR>(s3, top, red3, wave);
     }
     if (!live) return;
-    const NormFactors nf = norm_factors(r, top, nw);
+    const NormFactors nf = norm_factors<Q>(r, top, nw);
 #pragma unroll
     for (int i = 0; i < VPL; ++i) {
         const int c = c0 + i * (WPR * 512);
-        if (c < a.d) norm_store8(a, base + c, h[i], wv[i], nf);
+        if (c < a.d) norm_store8<Q>(a, base + c, h[i], wv[i], nf);
     }
     if (a.y_scale && c0 == 0) a.y_scale[m] = nf.s;
 }
 
 // Rows too long for registers: one block of 16 waves per row, which it reads twice (the second
 // time mostly from L2).
+template <Rows8 Q>
 __global__ __launch_bounds__(1024) void rmsnorm_long_kernel(NormArgs a) {
     __shared__ float red[16][2], red2[16][2], red3[16][2];
     const int wave = threadIdx.x >> 6;
@@ -231,32 +269,32 @@ __global__ __launch_bounds__(1024) void rmsnorm_long_kernel(NormArgs a) {
     float ss, top, spare;
     stats(1.0f, 1.0f, ss, top);
     row_reduce<16>(ss, top, red, wave);
-    const float ms = ss / (float)a.d + a.eps;
+    const float ms = Q == kInt8Plain ? 1.0f : ss / (float)a.d + a.eps;
     float r = 1.0f / sqrtf(ms);
     if (!(ms < __builtin_inff())) {  // uniform in the block, as the next one
         stats(kShrink, 1.0f, ss, spare);
         row_reduce<16>(ss, spare, red2, wave);
         r = kShrink / sqrtf(ss / (float)a.d + a.eps * kShrink * kShrink);
     }
-    const bool nw = !(top < __builtin_inff());
+    const bool nw = Q != kInt8Plain && !(top < __builtin_inff());
     if (nw) {
         stats(1.0f, r, spare, top);
         row_reduce<16>(spare, top, red3, wave);
     }
-    const NormFactors nf = norm_factors(r, top, nw);
+    const NormFactors nf = norm_factors<Q>(r, top, nw);
     for (int c = threadIdx.x * 8; c < a.d; c += 8192) {
         float h[8];
         norm_h8(h, ld16(a.x + base + c), has_res ? ld16(a.residual + base + c) : zero, has_res);
-        norm_store8(a, base + c, h, a.weight ? ld16(a.weight + c) : one, nf);
+        norm_store8<Q>(a, base + c, h, a.weight ? ld16(a.weight + c) : one, nf);
     }
     if (a.y_scale && threadIdx.x == 0) a.y_scale[blockIdx.x] = nf.s;
 }
 
-template <int WPR, int VPL>
+template <Rows8 Q, int WPR, int VPL>
 void launch_one(const NormArgs &a, hipStream_t s) {
     constexpr int NW = WPR > 4 ? WPR : 4;
     constexpr int RPB = NW / WPR;
-    launch((rmsnorm_kernel<WPR, VPL>), dim3((unsigned)((a.M + RPB - 1) / RPB)), dim3(64 * NW), 0, s, a);
+    launch((rmsnorm_kernel<Q, WPR, VPL>), dim3((unsigned)((a.M + RPB - 1) / RPB)), dim3(64 * NW), 0, s, a);
 }
 
 }  // namespace
@@ -272,15 +310,16 @@ void launch_one(const NormArgs &a, hipStream_t s) {
 //   d 11008 8 x 3: 4.43 at 1 row, 75.9 at 4096;  16 x 2: 4.58, 92.1
 // so eight waves share a row wherever it has a piece for each of their lanes, and only rows of
 // 513-1024 elements go by the number of rows.
+template <Rows8 Q>
 static void launch_rows(const NormArgs &a, hipStream_t s) {
-    if (a.d <= 512) launch_one<1, 1>(a, s);
-    else if (a.d <= 1024 && a.M >= 1024) launch_one<1, 2>(a, s);
-    else if (a.d <= 2048) launch_one<4, 1>(a, s);
-    else if (a.d <= 4096) launch_one<8, 1>(a, s);
-    else if (a.d <= 8192) launch_one<8, 2>(a, s);
-    else if (a.d <= 12288) launch_one<8, 3>(a, s);
-    else if (a.d <= 16384) launch_one<16, 2>(a, s);
-    else launch(rmsnorm_long_kernel, dim3((unsigned)a.M), dim3(1024), 0, s, a);
+    if (a.d <= 512) launch_one<Q, 1, 1>(a, s);
+    else if (a.d <= 1024 && a.M >= 1024) launch_one<Q, 1, 2>(a, s);
+    else if (a.d <= 2048) launch_one<Q, 4, 1>(a, s);
+    else if (a.d <= 4096) launch_one<Q, 8, 1>(a, s);
+    else if (a.d <= 8192) launch_one<Q, 8, 2>(a, s);
+    else if (a.d <= 12288) launch_one<Q, 8, 3>(a, s);
+    else if (a.d <= 16384) launch_one<Q, 16, 2>(a, s);
+    else launch(rmsnorm_long_kernel<Q>, dim3((unsigned)a.M), dim3(1024), 0, s, a);
 }
 
 // A launch holds fewer than 2^32 threads: LORA_MAX_ROWS = 2^22 rows on blocks of 1024 are one too
@@ -299,7 +338,9 @@ hipError_t launch_rmsnorm(const NormArgs &a, hipStream_t s) {
             p.y8 = a.y8 + at;
             p.y_scale = a.y_scale + m;
         }
-        launch_rows(p, s);
+        if (!a.int8) launch_rows<kE4m3>(p, s);
+        else if (a.norm) launch_rows<kInt8>(p, s);
+        else launch_rows<kInt8Plain>(p, s);
     }
     return hipGetLastError();
 }

@@ -26,6 +26,10 @@ LORA_MOE_MAX_PAIRS = 8192
 
 LORA_BF16, LORA_F32 = 0, 1
 LORA_ACT_NONE, LORA_ACT_RELU, LORA_ACT_SILU, LORA_ACT_GELU, LORA_ACT_GELU_TANH = 0, 1, 2, 3, 4
+LORA_ROPE_HALF, LORA_ROPE_INTERLEAVED = 0, 1
+LORA_ROPE_PLAIN, LORA_ROPE_LINEAR, LORA_ROPE_NTK, LORA_ROPE_YARN = 0, 1, 2, 3
+LORA_ROPE_MAX_HEADS = LORA_ROPE_MAX_DIM = 1024
+LORA_ROPE_MAX_STRIDE = 1 << 28
 LORA_MODE_AUTO, LORA_MODE_DECODE, LORA_MODE_PREFILL = 0, 1, 2
 LORA_MODE_CHECKED = 0x100  # OR-ed into a mode: sync, check ids and adapter tables on the host
 
@@ -43,7 +47,8 @@ EXPORTS = ("lora_max_tiles", "lora_workspace_bytes", "lora_build_segments", "lor
            "lora_moe_workspace_bytes", "lora_moe_linear", "lora_moe_linear_profiled",
            "lora_workspace_bytes_multi", "lora_linear_multi", "lora_linear_multi_profiled",
            "lora_rmsnorm", "lora_linear_act", "lora_fp8_workspace_bytes",
-           "lora_linear_fp8", "lora_status_string", "lora_last_hip_error")
+           "lora_linear_fp8", "lora_rmsnorm_int8", "lora_quant_int8", "lora_rope", "lora_rope_freqs",
+           "lora_status_string", "lora_last_hip_error")
 
 
 class LoraError(RuntimeError):
@@ -145,6 +150,17 @@ def _load():
     lib.lora_linear_fp8.restype = ctypes.c_int
     lib.lora_rmsnorm.argtypes = [P, P, P, ctypes.c_float, I, I, P, P, P, P, P]
     lib.lora_rmsnorm.restype = ctypes.c_int
+    lib.lora_rmsnorm_int8.argtypes = lib.lora_rmsnorm.argtypes
+    lib.lora_rmsnorm_int8.restype = ctypes.c_int
+    lib.lora_quant_int8.argtypes = [P, I, I, P, P, P]
+    lib.lora_quant_int8.restype = ctypes.c_int
+    I64, D = ctypes.c_int64, ctypes.c_double
+    lib.lora_rope.argtypes = [P, P, P, P, I, I, I, I, I, I64, I64, ctypes.c_int, ctypes.c_float, I, P, I64,
+                              P, I64, ctypes.c_int, P]
+    lib.lora_rope.restype = ctypes.c_int
+    lib.lora_rope_freqs.argtypes = [I, D, ctypes.c_int, D, D, ctypes.POINTER(D),
+                                    ctypes.POINTER(ctypes.c_float)]
+    lib.lora_rope_freqs.restype = ctypes.c_int
     lib.lora_status_string.argtypes = [ctypes.c_int]
     lib.lora_status_string.restype = ctypes.c_char_p
     lib.lora_last_hip_error.argtypes = []
@@ -194,7 +210,9 @@ _current_stream = getattr(torch._C, "_cuda_getCurrentRawStream",
 _BF16 = (torch.bfloat16,)
 _F32 = (torch.float32,)
 _I32 = (torch.int32,)
+_F64 = (torch.float64,)
 _U8 = (torch.uint8,)
+_I8 = (torch.int8,)
 _E4M3 = (torch.float8_e4m3fn, torch.uint8)  # E4M3 codes, under either type
 
 
@@ -208,6 +226,28 @@ def _buf(a, name: str, n: int, dtypes) -> Optional[int]:
     if not a.is_contiguous() or a.numel() < n:
         raise ValueError(f"{name}: a contiguous tensor of {n} elements wanted, got {tuple(a.shape)}"
                          f" with strides {a.stride()}")
+    dev = a.get_device()
+    if dev < 0 or dev != _current_device():
+        raise ValueError(f"{name}: a tensor of the current device wanted, got one on {a.device}")
+    return a.data_ptr()
+
+
+def _rows(a, name: str, M: int, width: int, stride: int, dtypes) -> Optional[int]:
+    """_buf of M rows of `width` elements, `stride` apart: a tensor must hold each row's elements side
+    by side, from its first element on."""
+    if a is None or isinstance(a, int) or M <= 0:
+        return _ptr(a)
+    if a.dtype not in dtypes:
+        raise ValueError(f"{name}: {a.dtype} given, {dtypes[0]} wanted")
+    at = 1  # elements that the dimensions behind the first hold side by side
+    for n, s in zip(reversed(a.shape[1:]), reversed(a.stride()[1:])):
+        if n != 1 and s != at:
+            at = -1
+            break
+        at *= n
+    if a.dim() < 2 or a.shape[0] < M or at < width or (M > 1 and a.stride(0) != stride):
+        raise ValueError(f"{name}: {M} rows of {width} elements, {stride} apart, wanted, got"
+                         f" {tuple(a.shape)} with strides {a.stride()}")
     dev = a.get_device()
     if dev < 0 or dev != _current_device():
         raise ValueError(f"{name}: a tensor of the current device wanted, got one on {a.device}")
@@ -522,6 +562,52 @@ def lora_rmsnorm(x, residual, weight, eps: float, M: int, d: int, sum, y, y8, y_
         _buf(weight, "weight", d, _BF16), eps, M, d, _buf(sum, "sum", el, _BF16),
         _buf(y, "y", el, _BF16), _buf(y8, "y8", el, _E4M3), _buf(y_scale, "y_scale", M, _F32),
         _stream_here(stream)), "lora_rmsnorm")
+
+
+def lora_rmsnorm_int8(x, residual, weight, eps: float, M: int, d: int, sum, y, y8, y_scale,
+                      stream=None) -> None:
+    """lora_rmsnorm with 8-bit integers (int8) and their scale per row; sum and y may be None."""
+    el = M * d
+    _check(_lib.lora_rmsnorm_int8(
+        _buf(x, "x", el, _BF16), _buf(residual, "residual", el, _BF16),
+        _buf(weight, "weight", d, _BF16), eps, M, d, _buf(sum, "sum", el, _BF16),
+        _buf(y, "y", el, _BF16), _buf(y8, "y8", el, _I8), _buf(y_scale, "y_scale", M, _F32),
+        _stream_here(stream)), "lora_rmsnorm_int8")
+
+
+def lora_quant_int8(x, M: int, d: int, y8, y_scale, stream=None) -> None:
+    """M rows of d (bf16) as 8-bit integers y8 (int8) with a scale per row."""
+    el = M * d
+    _check(_lib.lora_quant_int8(_buf(x, "x", el, _BF16), M, d, _buf(y8, "y8", el, _I8),
+                                _buf(y_scale, "y_scale", M, _F32), _stream_here(stream)),
+           "lora_quant_int8")
+
+
+def lora_rope(q, k, positions, freqs, M: int, q_heads: int, k_heads: int, head_dim: int, rot_dim: int,
+              q_stride: int, k_stride: int, layout: int, factor: float, inverse: int, q_out,
+              q_out_stride: int, k_out, k_out_stride: int, dtype: int, stream=None) -> None:
+    """Rotary positions of q[M, q_heads, head_dim] and k (or None, k_heads = 0), whose rows are q_stride
+    and k_stride elements apart; freqs: lora_rope_freqs' table on the device (float64)."""
+    types = _F32 if dtype == LORA_F32 else _BF16
+    qw, kw = q_heads * head_dim, k_heads * head_dim
+    _check(_lib.lora_rope(
+        _rows(q, "q", M, qw, q_stride, types), _rows(k, "k", M, kw, k_stride, types),
+        _buf(positions, "positions", M, _I32), _buf(freqs, "freqs", rot_dim // 2, _F64), M, q_heads,
+        k_heads, head_dim, rot_dim, q_stride, k_stride, layout, factor, inverse,
+        _rows(q_out, "q_out", M, qw, q_out_stride, types), q_out_stride,
+        _rows(k_out, "k_out", M, kw, k_out_stride, types), k_out_stride, dtype, _stream_here(stream)),
+        "lora_rope")
+
+
+def lora_rope_freqs(rot_dim: int, base: float = 10000.0, scaling: int = LORA_ROPE_PLAIN,
+                    stretch: float = 1.0, length: float = 1.0, device="cuda"):
+    """(freqs, factor) for lora_rope: a float64 tensor of rot_dim / 2 turns per position on `device`, and
+    the factor of the turned values."""
+    table = (ctypes.c_double * max(rot_dim // 2, 1))()
+    factor = ctypes.c_float(0.0)
+    _check(_lib.lora_rope_freqs(rot_dim, base, scaling, stretch, length, table, ctypes.byref(factor)),
+           "lora_rope_freqs")
+    return torch.tensor(list(table), dtype=torch.float64, device=device), factor.value
 
 
 # ---- device buffers (torch is only the allocator here) ----------------------------------
