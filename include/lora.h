@@ -380,6 +380,26 @@ lora_status_t lora_linear_fp8(const void *x8, const float *x_scale, const void *
                               const lora_epilogue_t *epi, void *y, lora_dtype_t y_dtype,
                               lora_mode_t mode, void *ws, size_t ws_bytes, void *stream);
 
+/* The same on 8-bit integers: x as lora_rmsnorm_int8 or lora_quant_int8 writes it, the base in 8-bit
+ * integers with a scale per column, the adapters in bf16:
+ *     z = x_scale[m] * ( w_scale[c] sum_k x8[m, k] W8[c, k] + scale_i ((x8[m, :] A_i) B_i)[c] )
+ * (rows with id -1: the first sum alone), then epi.  x8: int8 [M][d_in]; W8: int8 [d_out][d_in], any
+ * values (-128 too).  The sum over k is exact in int32 (up to a split of K into at most 16 parts, which
+ * are rounded to fp32 and added there); for that d_in is at most LORA_INT8_MAX_D_IN (else
+ * LORA_ERR_SHAPE).  With y in bf16 scale t may enter as a pair of bf16 values (16 bits); with y in
+ * fp32 it does not.  Everything else is as for lora_linear_fp8.  ws: lora_int8_workspace_bytes() bytes of
+ * the same sizes. */
+#define LORA_INT8_MAX_D_IN ((1 << 17) - 16)
+size_t lora_int8_workspace_bytes(int32_t M, int32_t d_in, int32_t d_out, int32_t r_max,
+                                 int32_t n_adapters);
+lora_status_t lora_linear_int8(const void *x8, const float *x_scale, const void *W8,
+                               const float *w_scale, const void *A, const void *B,
+                               const float *scale, const int32_t *ranks, const int32_t *ids,
+                               int32_t M, int32_t d_in, int32_t d_out, int32_t r_max,
+                               int32_t n_adapters, const lora_segments_t *segs,
+                               const lora_epilogue_t *epi, void *y, lora_dtype_t y_dtype,
+                               lora_mode_t mode, void *ws, size_t ws_bytes, void *stream);
+
 /* The step in front of a projection in a serving loop (the pages take x as given and define no
  * such call): residual addition and root-mean-square norm of every row, written in bf16, as
  * 8-bit codes with one scale per row (the x operand of lora_linear_fp8), or both:

@@ -6,6 +6,7 @@
 #include <stdint.h>
 #include <string.h>
 
+#include <type_traits>
 #include <vector>
 
 #include "common.h"
@@ -582,7 +583,7 @@ lora_status_t check_fp8w(const void *x, const void *W8, const float *w_scale, co
 
 namespace {
 
-// lora_linear_fp8 (arguments already validated, M > 0):
+// lora_linear_fp8 and lora_linear_int8 (arguments already validated, M > 0):
 //   up to 128 rows, pool padded at a rank bucket: the split-K fp8 GEMM with the shrink as
 //            adapter tiles of the same launch, then the reduction (two launches, no segments)
 //   up to 192 rows: the split-K fp8 GEMM with build_segments in one extra workgroup, the shrink
@@ -593,7 +594,8 @@ namespace {
 // 4096 x 4104, rank 16, us per call of the three: 1 row 12.4, 15.8, 29.1; 64 rows 17.5, 18.4, 38.6;
 // 117 rows 20.8, 24.0, 40.7; 160 rows -, 31.2, 41.8; 256 rows -, 42.1, 44.7 (11008 x 4096 with 256
 // adapters: 69.6, 61.8).
-hipError_t run_fp8(const Fp8Gemm &g, const uint16_t *A, const uint16_t *B, const float *scale,
+template <class X>
+hipError_t run_fp8(const Gemm8<X> &g, const uint16_t *A, const uint16_t *B, const float *scale,
                    const int32_t *ranks, const int32_t *ids, int32_t r_max, int32_t n_adapters,
                    const lora_segments_t *segs, const Epilogue &epi, void *y, bool y_f32, void *ws,
                    hipStream_t s) {
@@ -1177,25 +1179,34 @@ lora_status_t lora_linear_act(const void *x, const void *W, const void *A, const
                                  nullptr, epi ? &e : nullptr));
 }
 
-size_t lora_fp8_workspace_bytes(int32_t M, int32_t d_in, int32_t d_out, int32_t r_max,
-                                int32_t n_adapters) {
-    if (check_common(M, r_max, n_adapters) != LORA_OK || !dim_ok(d_in) || !dim_ok(d_out) || d_in % 16 != 0)
-        return 0;
+}  // extern "C"
+
+namespace {
+
+// A d_in of the 8-bit layers; an integer sum of int8_t products up to 2^14 stays below 2^31 to the last.
+bool dim8_ok(int32_t d_in, bool ints) {
+    static_assert((int64_t)LORA_INT8_MAX_D_IN << 14 < (int64_t)1 << 31, "int32 sums");
+    return dim_ok(d_in) && d_in % 16 == 0 && (!ints || d_in <= LORA_INT8_MAX_D_IN);
+}
+
+size_t workspace8(int32_t M, int32_t d_in, int32_t d_out, int32_t r_max, int32_t n_adapters, bool ints) {
+    if (check_common(M, r_max, n_adapters) != LORA_OK || !dim8_ok(d_in, ints) || !dim_ok(d_out)) return 0;
     if (M == 0) return 0;
     return segments_bytes(M, n_adapters) + shrink_partial_bytes(M, d_in, r_max) +
            fp8_gemm_bytes(M, d_in, d_out, r_max, n_adapters);
 }
 
-lora_status_t lora_linear_fp8(const void *x8, const float *x_scale, const void *W8,
-                              const float *w_scale, const void *A, const void *B,
-                              const float *scale, const int32_t *ranks, const int32_t *ids,
-                              int32_t M, int32_t d_in, int32_t d_out, int32_t r_max,
-                              int32_t n_adapters, const lora_segments_t *segs,
-                              const lora_epilogue_t *epi, void *y, lora_dtype_t y_dtype,
-                              lora_mode_t mode, void *ws, size_t ws_bytes, void *stream) {
+// lora_linear_fp8 (X: uint8_t) and lora_linear_int8 (int8_t).
+template <class X>
+lora_status_t linear8(const void *x8, const float *x_scale, const void *W8, const float *w_scale,
+                      const void *A, const void *B, const float *scale, const int32_t *ranks,
+                      const int32_t *ids, int32_t M, int32_t d_in, int32_t d_out, int32_t r_max,
+                      int32_t n_adapters, const lora_segments_t *segs, const lora_epilogue_t *epi, void *y,
+                      lora_dtype_t y_dtype, lora_mode_t mode, void *ws, size_t ws_bytes, void *stream) {
+    constexpr bool kInts = std::is_same_v<X, int8_t>;
     lora_status_t st = check_common(M, r_max, n_adapters);
     if (st != LORA_OK) return st;
-    if (!dim_ok(d_in) || !dim_ok(d_out) || d_in % 16 != 0) return LORA_ERR_SHAPE;
+    if (!dim8_ok(d_in, kInts) || !dim_ok(d_out)) return LORA_ERR_SHAPE;
     if (y_dtype != LORA_BF16 && y_dtype != LORA_F32) return LORA_ERR_DTYPE;
     if ((mode & ~LORA_MODE_CHECKED) != LORA_MODE_AUTO) return LORA_ERR_MODE;
     if ((st = check_epilogue(epi)) != LORA_OK) return st;
@@ -1207,16 +1218,52 @@ lora_status_t lora_linear_fp8(const void *x8, const float *x_scale, const void *
         !aligned(ws, kAlign) || !aligned(x_scale, 4) || !aligned(w_scale, 4) || !aligned(scale, 4) ||
         !aligned(ids, 4) || (ranks && !aligned(ranks, 4)))
         return LORA_ERR_ALIGN;
-    if (ws_bytes < lora_fp8_workspace_bytes(M, d_in, d_out, r_max, n_adapters)) return LORA_ERR_WORKSPACE;
+    if (ws_bytes < workspace8(M, d_in, d_out, r_max, n_adapters, kInts)) return LORA_ERR_WORKSPACE;
     clear_stale_error();
     if ((mode & LORA_MODE_CHECKED) &&
         (st = check_tables(ids, M, ranks, nullptr, 0, r_max, n_adapters, (hipStream_t)stream)) != LORA_OK)
         return st;
-    return hip_status(run_fp8(Fp8Gemm{static_cast<const uint8_t *>(x8), static_cast<const uint8_t *>(W8),
-                                      w_scale, M, d_in, d_out},
+    return hip_status(run_fp8(Gemm8<X>{static_cast<const X *>(x8), static_cast<const X *>(W8), w_scale, M,
+                                       d_in, d_out},
                               static_cast<const uint16_t *>(A), static_cast<const uint16_t *>(B), scale,
                               ranks, ids, r_max, n_adapters, segs, to_epilogue(epi, x_scale), y,
                               y_dtype == LORA_F32, ws, (hipStream_t)stream));
+}
+
+}  // namespace
+
+extern "C" {
+
+size_t lora_fp8_workspace_bytes(int32_t M, int32_t d_in, int32_t d_out, int32_t r_max,
+                                int32_t n_adapters) {
+    return workspace8(M, d_in, d_out, r_max, n_adapters, false);
+}
+
+lora_status_t lora_linear_fp8(const void *x8, const float *x_scale, const void *W8,
+                              const float *w_scale, const void *A, const void *B,
+                              const float *scale, const int32_t *ranks, const int32_t *ids,
+                              int32_t M, int32_t d_in, int32_t d_out, int32_t r_max,
+                              int32_t n_adapters, const lora_segments_t *segs,
+                              const lora_epilogue_t *epi, void *y, lora_dtype_t y_dtype,
+                              lora_mode_t mode, void *ws, size_t ws_bytes, void *stream) {
+    return linear8<uint8_t>(x8, x_scale, W8, w_scale, A, B, scale, ranks, ids, M, d_in, d_out, r_max,
+                            n_adapters, segs, epi, y, y_dtype, mode, ws, ws_bytes, stream);
+}
+
+size_t lora_int8_workspace_bytes(int32_t M, int32_t d_in, int32_t d_out, int32_t r_max,
+                                 int32_t n_adapters) {
+    return workspace8(M, d_in, d_out, r_max, n_adapters, true);
+}
+
+lora_status_t lora_linear_int8(const void *x8, const float *x_scale, const void *W8,
+                               const float *w_scale, const void *A, const void *B,
+                               const float *scale, const int32_t *ranks, const int32_t *ids,
+                               int32_t M, int32_t d_in, int32_t d_out, int32_t r_max,
+                               int32_t n_adapters, const lora_segments_t *segs,
+                               const lora_epilogue_t *epi, void *y, lora_dtype_t y_dtype,
+                               lora_mode_t mode, void *ws, size_t ws_bytes, void *stream) {
+    return linear8<int8_t>(x8, x_scale, W8, w_scale, A, B, scale, ranks, ids, M, d_in, d_out, r_max,
+                           n_adapters, segs, epi, y, y_dtype, mode, ws, ws_bytes, stream);
 }
 
 }  // extern "C"

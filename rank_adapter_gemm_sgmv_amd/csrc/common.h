@@ -66,6 +66,26 @@ __device__ __forceinline__ uint4 e4m3x8_to_bf16(uint32_t lo, uint32_t hi) {
                       __builtin_bit_cast(uint32_t, c), __builtin_bit_cast(uint32_t, d));
 }
 
+// 8 integers (two dwords of four) -> 8 bf16 of the same values (exact: at most 8 significant bits, so
+// the floats' low halves are zeros)
+__device__ __forceinline__ uint4 int8x8_to_bf16(uint32_t lo, uint32_t hi) {
+    uint32_t o[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        const int w = (int)(i < 2 ? lo : hi) >> (16 * (i & 1));
+        const float a = (float)(int8_t)w, b = (float)(int8_t)(w >> 8);
+        o[i] = (__float_as_uint(a) >> 16) | (__float_as_uint(b) & 0xFFFF0000u);
+    }
+    return make_uint4(o[0], o[1], o[2], o[3]);
+}
+// By the type an 8-bit operand is held in: E4M3 codes are uint8_t, integers int8_t.
+template <class X>
+__device__ __forceinline__ uint4 codes8_to_bf16(uint32_t lo, uint32_t hi) {
+    static_assert(sizeof(X) == 1, "8-bit operands");
+    if constexpr (static_cast<X>(-1) < 0) return int8x8_to_bf16(lo, hi);
+    else return e4m3x8_to_bf16(lo, hi);
+}
+
 __device__ __forceinline__ uint4 ld16(const void *p) { return *reinterpret_cast<const uint4 *>(p); }
 __device__ __forceinline__ void st16(void *p, uint4 v) { *reinterpret_cast<uint4 *>(p) = v; }
 // A store of data that this kernel does not read again (nontemporal).
@@ -118,13 +138,13 @@ constexpr int rank_bucket(int r_max) { return r_max <= 8 ? 8 : r_max <= 16 ? 16 
 // step against 18.3 at rank 16); in a 16-wide slot the second group re-reads the first.
 constexpr int fused_tile_rank(int rb) { return rb < 16 ? 16 : rb; }
 
-// Bias, activation, gate product and residual of lora_linear_act and lora_linear_fp8, applied
+// Bias, activation, gate product and residual of lora_linear_act and the 8-bit layers, applied
 // where y is rounded (csrc/epilogue.h): y = act(row_scale[m] z + bias) * mul + residual.
 struct Epilogue {
     const uint16_t *bias;    // [N] bf16, or nullptr
     const void *mul;         // [M][N] in y's type, or nullptr
     const void *residual;    // [M][N] in y's type, or nullptr; mul and residual may be y
-    const float *row_scale;  // [M] (the fp8 layer's x scales), or nullptr
+    const float *row_scale;  // [M] (the 8-bit layers' x scales), or nullptr
     int act;                 // lora_act_t
 };
 
@@ -166,10 +186,12 @@ hipError_t launch_shrink(const uint16_t *x, const uint16_t *A, const int32_t *ra
                          const int32_t *roff, int pool_rows, int pstride, int M, int d_in,
                          int r_max, int n_adapters, Seg seg, float *partial, int kc, int ksplit,
                          hipStream_t s);
-// The same on E4M3 codes x8[M][d_in] (a padded pool): t of the codes' values, unscaled.
-hipError_t launch_shrink_x8(const uint8_t *x8, const uint16_t *A, const int32_t *ranks,
-                            int pstride, int M, int d_in, int r_max, int n_adapters, Seg seg,
-                            float *partial, int kc, int ksplit, hipStream_t s);
+// The same on E4M3 codes (uint8_t) or integers (int8_t) x8[M][d_in] (a padded pool): t of their
+// values, unscaled.
+template <class X>
+hipError_t launch_shrink_x8(const X *x8, const uint16_t *A, const int32_t *ranks, int pstride, int M,
+                            int d_in, int r_max, int n_adapters, Seg seg, float *partial, int kc,
+                            int ksplit, hipStream_t s);
 // The same over n_proj <= kMaxProj pools that share x, the tables and the segments
 // (lora_linear_multi) in one launch: pool p reads A[p] and writes partial[p].
 hipError_t launch_shrink_multi(const uint16_t *x, int n_proj, const uint16_t *const *A,
@@ -323,15 +345,18 @@ hipError_t launch_decode_gemm_fp8_lora(const uint16_t *x, const uint8_t *W8, con
                                        const uint16_t *A, int M, int K, int N,
                                        const DecodeLora &lo, float *partial, hipStream_t s);
 
-// Both with E4M3 x (lora_linear_fp8; the rows' scales are the reduction's epilogue's), for which
-// K may be any multiple of 16 from 128 (decode_fp8_supported).
+// Both with 8-bit x too, E4M3 codes (lora_linear_fp8) or integers (int8_t, lora_linear_int8); the
+// rows' scales are the reduction's epilogue's.  K may be any multiple of 16 from 128
+// (decode_fp8_supported).
 constexpr int kFp8DecodeMaxRows = 192;
 bool decode_fp8_supported(int M, int K, int N);
 size_t decode_fp8_partial_floats(int M, int K, int N, int r_max, int n_adapters);
-hipError_t launch_decode_gemm_fp8_x8(const uint8_t *x8, const uint8_t *W8, const float *w_scale,
+template <class X>
+hipError_t launch_decode_gemm_fp8_x8(const X *x8, const X *W8, const float *w_scale,
                                      int M, int K, int N, float *partial, const SegBuild *build,
                                      hipStream_t s);
-hipError_t launch_decode_gemm_fp8_lora_x8(const uint8_t *x8, const uint8_t *W8, const float *w_scale,
+template <class X>
+hipError_t launch_decode_gemm_fp8_lora_x8(const X *x8, const X *W8, const float *w_scale,
                                           const uint16_t *A, int M, int K, int N,
                                           const DecodeLora &lo, float *partial, hipStream_t s);
 
@@ -389,9 +414,11 @@ hipError_t launch_moe_gemm(const MoePlan &p, const MoeGemmArgs &a, hipStream_t s
 hipError_t launch_moe_reduce(const MoePlan &p, const MoeReduceArgs &a, bool y_f32, hipStream_t s);
 
 // ---- the layer on 8-bit operands (csrc/gemm_fp8.hip) ------------------------------------------
-struct Fp8Gemm {
-    const uint8_t *x8;     // [M][K] E4M3 codes
-    const uint8_t *W8;     // [N][K] E4M3 codes
+// X: E4M3 codes (uint8_t, lora_linear_fp8) or integers (int8_t, lora_linear_int8).
+template <class X>
+struct Gemm8 {
+    const X *x8;           // [M][K]
+    const X *W8;           // [N][K]
     const float *w_scale;  // [N]
     int M, K, N;           // K % 16 == 0, N % 8 == 0
 };
@@ -404,7 +431,8 @@ Fp8Plan fp8_plan(int M, int K, int N, bool y_f32, int r_max, int n_adapters);
 size_t fp8_partial_floats(int M, int K, int N, int r_max, int n_adapters);
 // !p.split: y from rows in segment order, with the delta and the epilogue.  p.split: slices
 // partial[ks][M][N] of x8 W8^T w_scale (launch_splitk_reduce_lora must follow).
-hipError_t launch_gemm_fp8(const Fp8Gemm &g, const Fp8Plan &p, void *y, bool y_f32, Seg seg,
+template <class X>
+hipError_t launch_gemm_fp8(const Gemm8<X> &g, const Fp8Plan &p, void *y, bool y_f32, Seg seg,
                            const LoraEpilogue &ep, const Epilogue &epi, float *partial,
                            hipStream_t s);
 

@@ -322,7 +322,7 @@ __global__ __launch_bounds__(kThreads) void decode_gemm_kernel(
         dec_tile_out<C, false>(acc, lds, lo, M, mine, tid, lane, wave);
 }
 
-// ---- the same split-K GEMM with an fp8 base weight -----------------------------------------
+// ---- the same split-K GEMM with an 8-bit base weight -----------------------------------------
 // W8 holds E4M3 codes (OCP 8-bit floating point) laid out W8[N][K] -- each output column's K
 // codes contiguous -- with one fp32 scale per column: W_eff[k, n] = w_scale[n] dec(W8[n, k]).
 // Tiles and splits are decode_gemm_kernel's (dec_plan without adapter tiles), so the decode
@@ -347,15 +347,20 @@ __global__ __launch_bounds__(kThreads) void decode_gemm_kernel(
 //    of the MFMAs (with a branch per step and one set: 16.3 us at 64 x 4096 x 4096, now
 //    11.6 us); each wave writes its columns of the partial tile straight from its
 //    accumulators.
-constexpr int kF8K = 128;  // k per fp8 stage
+//
+// Integers (int8_t, lora_linear_int8: x and W8 both) lie and are staged alike and skip the widening: a
+// step is 32 k of v_mfma_i32_32x32x32_i8, whose operands are whole 16-byte chunks (two ds_read_b128
+// where eight of k took two ds_read_b64 and eight conversions), with exact int32 sums.
+constexpr int kF8K = 128;  // k per stage
 
-// X8: x holds E4M3 codes too (lora_linear_fp8): row r, 16-k chunk kc at slot 8 r + (kc ^ ((r >> 1) &
-// 7)), as a column of W8, and the codes become bf16 as they are read for the MFMAs.
-template <int BM_, bool X8_ = false>
+// X8: x holds E4M3 codes (uint8_t, lora_linear_fp8) or integers too: row r, 16-k chunk kc at slot
+// 8 r + (kc ^ ((r >> 1) & 7)), as a column of W8; E4M3 codes become bf16 as they are read for the MFMAs.
+template <int BM_, class X_ = uint16_t>
 struct DecF8 {
     static constexpr int BM = BM_;
-    static constexpr bool X8 = X8_;
-    using X = std::conditional_t<X8, uint8_t, uint16_t>;
+    using X = X_;
+    static constexpr bool X8 = sizeof(X) == 1, INT = std::is_same_v<X, int8_t>;
+    using WT = std::conditional_t<INT, int8_t, uint8_t>;  // W8's elements
     static constexpr int TM = BM / 32;
     static constexpr int XSLOT = BM * kF8K * (int)sizeof(X) / 16;  // uint4 per x stage
     static constexpr int WSLOT_W = 32 * kF8K / 16;         // uint4 per W stage of one wave
@@ -370,6 +375,9 @@ struct DecF8 {
 
 typedef uint32_t u32x2_t __attribute__((ext_vector_type(2)));
 typedef __attribute__((address_space(3))) u32x2_t lds_u32x2_t;
+typedef int32_t i32x4_t __attribute__((ext_vector_type(4)));
+typedef int32_t i32x16_t __attribute__((ext_vector_type(16)));
+typedef __attribute__((address_space(3))) i32x4_t lds_i32x4_t;
 
 // 8 codes (two dwords) -> 8 bf16
 __device__ __forceinline__ bf16x8_t dec_fp8x8(uint32_t lo, uint32_t hi) {
@@ -382,7 +390,7 @@ __device__ __forceinline__ bf16x8_t dec_fp8x8(uint32_t lo, uint32_t hi) {
 // must call it (barriers).
 template <class C, bool WT>
 __device__ __forceinline__ void f8_tile(uint4 *lds, const typename C::X *__restrict__ x,
-                                        const uint8_t *__restrict__ W8,
+                                        const typename C::WT *__restrict__ W8,
                                         const float *__restrict__ w_scale, int M, int K, int N,
                                         int n_tiles, int tile, int split, int tm, int tn,
                                         int k_per_split, float *__restrict__ partial, int lane,
@@ -397,7 +405,7 @@ __device__ __forceinline__ void f8_tile(uint4 *lds, const typename C::X *__restr
     // W8 load q of a stage, lane l: column c = 8 q + l / 8 of the wave's 32 (columns past N
     // read the last one, never used), chunk (l % 8) ^ ((c >> 1) & 7), to slot 64 q + l = 8 c +
     // (l % 8)
-    const uint8_t *wp[C::WI];
+    const typename C::WT *wp[C::WI];
     int wkc[C::WI];
 #pragma unroll
     for (int q = 0; q < C::WI; ++q) {
@@ -439,11 +447,11 @@ __device__ __forceinline__ void f8_tile(uint4 *lds, const typename C::X *__restr
 
     // two accumulator sets (even and odd steps) so that twice as many MFMA chains are
     // independent; added at the end
-    f32x16_t acc[C::TM][2];
+    std::conditional_t<C::INT, i32x16_t, f32x16_t> acc[C::TM][2];
 #pragma unroll
     for (int i = 0; i < C::TM; ++i)
 #pragma unroll
-        for (int v = 0; v < 16; ++v) acc[i][0][v] = acc[i][1][v] = 0.0f;
+        for (int v = 0; v < 16; ++v) acc[i][0][v] = acc[i][1][v] = 0;
 
     uint4 *const S0 = lds, *const S1 = lds + C::SLOT, *const S2 = lds + 2 * C::SLOT;
     issue(0, S0);
@@ -459,22 +467,37 @@ __device__ __forceinline__ void f8_tile(uint4 *lds, const typename C::X *__restr
         const lds_char_t *ws = (const lds_char_t *)(SC + C::XSLOT + wave * C::WSLOT_W);
         // steps past the split's last carry zero codes (a select, not a branch, so the
         // compiler may issue every step's LDS reads ahead of the MFMAs)
+        if constexpr (C::INT) {
 #pragma unroll
-        for (int st = 0; st < 8; ++st) {
-            const u32x2_t v = *(const lds_u32x2_t *)(ws + (8 * c + (st ^ ((c >> 1) & 7))) * 16 + 8 * g);
-            const bool ok = 8 * u + st < nst;
-            const bf16x8_t b = dec_fp8x8(ok ? v[0] : 0u, ok ? v[1] : 0u);
+            for (int st = 0; st < 4; ++st) {
+                const int kc = 2 * st + g;
+                const i32x4_t w = *(const lds_i32x4_t *)(ws + (8 * c + (kc ^ ((c >> 1) & 7))) * 16);
+                const i32x4_t b = 8 * u + kc < nst ? w : i32x4_t{0, 0, 0, 0};
 #pragma unroll
-            for (int i = 0; i < C::TM; ++i) {
-                const int r = 32 * i + c;
-                bf16x8_t a;
-                if constexpr (C::X8) {
-                    const u32x2_t xv = *(const lds_u32x2_t *)((const lds_char_t *)xs + (8 * r + (st ^ ((r >> 1) & 7))) * 16 + 8 * g);
-                    a = dec_fp8x8(xv[0], xv[1]);
-                } else {
-                    a = *reinterpret_cast<const bf16x8_t *>(&xs[16 * r + ((2 * st + g) ^ (r & 15))]);
+                for (int i = 0; i < C::TM; ++i) {
+                    const int r = 32 * i + c;
+                    const i32x4_t a = *(const lds_i32x4_t *)((const lds_char_t *)xs + (8 * r + (kc ^ ((r >> 1) & 7))) * 16);
+                    acc[i][st & 1] = __builtin_amdgcn_mfma_i32_32x32x32_i8(a, b, acc[i][st & 1], 0, 0, 0);
                 }
-                acc[i][st & 1] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(a, b, acc[i][st & 1], 0, 0, 0);
+            }
+        } else {
+#pragma unroll
+            for (int st = 0; st < 8; ++st) {
+                const u32x2_t v = *(const lds_u32x2_t *)(ws + (8 * c + (st ^ ((c >> 1) & 7))) * 16 + 8 * g);
+                const bool ok = 8 * u + st < nst;
+                const bf16x8_t b = dec_fp8x8(ok ? v[0] : 0u, ok ? v[1] : 0u);
+#pragma unroll
+                for (int i = 0; i < C::TM; ++i) {
+                    const int r = 32 * i + c;
+                    bf16x8_t a;
+                    if constexpr (C::X8) {
+                        const u32x2_t xv = *(const lds_u32x2_t *)((const lds_char_t *)xs + (8 * r + (st ^ ((r >> 1) & 7))) * 16 + 8 * g);
+                        a = dec_fp8x8(xv[0], xv[1]);
+                    } else {
+                        a = *reinterpret_cast<const bf16x8_t *>(&xs[16 * r + ((2 * st + g) ^ (r & 15))]);
+                    }
+                    acc[i][st & 1] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(a, b, acc[i][st & 1], 0, 0, 0);
+                }
             }
         }
     }
@@ -490,7 +513,7 @@ __device__ __forceinline__ void f8_tile(uint4 *lds, const typename C::X *__restr
 #pragma unroll
         for (int v = 0; v < 16; ++v) {
             float *const o = &P[(size_t)(32 * i + (v / 4) * 8 + g * 4 + v % 4) * kBN];
-            const float val = sc * (acc[i][0][v] + acc[i][1][v]);
+            const float val = sc * (float)(acc[i][0][v] + acc[i][1][v]);
             if constexpr (WT) st_wt(o, val);
             else *o = val;
         }
@@ -500,7 +523,7 @@ __device__ __forceinline__ void f8_tile(uint4 *lds, const typename C::X *__restr
 // segments instead.
 template <class C, bool BUILD>
 __global__ __launch_bounds__(kThreads) void decode_gemm_fp8_kernel(
-    const typename C::X *__restrict__ x, const uint8_t *__restrict__ W8, const float *__restrict__ w_scale,
+    const typename C::X *__restrict__ x, const typename C::WT *__restrict__ W8, const float *__restrict__ w_scale,
     int M, int K, int N, int n_tm, int n_tn, int k_per_split, float *__restrict__ partial,
     int n_gemm_blocks, SegBuild build) {
     __shared__ __attribute__((aligned(1024))) uint4 lds[C::LDS16];
@@ -536,10 +559,10 @@ __global__ __launch_bounds__(kThreads) void decode_gemm_fp8_kernel(
 // decode_gemm_kernel.  Both kinds of workgroup share one LDS array sized for the larger.
 template <class CF, class CB, int RM>
 __global__ __launch_bounds__(kThreads) void decode_gemm_fp8_lora_kernel(
-    const typename CF::X *__restrict__ x, const uint8_t *__restrict__ W8, const float *__restrict__ w_scale,
+    const typename CF::X *__restrict__ x, const typename CF::WT *__restrict__ W8, const float *__restrict__ w_scale,
     const uint16_t *__restrict__ A, int M, int K, int N, int n_tm, int n_tn, int n_lt,
     int k_per_split, float *__restrict__ partial, DecodeLora lo, int n_gemm_blocks) {
-    static_assert(CF::BM == CB::BM && CF::TILE == CB::TILE && CF::X8 == CB::X8, "one tile shape");
+    static_assert(CF::BM == CB::BM && CF::TILE == CB::TILE && std::is_same_v<typename CF::X, typename CB::X>, "one tile shape");
     constexpr int L16 = CF::LDS16 > kWaves * CB::WAVE ? CF::LDS16 : kWaves * CB::WAVE;
     __shared__ __attribute__((aligned(1024))) uint4 lds[L16];
 
@@ -1119,8 +1142,8 @@ hipError_t launch_decode_gemm(const uint16_t *x, const uint16_t *W, const uint16
 
 namespace {
 
-template <class X>
-hipError_t launch_f8(const X *x, const uint8_t *W8, const float *w_scale, int M, int K, int N,
+template <class X, class WT>
+hipError_t launch_f8(const X *x, const WT *W8, const float *w_scale, int M, int K, int N,
                      float *partial, const SegBuild *build, hipStream_t s) {
     constexpr bool X8 = sizeof(X) == 1;
     if (!(X8 ? decode_fp8_supported(M, K, N) : decode_gemm_supported(M, K, N)) || N % 8 != 0 || partial == nullptr || w_scale == nullptr)
@@ -1133,10 +1156,10 @@ hipError_t launch_f8(const X *x, const uint8_t *W8, const float *w_scale, int M,
     const SegBuild bld = build ? *build : SegBuild{nullptr, 1, Seg{}};
 #define F8_LAUNCH(BM)                                                                          \
     if (build)                                                                                 \
-        launch((decode_gemm_fp8_kernel<DecF8<BM, X8>, true>), grid, dim3(kThreads), 0, s, x, W8,     \
+        launch((decode_gemm_fp8_kernel<DecF8<BM, X>, true>), grid, dim3(kThreads), 0, s, x, W8,     \
                w_scale, M, K, N, p.n_tm, p.n_tn, p.k_per_split, partial, n_gemm, bld);          \
     else                                                                                       \
-        launch((decode_gemm_fp8_kernel<DecF8<BM, X8>, false>), grid, dim3(kThreads), 0, s, x, W8,    \
+        launch((decode_gemm_fp8_kernel<DecF8<BM, X>, false>), grid, dim3(kThreads), 0, s, x, W8,    \
                w_scale, M, K, N, p.n_tm, p.n_tn, p.k_per_split, partial, n_gemm, bld)
     if (p.bm == 32) {
         F8_LAUNCH(32);
@@ -1147,8 +1170,8 @@ hipError_t launch_f8(const X *x, const uint8_t *W8, const float *w_scale, int M,
     return hipGetLastError();
 }
 
-template <class X>
-hipError_t launch_f8_lora(const X *x, const uint8_t *W8, const float *w_scale, const uint16_t *A, int M,
+template <class X, class WT>
+hipError_t launch_f8_lora(const X *x, const WT *W8, const float *w_scale, const uint16_t *A, int M,
                           int K, int N, const DecodeLora &lo, float *partial, hipStream_t s) {
     constexpr bool X8 = sizeof(X) == 1;
     if (!(X8 ? decode_fp8_supported(M, K, N) : decode_gemm_supported(M, K, N)) || M > kDecodeMaxRows || N % 8 != 0 || partial == nullptr ||
@@ -1159,7 +1182,7 @@ hipError_t launch_f8_lora(const X *x, const uint8_t *W8, const float *w_scale, c
     const DecPlan p = dec_plan(M, K, N, n_lt);
     const int n_gemm = p.n_tm * (p.n_tn + n_lt) * p.ks;
 #define F8L_ONE(BM, RMX)                                                                        \
-    launch((decode_gemm_fp8_lora_kernel<DecF8<BM, X8>, Dec<BM, X8>, RMX>), dim3(n_gemm), dim3(kThreads), \
+    launch((decode_gemm_fp8_lora_kernel<DecF8<BM, X>, Dec<BM, X>, RMX>), dim3(n_gemm), dim3(kThreads), \
            0, s, x, W8, w_scale, A, M, K, N, p.n_tm, p.n_tn, n_lt, p.k_per_split, partial, lo,   \
            n_gemm)
 #define F8L_RANK(BM)                                                                            \
@@ -1187,11 +1210,16 @@ hipError_t launch_decode_gemm_fp8(const uint16_t *x, const uint8_t *W8, const fl
     return launch_f8(x, W8, w_scale, M, K, N, partial, build, s);
 }
 
-hipError_t launch_decode_gemm_fp8_x8(const uint8_t *x8, const uint8_t *W8, const float *w_scale,
+template <class X>
+hipError_t launch_decode_gemm_fp8_x8(const X *x8, const X *W8, const float *w_scale,
                                      int M, int K, int N, float *partial, const SegBuild *build,
                                      hipStream_t s) {
     return launch_f8(x8, W8, w_scale, M, K, N, partial, build, s);
 }
+template hipError_t launch_decode_gemm_fp8_x8(const uint8_t *, const uint8_t *, const float *, int, int, int,
+                                              float *, const SegBuild *, hipStream_t);
+template hipError_t launch_decode_gemm_fp8_x8(const int8_t *, const int8_t *, const float *, int, int, int,
+                                              float *, const SegBuild *, hipStream_t);
 
 hipError_t launch_decode_gemm_fp8_lora(const uint16_t *x, const uint8_t *W8, const float *w_scale,
                                        const uint16_t *A, int M, int K, int N,
@@ -1199,11 +1227,18 @@ hipError_t launch_decode_gemm_fp8_lora(const uint16_t *x, const uint8_t *W8, con
     return launch_f8_lora(x, W8, w_scale, A, M, K, N, lo, partial, s);
 }
 
-hipError_t launch_decode_gemm_fp8_lora_x8(const uint8_t *x8, const uint8_t *W8, const float *w_scale,
+template <class X>
+hipError_t launch_decode_gemm_fp8_lora_x8(const X *x8, const X *W8, const float *w_scale,
                                           const uint16_t *A, int M, int K, int N,
                                           const DecodeLora &lo, float *partial, hipStream_t s) {
     return launch_f8_lora(x8, W8, w_scale, A, M, K, N, lo, partial, s);
 }
+template hipError_t launch_decode_gemm_fp8_lora_x8(const uint8_t *, const uint8_t *, const float *,
+                                                   const uint16_t *, int, int, int, const DecodeLora &,
+                                                   float *, hipStream_t);
+template hipError_t launch_decode_gemm_fp8_lora_x8(const int8_t *, const int8_t *, const float *,
+                                                   const uint16_t *, int, int, int, const DecodeLora &,
+                                                   float *, hipStream_t);
 
 hipError_t launch_decode_reduce(const float *partial, int M, int K, int N, void *y, bool y_f32,
                                 const DecodeLora &lo, bool adapters, const Seg *seg,

@@ -33,14 +33,14 @@ constexpr int kThreads = 64 * kWaves;
 // Per wave: four W stages of 16 rows x 128 columns (256-byte rows, one direct load covers 4
 // whole rows) and two x stages of BM rows x 64 k (128-byte rows, 8 whole rows per load).  A
 // 128-column tile reads each x byte for twice the W bytes a 64-column tile did.
-// X8: x holds E4M3 codes; a stage's rows are the same 128 bytes, so 128 k, and the codes become
-// bf16 (exactly) as they are read for the MFMAs.
-template <int BM_, bool X8_ = false>
+// X: bf16 (uint16_t), or (X8) x holds E4M3 codes (uint8_t) or integers (int8_t); a stage's rows are the
+// same 128 bytes, so 128 k, and the codes become bf16 (exactly) as they are read for the MFMAs.
+template <int BM_, class X_ = uint16_t>
 struct Dec {
     static constexpr int BM = BM_;
-    static constexpr bool X8 = X8_;
+    using X = X_;
+    static constexpr bool X8 = sizeof(X) == 1;
     static constexpr int KX = X8 ? 2 * kBKX : kBKX;  // k of an x stage
-    using X = std::conditional_t<X8, uint8_t, uint16_t>;
     static constexpr int TM = BM / 32, TN = kBN / 32;
     static constexpr int XSLOT = BM * kBKX * 2 / 16;     // uint4 per x stage (128-byte rows)
     static constexpr int WSLOT = kBKW * kBN * 2 / 16;    // uint4 per W stage
@@ -77,7 +77,7 @@ __device__ __forceinline__ void dec_mfma(f32x16_t (&acc)[C::TM][C::TN], const ui
         const int row = 32 * i + (lane & 31);
         if constexpr (C::X8) {
             const uint2 v = reinterpret_cast<const uint2 *>(&xs[row * 8 + (quarter ^ (row & 7))])[lane >> 5];
-            af[i] = __builtin_bit_cast(bf16x8_t, e4m3x8_to_bf16(v.x, v.y));
+            af[i] = __builtin_bit_cast(bf16x8_t, codes8_to_bf16<typename C::X>(v.x, v.y));
         } else {
             const int lc = 2 * quarter + (lane >> 5);
             af[i] = *reinterpret_cast<const bf16x8_t *>(&xs[row * 8 + (lc ^ (row & 7))]);

@@ -1,6 +1,6 @@
-// gemm_fp8.hip -- z = (x8 W8^T) w_scale on 8-bit operands (E4M3) with fp32 sums, for
-// lora_linear_fp8: x8[M][K] codes with a scale per row (applied with the epilogue), W8[N][K]
-// codes with a scale per column.
+// gemm_fp8.hip -- z = (x8 W8^T) w_scale on 8-bit operands: E4M3 codes with fp32 sums, for
+// lora_linear_fp8, or integers with int32 sums, for lora_linear_int8: x8[M][K] with a scale per row
+// (applied with the epilogue), W8[N][K] with a scale per column.
 //
 // gfx950 design
 //  * v_mfma_f32_32x32x64_f8f6f4: 64 k per instruction at twice the bf16 rate (its unscaled form:
@@ -38,6 +38,11 @@ constexpr int kK8 = 128;  // k per stage: two MFMA steps
 
 typedef int i32x8_t __attribute__((ext_vector_type(8)));
 typedef int i32x4_t __attribute__((ext_vector_type(4)));
+typedef int i32x16_t __attribute__((ext_vector_type(16)));
+
+// The K loop's sums: fp32, or exact int32 for integers.
+template <bool INT>
+using Sum8 = std::conditional_t<INT, i32x16_t, f32x16_t>;
 
 template <class C>
 struct Frags8 {
@@ -76,10 +81,25 @@ __device__ __forceinline__ void read_frags8(Frags8<C> &f, const uint4 *__restric
     for (int j = 0; j < C::TN; ++j) f.b[j] = read_row8(ws, wn0 + 32 * j + li, h, g);
 }
 
-// WIDE: the codes widened to bf16, octet by octet.
-template <class C, bool WIDE>
-__device__ __forceinline__ void mfma_frags8(f32x16_t (&acc)[C::TM][C::TN], const Frags8<C> &f) {
-    if constexpr (WIDE) {
+// WIDE: the codes widened to bf16, octet by octet.  INT: each of the lane's two chunks of every operand
+// is one instruction's.
+template <class C, bool WIDE, bool INT>
+__device__ __forceinline__ void mfma_frags8(Sum8<INT> (&acc)[C::TM][C::TN], const Frags8<C> &f) {
+    if constexpr (INT) {
+#pragma unroll
+        for (int q = 0; q < 2; ++q)
+#pragma unroll
+            for (int i = 0; i < C::TM; ++i)
+#pragma unroll
+                for (int j = 0; j < C::TN; ++j) {
+                    const i32x4_t a = q == 0 ? __builtin_shufflevector(f.a[i], f.a[i], 0, 1, 2, 3)
+                                             : __builtin_shufflevector(f.a[i], f.a[i], 4, 5, 6, 7);
+                    const i32x4_t b = q == 0 ? __builtin_shufflevector(f.b[j], f.b[j], 0, 1, 2, 3)
+                                             : __builtin_shufflevector(f.b[j], f.b[j], 4, 5, 6, 7);
+                    acc[i][j] = __builtin_amdgcn_mfma_i32_32x32x32_i8(a, b, acc[i][j], 0, 0, 0);
+                }
+        return;
+    } else if constexpr (WIDE) {
 #pragma unroll
         for (int q = 0; q < 4; ++q) {
             bf16x8_t b[C::TN];
@@ -97,19 +117,20 @@ __device__ __forceinline__ void mfma_frags8(f32x16_t (&acc)[C::TM][C::TN], const
             }
         }
         return;
+    } else {
+#pragma unroll
+        for (int i = 0; i < C::TM; ++i)
+#pragma unroll
+            for (int j = 0; j < C::TN; ++j)
+                acc[i][j] = __builtin_amdgcn_mfma_scale_f32_32x32x64_f8f6f4(f.a[i], f.b[j], acc[i][j], 0, 0,
+                                                                            0, 0, 0, 0);
     }
-#pragma unroll
-    for (int i = 0; i < C::TM; ++i)
-#pragma unroll
-        for (int j = 0; j < C::TN; ++j)
-            acc[i][j] = __builtin_amdgcn_mfma_scale_f32_32x32x64_f8f6f4(f.a[i], f.b[j], acc[i][j], 0, 0, 0,
-                                                                        0, 0, 0);
 }
 
 // The next step's LDS reads among this step's MFMAs.
-template <class C>
+template <class C, bool INT>
 __device__ __forceinline__ void interleave_reads8() {
-    constexpr int reads = 2 * (C::TM + C::TN), mfmas = C::TM * C::TN;
+    constexpr int reads = 2 * (C::TM + C::TN), mfmas = (INT ? 2 : 1) * C::TM * C::TN;
     constexpr int groups = mfmas < 4 ? mfmas : 4;
 #pragma unroll
     for (int gi = 0; gi < groups; ++gi) {
@@ -164,15 +185,17 @@ __device__ __forceinline__ void fill8(uint4 *slot, const uint8_t *__restrict__ s
     }
 }
 
-// WIDE: y is fp32 (see the top).  FUSED: whole K, rows in segment order, delta and epilogue; else slice blockIdx.y of K, rows in
+// X: E4M3 codes (uint8_t) or integers (int8_t).  WIDE: y is fp32 (see the top).  FUSED: whole K, rows in segment order, delta and epilogue; else slice blockIdx.y of K, rows in
 // their own order, into partial[blockIdx.y][M][N].
-template <class C, bool FUSED, bool WIDE, bool O32>
+template <class C, class X, bool FUSED, bool WIDE, bool O32>
 __global__ __launch_bounds__(C::NT, 2) void gemm_fp8_kernel(
-    const uint8_t *__restrict__ x8, const uint8_t *__restrict__ W8,
+    const X *__restrict__ x, const X *__restrict__ W,
     const float *__restrict__ w_scale, int M, int K, int N, int k_per_split,
     float *__restrict__ partial, void *y, int n_tm, int n_tn, Seg seg, LoraEpilogue ep,
     Epilogue epi) {
     using G = Stage8<C>;
+    constexpr bool INT = std::is_same_v<X, int8_t>;
+    const uint8_t *const x8 = reinterpret_cast<const uint8_t *>(x), *const W8 = reinterpret_cast<const uint8_t *>(W);
     __shared__ __attribute__((aligned(1024))) uint4 X0[G::XSLOT];
     __shared__ __attribute__((aligned(1024))) uint4 X1[G::XSLOT];
     __shared__ __attribute__((aligned(1024))) uint4 W0[G::WSLOT];
@@ -210,13 +233,13 @@ __global__ __launch_bounds__(C::NT, 2) void gemm_fp8_kernel(
         else src.wp[j] = W8 + o;
     }
 
-    f32x16_t acc[C::TM][C::TN];
+    Sum8<INT> sum[C::TM][C::TN];
 #pragma unroll
     for (int i = 0; i < C::TM; ++i)
 #pragma unroll
         for (int j = 0; j < C::TN; ++j)
 #pragma unroll
-            for (int v = 0; v < 16; ++v) acc[i][j][v] = 0.0f;
+            for (int v = 0; v < 16; ++v) sum[i][j][v] = 0;
 
     // Per stage: multiply its first step while reading the second; then wait for the next
     // stage's loads (issued a stage ago) and, at the barrier, for every wave to have read this
@@ -234,14 +257,14 @@ __global__ __launch_bounds__(C::NT, 2) void gemm_fp8_kernel(
         read_frags8<C>(fa, X0, W0, 0, lane, wm0, wn0);
 #define LORA_FP8_STAGE(XP, WP, XQ, WQ)                                           \
         read_frags8<C>(fb, XP, WP, 1, lane, wm0, wn0);                           \
-        mfma_frags8<C, WIDE>(acc, fa);                                           \
-        if constexpr (!WIDE) interleave_reads8<C>();                             \
+        mfma_frags8<C, WIDE, INT>(sum, fa);                                      \
+        if constexpr (!WIDE || INT) interleave_reads8<C, INT>();                 \
         wait_vm<0>();                                                            \
         lds_barrier();                                                           \
         issue8<C>(src, XP, WP, wave, k_lo + min(s + 2, n - 1) * kK8);            \
         read_frags8<C>(fa, XQ, WQ, 0, lane, wm0, wn0);                           \
-        mfma_frags8<C, WIDE>(acc, fb);                                           \
-        if constexpr (!WIDE) interleave_reads8<C>();                             \
+        mfma_frags8<C, WIDE, INT>(sum, fb);                                      \
+        if constexpr (!WIDE || INT) interleave_reads8<C, INT>();                 \
         if (++s == n) break;
         for (int s = 0;;) {
             LORA_FP8_STAGE(X0, W0, X1, W1)
@@ -264,19 +287,20 @@ __global__ __launch_bounds__(C::NT, 2) void gemm_fp8_kernel(
             if (k0 + 64 * h < k_hi) {
                 Frags8<C> f;
                 read_frags8<C>(f, X0, W0, h, lane, wm0, wn0);
-                mfma_frags8<C, WIDE>(acc, f);
+                mfma_frags8<C, WIDE, INT>(sum, f);
             }
         }
     }
 
-    // the columns' scales
+    // the columns' scales (an integer sum is rounded to fp32 here)
+    f32x16_t acc[C::TM][C::TN];
 #pragma unroll
     for (int j = 0; j < C::TN; ++j) {
         const float ws = w_scale[min(n0 + wn0 + 32 * j + (lane & 31), N - 1)];
 #pragma unroll
         for (int i = 0; i < C::TM; ++i)
 #pragma unroll
-            for (int v = 0; v < 16; ++v) acc[i][j][v] *= ws;
+            for (int v = 0; v < 16; ++v) acc[i][j][v] = (float)sum[i][j][v] * ws;
     }
 
     if constexpr (FUSED) {
@@ -309,15 +333,15 @@ __global__ __launch_bounds__(C::NT, 2) void gemm_fp8_kernel(
     }
 }
 
-template <class C, bool FUSED>
-hipError_t launch_fp8_cfg(const Fp8Gemm &g, const Fp8Plan &p, void *y, bool y_f32, Seg seg,
+template <class C, bool FUSED, class X>
+hipError_t launch_fp8_cfg(const Gemm8<X> &g, const Fp8Plan &p, void *y, bool y_f32, Seg seg,
                           const LoraEpilogue &ep, const Epilogue &epi, float *partial,
                           hipStream_t s) {
     const int n_tm = (g.M + C::BM - 1) / C::BM, n_tn = (g.N + C::BN - 1) / C::BN;
     const bool o32 = (size_t)g.M * g.K <= 0xFFFFFFFFull && (size_t)g.N * g.K <= 0xFFFFFFFFull;
     const dim3 grid(n_tm * n_tn, p.ks);
 #define FP8_ONE(WIDE, O32)                                                                     \
-    launch((gemm_fp8_kernel<C, FUSED, WIDE, O32>), grid, dim3(C::NT), 0, s, g.x8, g.W8, g.w_scale, \
+    launch((gemm_fp8_kernel<C, X, FUSED, WIDE, O32>), grid, dim3(C::NT), 0, s, g.x8, g.W8, g.w_scale, \
            g.M, g.K, g.N, p.k_per_split, partial, y, n_tm, n_tn, seg, ep, epi)
     if constexpr (C::BM == 128) {  // (fp8_plan: fp32 y takes the small tiles)
         if (y_f32) {
@@ -374,7 +398,8 @@ size_t fp8_partial_floats(int M, int K, int N, int r_max, int n_adapters) {
     return p.split ? (size_t)p.ks * M * N : 0;
 }
 
-hipError_t launch_gemm_fp8(const Fp8Gemm &g, const Fp8Plan &p, void *y, bool y_f32, Seg seg,
+template <class X>
+hipError_t launch_gemm_fp8(const Gemm8<X> &g, const Fp8Plan &p, void *y, bool y_f32, Seg seg,
                            const LoraEpilogue &ep, const Epilogue &epi, float *partial,
                            hipStream_t s) {
     if (g.M < 1 || g.K < 16 || g.K % 16 != 0 || g.N < 8 || g.N % 8 != 0) return hipErrorInvalidValue;
@@ -385,5 +410,9 @@ hipError_t launch_gemm_fp8(const Fp8Gemm &g, const Fp8Plan &p, void *y, bool y_f
     if (p.big) return launch_fp8_cfg<Big<256, 256, 2, 4>, true>(g, p, y, y_f32, seg, ep, epi, nullptr, s);
     return launch_fp8_cfg<Big<128, 128>, true>(g, p, y, y_f32, seg, ep, epi, nullptr, s);
 }
+template hipError_t launch_gemm_fp8(const Gemm8<uint8_t> &, const Fp8Plan &, void *, bool, Seg,
+                                    const LoraEpilogue &, const Epilogue &, float *, hipStream_t);
+template hipError_t launch_gemm_fp8(const Gemm8<int8_t> &, const Fp8Plan &, void *, bool, Seg,
+                                    const LoraEpilogue &, const Epilogue &, float *, hipStream_t);
 
 }  // namespace lora

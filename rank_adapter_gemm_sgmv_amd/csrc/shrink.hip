@@ -58,14 +58,14 @@ struct MfmaShrink {
 
 // The MFMA steps over one LDS fill: rows kb .. kb + KS of the chunk (x beyond k_hi masked),
 // v_mfma_f32_16x16x32_bf16 per 16 rank columns below the rank.
-template <class C, int RM, class XV>
+template <class C, int RM, class XE, class XV>
 __device__ __forceinline__ void shrink_mfma_fill(f32x4_t (&acc)[C::NB], const XV (&xv)[C::STEPS],
                                                  const lds_char_t *wl, int kb, int k_hi, int g,
                                                  int li, int r) {
 #pragma unroll
     for (int st = 0; st < C::STEPS; ++st) {
         uint4 xw;
-        if constexpr (std::is_same_v<XV, uint2>) xw = e4m3x8_to_bf16(xv[st].x, xv[st].y);
+        if constexpr (sizeof(XE) == 1) xw = codes8_to_bf16<XE>(xv[st].x, xv[st].y);
         else xw = xv[st];
         const uint4 xs = kb + 32 * st + 8 * g < k_hi ? xw : make_uint4(0, 0, 0, 0);
         const bf16x8_t xa = __builtin_bit_cast(bf16x8_t, xs);
@@ -110,9 +110,10 @@ struct ShrinkPools {
     int n;
 };
 
-// X8: x holds E4M3 codes instead (t of their values; the row's scale is applied with the
-// epilogue): half the bytes, each lane's 8 codes widened to bf16 (exactly) when they are used.
-template <int RM, int LAYOUT, bool X8>
+// XE: x holds bf16 (uint16_t), or E4M3 codes (uint8_t) or integers (int8_t) instead (t of their values;
+// the row's scale is applied with the epilogue): half the bytes, each lane's 8 codes widened to
+// bf16 (exactly) when they are used.
+template <int RM, int LAYOUT, class XE>
 __global__ __launch_bounds__(64 * kWavesPerBlock) void shrink_mfma_kernel(
     const void *__restrict__ x, ShrinkPools pools, const int32_t *__restrict__ ranks,
     const int32_t *__restrict__ roff, int pool_rows, int pstride, int M, int d_in, int n_adapters,
@@ -155,8 +156,7 @@ __global__ __launch_bounds__(64 * kWavesPerBlock) void shrink_mfma_kernel(
         const int k_lo = min(k0, d_in), k_hi = min(k0 + kw, d_in);
         // this lane's x row (rows beyond the tile repeat its last row; their sums are dropped)
         const int mrow = seg.perm[p0 + min(li, rows - 1)];
-        using XV = std::conditional_t<X8, uint2, uint4>;  // 8 elements of x
-        using XE = std::conditional_t<X8, uint8_t, uint16_t>;
+        using XV = std::conditional_t<sizeof(XE) == 1, uint2, uint4>;  // 8 elements of x
         const XE *xr = static_cast<const XE *>(x) + (size_t)mrow * d_in;
         auto load_x = [&](int k) { return *reinterpret_cast<const XV *>(xr + min(k, d_in - 8)); };
         const uint16_t *Aa = A + (size_t)row0 * d_in;
@@ -220,7 +220,7 @@ __global__ __launch_bounds__(64 * kWavesPerBlock) void shrink_mfma_kernel(
                     *reinterpret_cast<uint4 *>(wg + kr * C::LROW + gr * 16) = av[i];
                 }
                 __builtin_amdgcn_s_waitcnt(0xC07F);  // lgkmcnt(0): this wave's LDS writes are done
-                shrink_mfma_fill<C, RM>(acc, xv, wl, kb, k_hi, g, li, r);
+                shrink_mfma_fill<C, RM, XE>(acc, xv, wl, kb, k_hi, g, li, r);
                 __builtin_amdgcn_s_waitcnt(0xC07F);  // LDS reads done before the next fill overwrites
             }
         } else {
@@ -274,7 +274,7 @@ __global__ __launch_bounds__(64 * kWavesPerBlock) void shrink_mfma_kernel(
 #pragma unroll
                 for (int st = 0; st < C::STEPS; ++st) xv[st] = load_x(kb + 32 * st + 8 * g);
                 __builtin_amdgcn_s_waitcnt(0xC07F);  // lgkmcnt(0): this wave's LDS writes are done
-                shrink_mfma_fill<C, RM>(acc, xv, wl, kb, k_hi, g, li, r);
+                shrink_mfma_fill<C, RM, XE>(acc, xv, wl, kb, k_hi, g, li, r);
                 __builtin_amdgcn_s_waitcnt(0xC07F);  // LDS reads done before the next fill overwrites
             }
         }
@@ -354,8 +354,8 @@ void shrink_plan(int d_in, int r_max, int *kc, int *ksplit) {
 
 namespace {
 
-template <bool X8>
-hipError_t launch_shrink_pools(const void *x, const ShrinkPools &pools, const int32_t *ranks,
+template <class X>
+hipError_t launch_shrink_pools(const X *x, const ShrinkPools &pools, const int32_t *ranks,
                                const int32_t *roff, int pool_rows, int pstride, int M, int d_in,
                                int r_max, int n_adapters, Seg seg, int kc, int ksplit,
                                hipStream_t s) {
@@ -371,7 +371,7 @@ hipError_t launch_shrink_pools(const void *x, const ShrinkPools &pools, const in
                        : (pstride & 7) != 0  ? kFlat
                                              : kVarW;
 #define LORA_SHRINK_ONE(RMV, LAY)                                                                \
-    launch(shrink_mfma_kernel<RMV, LAY, X8>, wgrid, wblock, 0, s, x, pools, ranks, roff, pool_rows,  \
+    launch(shrink_mfma_kernel<RMV, LAY, X>, wgrid, wblock, 0, s, static_cast<const void *>(x), pools, ranks, roff, pool_rows, \
            pstride, M, d_in, n_adapters, seg, ksplit, kc)
 #define LORA_SHRINK_LAUNCH(RMV)                                                                  \
     if (layout == kPadRM) LORA_SHRINK_ONE(RMV, kPadRM);                                          \
@@ -399,20 +399,25 @@ hipError_t launch_shrink(const uint16_t *x, const uint16_t *A, const int32_t *ra
     pools.A[0] = A;
     pools.partial[0] = partial;
     pools.n = 1;
-    return launch_shrink_pools<false>(x, pools, ranks, roff, pool_rows, pstride, M, d_in, r_max,
+    return launch_shrink_pools(x, pools, ranks, roff, pool_rows, pstride, M, d_in, r_max,
                                n_adapters, seg, kc, ksplit, s);
 }
 
-hipError_t launch_shrink_x8(const uint8_t *x8, const uint16_t *A, const int32_t *ranks,
-                            int pstride, int M, int d_in, int r_max, int n_adapters, Seg seg,
-                            float *partial, int kc, int ksplit, hipStream_t s) {
+template <class X>
+hipError_t launch_shrink_x8(const X *x8, const uint16_t *A, const int32_t *ranks, int pstride, int M,
+                            int d_in, int r_max, int n_adapters, Seg seg, float *partial, int kc,
+                            int ksplit, hipStream_t s) {
     ShrinkPools pools{};
     pools.A[0] = A;
     pools.partial[0] = partial;
     pools.n = 1;
-    return launch_shrink_pools<true>(x8, pools, ranks, nullptr, 0, pstride, M, d_in, r_max, n_adapters,
-                                     seg, kc, ksplit, s);
+    return launch_shrink_pools(x8, pools, ranks, nullptr, 0, pstride, M, d_in, r_max, n_adapters, seg, kc,
+                               ksplit, s);
 }
+template hipError_t launch_shrink_x8(const uint8_t *, const uint16_t *, const int32_t *, int, int, int, int,
+                                     int, Seg, float *, int, int, hipStream_t);
+template hipError_t launch_shrink_x8(const int8_t *, const uint16_t *, const int32_t *, int, int, int, int,
+                                     int, Seg, float *, int, int, hipStream_t);
 
 hipError_t launch_shrink_multi(const uint16_t *x, int n_proj, const uint16_t *const *A,
                                float *const *partial, const int32_t *ranks, int pstride, int M,
@@ -425,7 +430,7 @@ hipError_t launch_shrink_multi(const uint16_t *x, int n_proj, const uint16_t *co
         pools.partial[p] = partial[p];
     }
     pools.n = n_proj;
-    return launch_shrink_pools<false>(x, pools, ranks, nullptr, 0, pstride, M, d_in, r_max, n_adapters,
+    return launch_shrink_pools(x, pools, ranks, nullptr, 0, pstride, M, d_in, r_max, n_adapters,
                                seg, kc, ksplit, s);
 }
 

@@ -30,6 +30,7 @@ LORA_ROPE_HALF, LORA_ROPE_INTERLEAVED = 0, 1
 LORA_ROPE_PLAIN, LORA_ROPE_LINEAR, LORA_ROPE_NTK, LORA_ROPE_YARN = 0, 1, 2, 3
 LORA_ROPE_MAX_HEADS = LORA_ROPE_MAX_DIM = 1024
 LORA_ROPE_MAX_STRIDE = 1 << 28
+LORA_INT8_MAX_D_IN = (1 << 17) - 16
 LORA_MODE_AUTO, LORA_MODE_DECODE, LORA_MODE_PREFILL = 0, 1, 2
 LORA_MODE_CHECKED = 0x100  # OR-ed into a mode: sync, check ids and adapter tables on the host
 
@@ -47,7 +48,7 @@ EXPORTS = ("lora_max_tiles", "lora_workspace_bytes", "lora_build_segments", "lor
            "lora_moe_workspace_bytes", "lora_moe_linear", "lora_moe_linear_profiled",
            "lora_workspace_bytes_multi", "lora_linear_multi", "lora_linear_multi_profiled",
            "lora_rmsnorm", "lora_linear_act", "lora_fp8_workspace_bytes",
-           "lora_linear_fp8", "lora_rmsnorm_int8", "lora_quant_int8", "lora_rope", "lora_rope_freqs",
+           "lora_linear_fp8", "lora_int8_workspace_bytes", "lora_linear_int8", "lora_rmsnorm_int8", "lora_quant_int8", "lora_rope", "lora_rope_freqs",
            "lora_status_string", "lora_last_hip_error")
 
 
@@ -148,6 +149,10 @@ def _load():
     lib.lora_fp8_workspace_bytes.restype = S
     lib.lora_linear_fp8.argtypes = [P, P, P, P] + lib.lora_linear_act.argtypes[2:]
     lib.lora_linear_fp8.restype = ctypes.c_int
+    lib.lora_int8_workspace_bytes.argtypes = [I, I, I, I, I]
+    lib.lora_int8_workspace_bytes.restype = S
+    lib.lora_linear_int8.argtypes = lib.lora_linear_fp8.argtypes
+    lib.lora_linear_int8.restype = ctypes.c_int
     lib.lora_rmsnorm.argtypes = [P, P, P, ctypes.c_float, I, I, P, P, P, P, P]
     lib.lora_rmsnorm.restype = ctypes.c_int
     lib.lora_rmsnorm_int8.argtypes = lib.lora_rmsnorm.argtypes
@@ -550,6 +555,33 @@ def lora_linear_fp8(x8, x_scale, W8, w_scale, A, B, scale, ranks, ids, M: int, d
         None if segs is None else _seg_struct(segs), _epi_struct(epi, M, d_out, y_types),
         _buf(y, "y", M * d_out, y_types), y_dtype, mode, _buf(ws, "ws", ws_bytes, _U8), ws_bytes,
         _stream_here(stream)), "lora_linear_fp8")
+
+
+def lora_int8_workspace_bytes(M: int, d_in: int, d_out: int, r_max: int, n_adapters: int) -> int:
+    return int(_lib.lora_int8_workspace_bytes(M, d_in, d_out, r_max, n_adapters))
+
+
+def int8_workspace(M: int, d_in: int, d_out: int, r_max: int, n_adapters: int, device="cuda"):
+    """A uint8 device tensor of lora_int8_workspace_bytes() bytes (256-byte aligned by torch)."""
+    nbytes = lora_int8_workspace_bytes(M, d_in, d_out, r_max, n_adapters)
+    return torch.empty(max(nbytes, 256), dtype=torch.uint8, device=device), nbytes
+
+
+def lora_linear_int8(x8, x_scale, W8, w_scale, A, B, scale, ranks, ids, M: int, d_in: int,
+                     d_out: int, r_max: int, n_adapters: int, segs, epi, y, y_dtype: int, mode: int,
+                     ws, ws_bytes: int, stream=None) -> None:
+    """The layer on 8-bit integers x8[M, d_in] (scale per row) and W8[d_out, d_in] (scale per column:
+    int8 tensors), followed by epi (a lora_epilogue, or None)."""
+    y_types = _F32 if y_dtype == LORA_F32 else _BF16
+    _check(_lib.lora_linear_int8(
+        _buf(x8, "x8", M * d_in, _I8), _buf(x_scale, "x_scale", M, _F32),
+        _buf(W8, "W8", d_in * d_out, _I8), _buf(w_scale, "w_scale", d_out, _F32),
+        _buf(A, "A", n_adapters * d_in * r_max, _BF16), _buf(B, "B", n_adapters * r_max * d_out, _BF16),
+        _buf(scale, "scale", n_adapters, _F32), _buf(ranks, "ranks", n_adapters, _I32),
+        _buf(ids, "ids", M, _I32), M, d_in, d_out, r_max, n_adapters,
+        None if segs is None else _seg_struct(segs), _epi_struct(epi, M, d_out, y_types),
+        _buf(y, "y", M * d_out, y_types), y_dtype, mode, _buf(ws, "ws", ws_bytes, _U8), ws_bytes,
+        _stream_here(stream)), "lora_linear_int8")
 
 
 def lora_rmsnorm(x, residual, weight, eps: float, M: int, d: int, sum, y, y8, y_scale,
