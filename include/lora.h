@@ -566,6 +566,40 @@ lora_status_t lora_moe_linear_profiled(const void *x, const void *W, const void 
                                        const char **kernel_names, int32_t max_kernels,
                                        int32_t *n_kernels);
 
+/* A whole mixture-of-experts layer for the tokens of a decode batch, every projection of every expert
+ * with the token's adapter as in lora_moe_linear, the routing (topk_ids, topk_w) as there too.  With
+ * e = topk_ids[m][j], i = ids[m] and v P[e] = v W[e] + scale_i (v A[i][e]) B[i][e]:
+ *     h[m][j] = act(x[m] gate[e]) * (x[m] up[e])
+ *     y[m]    = residual[m] + sum_j topk_w[m][j] (h[m][j] down[e])      (one rounding, into y's type)
+ * A slot with no expert (-1, or outside [0, n_experts)) adds nothing; an expert that a token names
+ * twice counts twice.  Everything is summed in fp32; h enters the down projection rounded to bf16 with
+ * y in bf16, and with all of its 24 bits (three bf16 parts) with y in fp32.
+ * weights: a HOST struct read during the call, of device arrays: gate and up W [n_experts][d][d_ff],
+ * A [n_adapters][n_experts][d][r_max], B [n_adapters][n_experts][r_max][d_ff]; down the same with d and
+ * d_ff exchanged; all required.  x: bf16 [M][d].  residual: [M][d] in y's type, y itself or apart from
+ * it; NULL: 0.  topk_w NULL: weight 1; ranks NULL: all r_max.  Limits as lora_moe_linear's, but d and
+ * d_ff multiples of 16, at least 128.  Modes, checked mode and errors as lora_moe_linear's;
+ * LORA_ERR_VALUE for an unknown activation.  ws: lora_moe_layer_workspace_bytes() bytes of the same
+ * sizes, 256-byte aligned.  Four launches, no allocation, no host synchronisation (except checked mode). */
+typedef struct {
+    const void *W;
+    const void *A;
+    const void *B;
+} lora_moe_proj_t;
+typedef struct {
+    lora_moe_proj_t gate;
+    lora_moe_proj_t up;
+    lora_moe_proj_t down;
+} lora_moe_weights_t;
+size_t lora_moe_layer_workspace_bytes(int32_t M, int32_t top_k, int32_t n_experts, int32_t d, int32_t d_ff,
+                                      int32_t r_max, int32_t n_adapters);
+lora_status_t lora_moe_layer(const void *x, const lora_moe_weights_t *weights, const float *scale,
+                             const int32_t *ranks, const int32_t *ids, const int32_t *topk_ids,
+                             const float *topk_w, const void *residual, int32_t M, int32_t top_k,
+                             int32_t n_experts, int32_t d, int32_t d_ff, int32_t r_max,
+                             int32_t n_adapters, lora_act_t act, void *y, lora_dtype_t y_dtype,
+                             lora_mode_t mode, void *ws, size_t ws_bytes, void *stream);
+
 /* Measurement aid: lora_linear_profiled for lora_linear_compact's arguments. */
 lora_status_t lora_linear_compact_profiled(
     const void *x, const void *W, const void *A, const void *B, const float *scale,

@@ -23,7 +23,7 @@ LIB = os.path.join(PKG, "liblora_mi355x.so")
 ARCH = "gfx950"
 
 SOURCES = ["segments.hip", "shrink.hip", "expand.hip", "gemm.hip", "gemm_big.hip", "decode_gemm.hip", "moe.hip", "noalloc.hip", "norm.hip",
-           "gemm_fp8.hip", "rope.hip", "api.cpp"]
+           "gemm_fp8.hip", "rope.hip", "moe_layer.hip", "api.cpp"]
 
 COMMON_FLAGS = [
     f"--offload-arch={ARCH}", "-O3", "-fPIC", "-std=c++17", "-Wall",

@@ -1080,14 +1080,16 @@ hipError_t run_moe(const void *x, const void *W, const void *A, const void *B, c
     float *tpart = reinterpret_cast<float *>(c);
     MoeGemmArgs g{};
     g.x = static_cast<const uint16_t *>(x);
-    g.W = static_cast<const uint16_t *>(W);
-    g.A = static_cast<const uint16_t *>(A);
+    g.W[0] = static_cast<const uint16_t *>(W);
+    g.A[0] = static_cast<const uint16_t *>(A);
+    g.n_proj = 1;
+    g.rows = kMoeToken;
     g.topk_ids = topk_ids;
     g.ids = ids;
     g.P = P; g.top_k = top_k; g.E = n_experts; g.K = d_in; g.N = d_out;
     g.r_stride = r_max; g.n_adapters = n_adapters;
-    g.partial = partial;
-    g.tpart = tpart;
+    g.partial[0] = partial;
+    g.tpart[0] = tpart;
     hipError_t e = launch_moe_gemm(p, g, s);
     if (e != hipSuccess) return e;
     mark(mk, "moe_gemm");
@@ -1156,6 +1158,135 @@ lora_status_t lora_moe_linear_profiled(const void *x, const void *W, const void 
                            d_in, d_out, r_max, n_adapters, y, y_dtype, ws, (hipStream_t)stream, mk);
         },
         kernel_ms, kernel_names, max_kernels, n_kernels);
+}
+
+}  // extern "C"
+
+namespace {
+
+// ---- a whole expert layer ------------------------------------------------------------------
+
+struct MoeLayerDims {
+    int32_t M, top_k, E, d, ff, r_max, n_adapters;
+    int32_t pairs() const { return M * top_k; }
+};
+
+lora_status_t check_moe_layer_sizes(const MoeLayerDims &z) {
+    if (z.M < 0 || z.top_k < 1 || z.top_k > 64 || z.E < 1 || z.E > 4096 ||
+        (int64_t)z.M * z.top_k > LORA_MOE_MAX_PAIRS || z.n_adapters < 1 || z.n_adapters > LORA_MAX_ADAPTERS)
+        return LORA_ERR_SHAPE;
+    for (const int32_t k : {z.d, z.ff})
+        if (!dim_ok(k) || k % 16 != 0 || k < 128) return LORA_ERR_SHAPE;
+    if (z.r_max < 8 || z.r_max > 64 || z.r_max % 8 != 0) return LORA_ERR_RANK;
+    return LORA_OK;
+}
+
+// The workspace: the partial sums of gate and up, then of down (the same memory: each is read before
+// the other is written), t's parts alike, and the hidden rows.
+struct MoeLayerPlan {
+    MoePlan in, out;
+    size_t partial, tpart, hidden, bytes;  // bytes of each part
+};
+MoeLayerPlan moe_layer_plan(const MoeLayerDims &z) {
+    MoeLayerPlan p;
+    p.in = moe_plan(z.M, z.top_k, z.E, z.d, z.ff, z.r_max, z.n_adapters, 2);
+    p.out = moe_plan(z.M, z.top_k, z.E, z.ff, z.d, z.r_max, z.n_adapters);
+    const size_t a = 2 * round_up(moe_partial_floats(p.in, z.pairs()) * 4),
+                 b = round_up(moe_partial_floats(p.out, z.pairs()) * 4),
+                 ta = 2 * round_up(moe_tpart_floats(p.in, z.pairs()) * 4),
+                 tb = round_up(moe_tpart_floats(p.out, z.pairs()) * 4);
+    p.partial = a > b ? a : b;
+    p.tpart = ta > tb ? ta : tb;
+    p.hidden = round_up((size_t)z.pairs() * z.ff * 2 * 4);  // (four bf16 parts, with y in fp32)
+    p.bytes = p.partial + p.tpart + p.hidden;
+    return p;
+}
+
+// The launch sequence of lora_moe_layer (arguments validated, M > 0): gate and up with their adapters'
+// shrinks, the hidden rows, down with its shrink, the sum over each token's slots.
+hipError_t run_moe_layer(const MoeLayerDims &z, const void *x, const lora_moe_weights_t &w, const float *scale,
+                         const int32_t *ranks, const int32_t *ids, const int32_t *topk_ids, const float *topk_w,
+                         const void *residual, lora_act_t act, void *y, bool y_f32, void *ws, hipStream_t s) {
+    const MoeLayerPlan pl = moe_layer_plan(z);
+    const int P = z.pairs();
+    char *const c = static_cast<char *>(ws);
+    auto floats = [](char *p) { return reinterpret_cast<float *>(p); };
+    auto bf16 = [](const void *p) { return static_cast<const uint16_t *>(p); };
+    char *const tc = c + pl.partial;
+    uint16_t *const h = reinterpret_cast<uint16_t *>(tc + pl.tpart);
+    MoeGemmArgs g{};
+    g.x = bf16(x);
+    g.W[0] = bf16(w.gate.W); g.W[1] = bf16(w.up.W);
+    g.A[0] = bf16(w.gate.A); g.A[1] = bf16(w.up.A);
+    g.topk_ids = topk_ids;
+    g.ids = ids;
+    g.P = P; g.top_k = z.top_k; g.E = z.E; g.K = z.d; g.N = z.ff;
+    g.r_stride = z.r_max; g.n_adapters = z.n_adapters; g.n_proj = 2;
+    g.rows = kMoeToken;
+    g.partial[0] = floats(c);
+    g.partial[1] = floats(c + round_up(moe_partial_floats(pl.in, P) * 4));
+    g.tpart[0] = floats(tc);
+    g.tpart[1] = floats(tc + round_up(moe_tpart_floats(pl.in, P) * 4));
+    hipError_t e = launch_moe_gemm(pl.in, g, s);
+    if (e != hipSuccess) return e;
+    const MoeLayerArgs a{scale, ranks, topk_ids, ids, topk_w, P, z.top_k, z.E, z.r_max, z.n_adapters};
+    if ((e = launch_moe_hidden(pl.in, a, MoeSums{g.partial[0], g.tpart[0], bf16(w.gate.B)},
+                               MoeSums{g.partial[1], g.tpart[1], bf16(w.up.B)}, z.ff, act, y_f32, h, s)) !=
+        hipSuccess)
+        return e;
+    g.x = h;
+    g.W[0] = bf16(w.down.W);
+    g.A[0] = bf16(w.down.A);
+    g.K = z.ff; g.N = z.d; g.n_proj = 1;
+    g.rows = y_f32 ? kMoeParts : kMoePair;
+    if ((e = launch_moe_gemm(pl.out, g, s)) != hipSuccess) return e;
+    return launch_moe_out(pl.out, a, MoeSums{g.partial[0], g.tpart[0], bf16(w.down.B)}, z.M, z.d, residual, y,
+                          y_f32, s);
+}
+
+}  // namespace
+
+extern "C" {
+
+size_t lora_moe_layer_workspace_bytes(int32_t M, int32_t top_k, int32_t n_experts, int32_t d, int32_t d_ff,
+                                      int32_t r_max, int32_t n_adapters) {
+    const MoeLayerDims z{M, top_k, n_experts, d, d_ff, r_max, n_adapters};
+    if (check_moe_layer_sizes(z) != LORA_OK || M == 0) return 0;
+    return moe_layer_plan(z).bytes;
+}
+
+lora_status_t lora_moe_layer(const void *x, const lora_moe_weights_t *weights, const float *scale,
+                             const int32_t *ranks, const int32_t *ids, const int32_t *topk_ids,
+                             const float *topk_w, const void *residual, int32_t M, int32_t top_k,
+                             int32_t n_experts, int32_t d, int32_t d_ff, int32_t r_max,
+                             int32_t n_adapters, lora_act_t act, void *y, lora_dtype_t y_dtype,
+                             lora_mode_t mode, void *ws, size_t ws_bytes, void *stream) {
+    const MoeLayerDims z{M, top_k, n_experts, d, d_ff, r_max, n_adapters};
+    lora_status_t st = check_moe_layer_sizes(z);
+    if (st != LORA_OK) return st;
+    if (act < LORA_ACT_NONE || act > LORA_ACT_GELU_TANH) return LORA_ERR_VALUE;
+    if (y_dtype != LORA_BF16 && y_dtype != LORA_F32) return LORA_ERR_DTYPE;
+    const int bm = mode & ~LORA_MODE_CHECKED;
+    if (bm != LORA_MODE_AUTO && bm != LORA_MODE_DECODE) return LORA_ERR_MODE;
+    if (M == 0) return LORA_OK;
+    if (!x || !weights || !scale || !ids || !topk_ids || !y || !ws) return LORA_ERR_NULL;
+    const lora_moe_weights_t w = *weights;
+    for (const lora_moe_proj_t *p : {&w.gate, &w.up, &w.down}) {
+        if (!p->W || !p->A || !p->B) return LORA_ERR_NULL;
+        if (!aligned(p->W, 16) || !aligned(p->A, 16) || !aligned(p->B, 16)) return LORA_ERR_ALIGN;
+    }
+    if (!aligned(x, 16) || !aligned(y, 16) || !aligned(residual, 16) || !aligned(ws, kAlign) ||
+        !aligned(scale, 4) || !aligned(ids, 4) || !aligned(topk_ids, 4) || !aligned(topk_w, 4) ||
+        !aligned(ranks, 4))
+        return LORA_ERR_ALIGN;
+    if (ws_bytes < moe_layer_plan(z).bytes) return LORA_ERR_WORKSPACE;
+    clear_stale_error();
+    if ((mode & LORA_MODE_CHECKED) &&
+        (st = check_moe_tables(ids, ranks, topk_ids, M, top_k, n_experts, r_max, n_adapters,
+                               (hipStream_t)stream)) != LORA_OK)
+        return st;
+    return hip_status(run_moe_layer(z, x, w, scale, ranks, ids, topk_ids, topk_w, residual, act, y,
+                                    y_dtype == LORA_F32, ws, (hipStream_t)stream));
 }
 
 lora_status_t lora_linear_act(const void *x, const void *W, const void *A, const void *B,

@@ -284,16 +284,6 @@ __device__ __forceinline__ void mfma_run(f32x16_t (&acc)[C::TM][C::TN], const ui
     }
 }
 
-// f's leading bf16 part: rounded to nearest, but a finite f stays finite (the largest ones are cut off
-// instead).  What it leaves of f: nothing of an infinity or a NaN.
-__device__ __forceinline__ uint32_t bf16_part(float f) {
-    const uint32_t h = f32_to_bf16_rne(f);
-    return (h & 0x7FFFu) == 0x7F80u ? __float_as_uint(f) >> 16 : h;
-}
-__device__ __forceinline__ float bf16_rest(float f) {
-    const uint32_t h = bf16_part(f);
-    return (h & 0x7F80u) == 0x7F80u ? 0.0f : f - __uint_as_float(h << 16);
-}
 __device__ __forceinline__ uint4 bf16_parts8(const float (&f)[8]) {
     uint32_t w[4];
 #pragma unroll

@@ -41,6 +41,17 @@ __device__ __forceinline__ uint32_t pack_bf16x2(float lo, float hi) {
     return f32_to_bf16_rne(lo) | (f32_to_bf16_rne(hi) << 16);
 }
 
+// f's leading bf16 part: rounded to nearest, but a finite f stays finite (the largest ones are cut off
+// instead).  What it leaves of f: nothing of an infinity or a NaN.
+__device__ __forceinline__ uint32_t bf16_part(float f) {
+    const uint32_t h = f32_to_bf16_rne(f);
+    return (h & 0x7FFFu) == 0x7F80u ? __float_as_uint(f) >> 16 : h;
+}
+__device__ __forceinline__ float bf16_rest(float f) {
+    const uint32_t h = bf16_part(f);
+    return (h & 0x7F80u) == 0x7F80u ? 0.0f : f - __uint_as_float(h << 16);
+}
+
 // 8 bf16 (one 16-byte vector) -> 8 floats
 __device__ __forceinline__ void unpack8(const uint4 v, float f[8]) {
     f[0] = bf16_lo(v.x); f[1] = bf16_hi(v.x);
@@ -383,20 +394,26 @@ void shrink_plan(int d_in, int r_max, int *kc, int *ksplit);
 struct MoePlan {
     int rm, bm, n_tn, n_lt, ks, k_per_split, np;
 };
-MoePlan moe_plan(int M, int top_k, int E, int K, int N, int r_max, int n_adapters);
+// n_proj: projections that share the rows, an expert layer's gate and up in one launch.
+MoePlan moe_plan(int M, int top_k, int E, int K, int N, int r_max, int n_adapters, int n_proj = 1);
 size_t moe_partial_floats(const MoePlan &p, int P);  // [ks][P][np]
 size_t moe_tpart_floats(const MoePlan &p, int P);    // [ks][P][rm]
 
+// The rows of x that a (token, slot) pair multiplies: its token's, its own, or its own row in four
+// bf16 parts that add up to it (rows 4 p .. 4 p + 3).
+enum MoeRows { kMoeToken, kMoePair, kMoeParts };
+
 struct MoeGemmArgs {
-    const uint16_t *x;         // [M][K]
-    const uint16_t *W;         // [E][K][N]
-    const uint16_t *A;         // [n_adapters][E][K][r_stride]
+    const uint16_t *x;         // [M][K], [P][K] or [4 P][K]
+    const uint16_t *W[2];      // n_proj of them: [E][K][N]
+    const uint16_t *A[2];      // [n_adapters][E][K][r_stride]
     const int32_t *topk_ids;   // [P] = [M][top_k]
     const int32_t *ids;        // [M]
-    int P, top_k, E, K, N, r_stride, n_adapters;
-    int n_tn, n_lt, k_per_split, np;  // set from the plan by launch_moe_gemm
-    float *partial;            // [ks][P][np]
-    float *tpart;              // [ks][P][rm]
+    int P, top_k, E, K, N, r_stride, n_adapters, n_proj;
+    MoeRows rows;
+    int n_slots, n_tn, n_lt, k_per_split, np;  // set from the plan by launch_moe_gemm
+    float *partial[2];         // [ks][P][np]
+    float *tpart[2];           // [ks][P][rm]
 };
 struct MoeReduceArgs {
     const float *partial, *tpart;
@@ -412,6 +429,28 @@ struct MoeReduceArgs {
 };
 hipError_t launch_moe_gemm(const MoePlan &p, const MoeGemmArgs &a, hipStream_t s);
 hipError_t launch_moe_reduce(const MoePlan &p, const MoeReduceArgs &a, bool y_f32, hipStream_t s);
+
+// The reductions of a whole expert layer (csrc/moe_layer.hip).  One projection's sums and the rest of
+// its adapter:
+struct MoeSums {
+    const float *partial, *tpart;  // [ks][P][np], [ks][P][rm]
+    const uint16_t *B;             // [n_adapters][E][r_stride][N]
+};
+struct MoeLayerArgs {
+    const float *scale;        // [n_adapters]
+    const int32_t *ranks;      // [n_adapters] or nullptr (= r_stride)
+    const int32_t *topk_ids;   // [P]
+    const int32_t *ids;        // [M]
+    const float *topk_w;       // [P] or nullptr (= 1)
+    int P, top_k, E, r_stride, n_adapters;
+};
+// h[p] = act(gate) * up of every pair with an expert, in bf16 ([P][N]) or (parts) in four bf16 parts
+// ([4 P][N]).
+hipError_t launch_moe_hidden(const MoePlan &p, const MoeLayerArgs &a, const MoeSums &gate, const MoeSums &up,
+                             int N, int act, bool parts, uint16_t *h, hipStream_t s);
+// y[m] = residual[m] + the sum over the token's slots of topk_w * down.
+hipError_t launch_moe_out(const MoePlan &p, const MoeLayerArgs &a, const MoeSums &down, int M, int N,
+                          const void *residual, void *y, bool y_f32, hipStream_t s);
 
 // ---- the layer on 8-bit operands (csrc/gemm_fp8.hip) ------------------------------------------
 // X: E4M3 codes (uint8_t, lora_linear_fp8) or integers (int8_t, lora_linear_int8).

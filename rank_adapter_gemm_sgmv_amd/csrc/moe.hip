@@ -24,6 +24,9 @@
 //    A[i][e] is read once.  Pairs are taken in blocks of BM rows; a block writes
 //    partial[split][pair][column] (W tiles) or tpart[split][pair][0 .. RM) (adapter tiles,
 //    each pair only its own adapter's columns).
+//  * The same kernel serves a whole expert layer (lora_moe_layer): gate and up side by side in one
+//    launch, and the down projection on each pair's own hidden row, or on four bf16 parts of it,
+//    which meet W in the same pass and add up in the partial tile.
 //  * moe_reduce_kernel, block (column chunk, pair): the splits added in order, t summed over
 //    the splits in order, scale_i t B[i][e] added, the routing weight applied, rounded once
 //    into y.  No atomics: results do not depend on scheduling.
@@ -49,7 +52,40 @@ __device__ __forceinline__ int moe_slot(const MoeShared &sh, int i) {
     return sh.wpre[w] + __popc(sh.bits[w] & ((1u << (i & 31)) - 1u));
 }
 
-template <class C, int RM>
+// The a-th expert, ascending, that some pair is routed to (-1: fewer are).  Only batches with fewer
+// pairs than experts ask; the others give every expert its workgroups.
+__device__ __forceinline__ int moe_routed_expert(MoeShared &sh, const int32_t *topk_ids, int P, int E, int a,
+                                                 int tid, int lane) {
+    const int nw = (E + 31) >> 5;  // at most 128 words
+    for (int w = tid; w < nw; w += kThreads) sh.bits[w] = 0u;
+    __syncthreads();
+    for (int p = tid; p < P; p += kThreads) {
+        const int e = topk_ids[p];
+        if (e >= 0 && e < E) atomicOr(&sh.bits[e >> 5], 1u << (e & 31));
+    }
+    __syncthreads();
+    // every wave finds it from the words' counts: two words per lane
+    const uint32_t b0 = 2 * lane < nw ? sh.bits[2 * lane] : 0u, b1 = 2 * lane + 1 < nw ? sh.bits[2 * lane + 1] : 0u;
+    const int c0 = __popc(b0), c = c0 + __popc(b1);
+    int v = c;
+#pragma unroll
+    for (int d = 1; d < 64; d <<= 1) {
+        const int u = __shfl_up(v, d, 64);
+        if (lane >= d) v += u;
+    }
+    int k = a - (v - c), e = -1;
+    if (k >= 0 && k < c) {
+        uint32_t bw = k < c0 ? b0 : b1;
+        const int w = 2 * lane + (k < c0 ? 0 : 1);
+        for (k -= k < c0 ? 0 : c0; k > 0; --k) bw &= bw - 1u;
+        e = 32 * w + __ffs(bw) - 1;
+    }
+    const uint64_t found = __ballot(e >= 0);
+    __syncthreads();  // bits is used again
+    return found ? __builtin_amdgcn_readlane(e, __ffsll((unsigned long long)found) - 1) : -1;
+}
+
+template <class C, int RM, MoeRows ROWS>
 __global__ __launch_bounds__(kThreads) void moe_gemm_kernel(MoeGemmArgs a) {
     __shared__ __attribute__((aligned(1024))) uint4 lds[kWaves * C::WAVE];
     __shared__ MoeShared sh;
@@ -58,11 +94,22 @@ __global__ __launch_bounds__(kThreads) void moe_gemm_kernel(MoeGemmArgs a) {
 
     const int tid = threadIdx.x, lane = tid & 63;
     const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+    constexpr int PARTS = ROWS == kMoeParts ? 4 : 1;
     const int n_cols = a.n_tn + a.n_lt;
-    const int lin = blockIdx.x;
-    const int ct = lin % n_cols;
-    const int e = (lin / n_cols) % a.E;
-    const int split = lin / (n_cols * a.E);
+    int lin = blockIdx.x;
+    int ct = lin % (n_cols * a.n_proj);
+    lin /= n_cols * a.n_proj;
+    const int split = lin / a.n_slots;
+    int e = lin % a.n_slots;
+    if (a.n_slots < a.E) {
+        e = moe_routed_expert(sh, a.topk_ids, a.P, a.E, e, tid, lane);
+        if (e < 0) return;  // whole workgroup
+    }
+    // gate and up: their column tiles side by side
+    const bool second = ct >= n_cols;
+    if (second) ct -= n_cols;
+    const uint16_t *const W = second ? a.W[1] : a.W[0], *const A = second ? a.A[1] : a.A[0];
+    float *const partial = second ? a.partial[1] : a.partial[0], *const tpart = second ? a.tpart[1] : a.tpart[0];
     const uint64_t below = lane == 0 ? 0ull : (~0ull >> (64 - lane));
 
     // 1. this expert's pairs, in pair order (count is uniform in the workgroup)
@@ -147,7 +194,7 @@ __global__ __launch_bounds__(kThreads) void moe_gemm_kernel(MoeGemmArgs a) {
     size_t ldw;
     const int n0 = ct * kBN;
     if (!adapter_tile) {
-        const uint16_t *We = a.W + (size_t)e * a.K * a.N;
+        const uint16_t *We = W + (size_t)e * a.K * a.N;
 #pragma unroll
         for (int q = 0; q < C::WINS; ++q) {
             const int r = 4 * q + (lane >> 4);
@@ -164,7 +211,7 @@ __global__ __launch_bounds__(kThreads) void moe_gemm_kernel(MoeGemmArgs a) {
             if (ad < 0) ad = sh.tile_ad[0];  // an empty slot reads a valid adapter, unused
             int cc = col % RM;
             if (cc >= a.r_stride) cc = 0;     // bucket columns past r_max: unused
-            src.wp[q] = a.A + (((size_t)ad * a.E + e) * a.K + r) * a.r_stride + cc;
+            src.wp[q] = A + (((size_t)ad * a.E + e) * a.K + r) * a.r_stride + cc;
         }
         ldw = (size_t)a.r_stride;
     }
@@ -175,7 +222,7 @@ __global__ __launch_bounds__(kThreads) void moe_gemm_kernel(MoeGemmArgs a) {
     const int kw0 = min(ks1, ks0 + wave * per_wave);
     const int kw1 = min(ks1, kw0 + per_wave);
     const int nst = (kw1 - kw0) / kBKW;
-    const int n_rb = (count + C::BM - 1) / C::BM;
+    const int n_rb = (count * PARTS + C::BM - 1) / C::BM;
     const int col = tid & 127;
 
     for (int rb = 0; rb < n_rb; ++rb) {
@@ -185,8 +232,10 @@ __global__ __launch_bounds__(kThreads) void moe_gemm_kernel(MoeGemmArgs a) {
         for (int q = 0; q < C::XINS; ++q) {
             const int row = 8 * q + (lane >> 3);
             const int lc = (lane & 7) ^ (lane >> 3);
-            const int p = sh.rows[min(rb * C::BM + row, count - 1)];
-            src.xp[q] = a.x + (size_t)(p / a.top_k) * a.K + lc * 8;
+            const int j = rb * C::BM + row;
+            const int p = sh.rows[min(j / PARTS, count - 1)];
+            const int xr = ROWS == kMoeToken ? p / a.top_k : PARTS * p + j % PARTS;
+            src.xp[q] = a.x + (size_t)xr * a.K + lc * 8;
         }
         f32x16_t acc[C::TM][C::TN];
 #pragma unroll
@@ -206,19 +255,20 @@ __global__ __launch_bounds__(kThreads) void moe_gemm_kernel(MoeGemmArgs a) {
         for (int q = 0; q < C::BM / 8; ++q) {
             const int g = (tid >> 7) + 2 * q;  // rows 4 g .. 4 g + 3 of the block
             const float4 s = reduce_waves_group<C>(red, g, col);
-            const float sv[4] = {s.x, s.y, s.z, s.w};
+            // (four parts of one pair: the last is zeros)
+            const float sv[4] = {PARTS == 4 ? s.x + (s.y + s.z) : s.x, s.y, s.z, s.w};
 #pragma unroll
-            for (int v = 0; v < 4; ++v) {
-                const int j = rb * C::BM + 4 * g + v;
+            for (int v = 0; v < 4 / PARTS; ++v) {
+                const int j = (rb * C::BM + 4 * g) / PARTS + v;
                 if (j >= count) continue;
                 const int p = sh.rows[j];
                 if (!adapter_tile) {
-                    a.partial[((size_t)split * a.P + p) * a.np + n0 + col] = sv[v];
+                    partial[((size_t)split * a.P + p) * a.np + n0 + col] = sv[v];
                 } else {
                     const int i = a.ids[p / a.top_k];
                     if (i < 0 || i >= a.n_adapters) continue;
                     const int sl = moe_slot(sh, i) - lt * APT;
-                    if (sl == col / RM) a.tpart[((size_t)split * a.P + p) * RM + col % RM] = sv[v];
+                    if (sl == col / RM) tpart[((size_t)split * a.P + p) * RM + col % RM] = sv[v];
                 }
             }
         }
@@ -311,7 +361,7 @@ __global__ __launch_bounds__(256) void moe_reduce_kernel(MoeReduceArgs a) {
 
 }  // namespace
 
-MoePlan moe_plan(int M, int top_k, int E, int K, int N, int r_max, int n_adapters) {
+MoePlan moe_plan(int M, int top_k, int E, int K, int N, int r_max, int n_adapters, int n_proj) {
     MoePlan p;
     const int P = M * top_k;
     p.rm = rank_bucket(r_max);
@@ -323,7 +373,7 @@ MoePlan moe_plan(int M, int top_k, int E, int K, int N, int r_max, int n_adapter
     p.n_lt = (distinct + apt - 1) / apt;
     // splits of K so that the W tiles of the experts that can be routed to fill the chip
     // about twice (at most 16 splits, each a multiple of 64 deep)
-    const long active = (long)(E < P ? E : P) * p.n_tn;
+    const long active = (long)(E < P ? E : P) * p.n_tn * n_proj;
     int ks = (int)((512 + active - 1) / active);
     const int kq = (K + kBKW * kWaves - 1) / (kBKW * kWaves);
     if (ks < 1) ks = 1;
@@ -338,7 +388,7 @@ size_t moe_partial_floats(const MoePlan &p, int P) { return (size_t)p.ks * P * p
 size_t moe_tpart_floats(const MoePlan &p, int P) { return (size_t)p.ks * P * p.rm; }
 
 hipError_t launch_moe_gemm(const MoePlan &p, const MoeGemmArgs &args, hipStream_t s) {
-    if (args.P < 1 || args.P > LORA_MOE_MAX_PAIRS || args.K % 32 != 0 || args.K < 128 ||
+    if (args.P < 1 || args.P > LORA_MOE_MAX_PAIRS || args.K % 16 != 0 || args.K < 128 || args.n_proj < 1 || args.n_proj > 2 ||
         args.N < 8 || args.N % 8 != 0 || args.r_stride % 8 != 0 || args.r_stride > p.rm ||
         args.n_adapters > LORA_MAX_ADAPTERS || p.bm != 32)
         return hipErrorInvalidValue;
@@ -347,13 +397,23 @@ hipError_t launch_moe_gemm(const MoePlan &p, const MoeGemmArgs &args, hipStream_
     a.n_lt = p.n_lt;
     a.k_per_split = p.k_per_split;
     a.np = p.np;
-    const dim3 grid((unsigned)((long)p.ks * a.E * (p.n_tn + p.n_lt)));
+    // workgroups for as many experts as the pairs can name
+    a.n_slots = a.E < a.P ? a.E : a.P;
+    const dim3 grid((unsigned)((long)p.ks * a.n_slots * a.n_proj * (p.n_tn + p.n_lt)));
+#define MOE_GEMM(RMX)                                                                            \
+    if (a.rows == kMoeToken)                                                                     \
+        launch(moe_gemm_kernel<Dec<32>, RMX, kMoeToken>, grid, dim3(kThreads), 0, s, a);         \
+    else if (a.rows == kMoePair)                                                                 \
+        launch(moe_gemm_kernel<Dec<32>, RMX, kMoePair>, grid, dim3(kThreads), 0, s, a);          \
+    else                                                                                         \
+        launch(moe_gemm_kernel<Dec<32>, RMX, kMoeParts>, grid, dim3(kThreads), 0, s, a)
     switch (p.rm) {
-        case 8: launch(moe_gemm_kernel<Dec<32>, 8>, grid, dim3(kThreads), 0, s, a); break;
-        case 16: launch(moe_gemm_kernel<Dec<32>, 16>, grid, dim3(kThreads), 0, s, a); break;
-        case 32: launch(moe_gemm_kernel<Dec<32>, 32>, grid, dim3(kThreads), 0, s, a); break;
-        default: launch(moe_gemm_kernel<Dec<32>, 64>, grid, dim3(kThreads), 0, s, a); break;
+        case 8: MOE_GEMM(8); break;
+        case 16: MOE_GEMM(16); break;
+        case 32: MOE_GEMM(32); break;
+        default: MOE_GEMM(64); break;
     }
+#undef MOE_GEMM
     return hipGetLastError();
 }
 

@@ -49,6 +49,7 @@ EXPORTS = ("lora_max_tiles", "lora_workspace_bytes", "lora_build_segments", "lor
            "lora_workspace_bytes_multi", "lora_linear_multi", "lora_linear_multi_profiled",
            "lora_rmsnorm", "lora_linear_act", "lora_fp8_workspace_bytes",
            "lora_linear_fp8", "lora_int8_workspace_bytes", "lora_linear_int8", "lora_rmsnorm_int8", "lora_quant_int8", "lora_rope", "lora_rope_freqs",
+           "lora_moe_layer_workspace_bytes", "lora_moe_layer",
            "lora_status_string", "lora_last_hip_error")
 
 
@@ -70,6 +71,14 @@ class lora_segments_t(ctypes.Structure):
 class lora_epilogue_t(ctypes.Structure):
     _fields_ = [("bias", ctypes.c_void_p), ("mul", ctypes.c_void_p),
                 ("residual", ctypes.c_void_p), ("act", ctypes.c_int32)]
+
+
+class lora_moe_proj_t(ctypes.Structure):
+    _fields_ = [("W", ctypes.c_void_p), ("A", ctypes.c_void_p), ("B", ctypes.c_void_p)]
+
+
+class lora_moe_weights_t(ctypes.Structure):
+    _fields_ = [("gate", lora_moe_proj_t), ("up", lora_moe_proj_t), ("down", lora_moe_proj_t)]
 
 
 def _load():
@@ -119,6 +128,11 @@ def _load():
     lib.lora_moe_linear_profiled.argtypes = lib.lora_moe_linear.argtypes + [
         ctypes.POINTER(ctypes.c_float), ctypes.POINTER(ctypes.c_char_p), I, ctypes.POINTER(I)]
     lib.lora_moe_linear_profiled.restype = ctypes.c_int
+    lib.lora_moe_layer_workspace_bytes.argtypes = [I, I, I, I, I, I, I]
+    lib.lora_moe_layer_workspace_bytes.restype = S
+    lib.lora_moe_layer.argtypes = [P, ctypes.POINTER(lora_moe_weights_t), P, P, P, P, P, P, I, I, I, I, I,
+                                   I, I, ctypes.c_int, P, ctypes.c_int, ctypes.c_int, P, S, P]
+    lib.lora_moe_layer.restype = ctypes.c_int
     lib.lora_linear_noalloc.argtypes = lib.lora_linear.argtypes[:16] + [P]
     lib.lora_linear_noalloc.restype = ctypes.c_int
     lib.lora_linear_profiled.argtypes = lib.lora_linear.argtypes + [
@@ -528,6 +542,56 @@ def lora_linear_act(x, W, A, B, scale, ranks, ids, M: int, d_in: int, d_out: int
         None if segs is None else _seg_struct(segs), _epi_struct(epi, M, d_out, y_types),
         _buf(y, "y", M * d_out, y_types), y_dtype, mode, _buf(ws, "ws", ws_bytes, _U8), ws_bytes,
         _stream_here(stream)), "lora_linear_act")
+
+
+def lora_moe_layer_workspace_bytes(M: int, top_k: int, n_experts: int, d: int, d_ff: int, r_max: int,
+                                   n_adapters: int) -> int:
+    return int(_lib.lora_moe_layer_workspace_bytes(M, top_k, n_experts, d, d_ff, r_max, n_adapters))
+
+
+def moe_layer_workspace(M: int, top_k: int, n_experts: int, d: int, d_ff: int, r_max: int,
+                        n_adapters: int, device="cuda"):
+    """A uint8 device tensor of lora_moe_layer_workspace_bytes() bytes (256-byte aligned by torch)."""
+    nbytes = lora_moe_layer_workspace_bytes(M, top_k, n_experts, d, d_ff, r_max, n_adapters)
+    return torch.empty(max(nbytes, 256), dtype=torch.uint8, device=device), nbytes
+
+
+class lora_moe_weights:
+    """W, A and B of an expert layer's gate, up and down projections: W [n_experts, d_in, d_out],
+    A [n_adapters, n_experts, d_in, r_max], B [n_adapters, n_experts, r_max, d_out]."""
+
+    __slots__ = ("gate", "up", "down")
+
+    def __init__(self, Wg, Ag, Bg, Wu, Au, Bu, Wd, Ad, Bd):
+        self.gate, self.up, self.down = (Wg, Ag, Bg), (Wu, Au, Bu), (Wd, Ad, Bd)
+
+    def struct(self, n_experts: int, d: int, d_ff: int, r_max: int, n_adapters: int) -> lora_moe_weights_t:
+        pool = n_adapters * n_experts * r_max
+
+        def proj(name, t, d_in, d_out):
+            return lora_moe_proj_t(_buf(t[0], name + ".W", n_experts * d_in * d_out, _BF16),
+                                   _buf(t[1], name + ".A", pool * d_in, _BF16),
+                                   _buf(t[2], name + ".B", pool * d_out, _BF16))
+
+        return lora_moe_weights_t(proj("gate", self.gate, d, d_ff), proj("up", self.up, d, d_ff),
+                                  proj("down", self.down, d_ff, d))
+
+
+def lora_moe_layer(x, weights, scale, ranks, ids, topk_ids, topk_w, residual, M: int, top_k: int,
+                   n_experts: int, d: int, d_ff: int, r_max: int, n_adapters: int, act: int, y,
+                   y_dtype: int, mode: int, ws, ws_bytes: int, stream=None) -> None:
+    """y[M, d] = residual + sum over the token's slots of topk_w * down(act(gate(x)) * up(x)); weights: a
+    lora_moe_weights."""
+    y_types = _F32 if y_dtype == LORA_F32 else _BF16
+    if isinstance(weights, lora_moe_weights):
+        weights = weights.struct(n_experts, d, d_ff, r_max, n_adapters)
+    _check(_lib.lora_moe_layer(
+        _buf(x, "x", M * d, _BF16), weights, _buf(scale, "scale", n_adapters, _F32),
+        _buf(ranks, "ranks", n_adapters, _I32), _buf(ids, "ids", M, _I32),
+        _buf(topk_ids, "topk_ids", M * top_k, _I32), _buf(topk_w, "topk_w", M * top_k, _F32),
+        _buf(residual, "residual", M * d, y_types), M, top_k, n_experts, d, d_ff, r_max, n_adapters, act,
+        _buf(y, "y", M * d, y_types), y_dtype, mode, _buf(ws, "ws", ws_bytes, _U8), ws_bytes,
+        _stream_here(stream)), "lora_moe_layer")
 
 
 def lora_fp8_workspace_bytes(M: int, d_in: int, d_out: int, r_max: int, n_adapters: int) -> int:
