@@ -394,8 +394,10 @@ void shrink_plan(int d_in, int r_max, int *kc, int *ksplit);
 struct MoePlan {
     int rm, bm, n_tn, n_lt, ks, k_per_split, np;
 };
-// n_proj: projections that share the rows, an expert layer's gate and up in one launch.
-MoePlan moe_plan(int M, int top_k, int E, int K, int N, int r_max, int n_adapters, int n_proj = 1);
+MoePlan moe_plan(int M, int top_k, int E, int K, int N, int r_max, int n_adapters);
+// The plans of a whole expert layer's launches.  n_proj: projections that share the rows (gate and up in
+// one launch).
+MoePlan moe_layer_plan(int M, int top_k, int E, int K, int N, int r_max, int n_adapters, int n_proj);
 size_t moe_partial_floats(const MoePlan &p, int P);  // [ks][P][np]
 size_t moe_tpart_floats(const MoePlan &p, int P);    // [ks][P][rm]
 

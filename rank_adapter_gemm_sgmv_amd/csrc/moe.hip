@@ -47,15 +47,17 @@ struct MoeShared {
     int32_t wc[kWaves];
 };
 
-__device__ __forceinline__ int moe_slot(const MoeShared &sh, int i) {
+template <class S>
+__device__ __forceinline__ int moe_slot(const S &sh, int i) {
     const int w = i >> 5;
     return sh.wpre[w] + __popc(sh.bits[w] & ((1u << (i & 31)) - 1u));
 }
 
 // The a-th expert, ascending, that some pair is routed to (-1: fewer are).  Only batches with fewer
 // pairs than experts ask; the others give every expert its workgroups.
-__device__ __forceinline__ int moe_routed_expert(MoeShared &sh, const int32_t *topk_ids, int P, int E, int a,
-                                                 int tid, int lane) {
+template <class S>
+__device__ __forceinline__ int moe_routed_expert(S &sh, const int32_t *topk_ids, int P, int E, int a, int tid,
+                                                 int lane) {
     const int nw = (E + 31) >> 5;  // at most 128 words
     for (int w = tid; w < nw; w += kThreads) sh.bits[w] = 0u;
     __syncthreads();
@@ -85,6 +87,88 @@ __device__ __forceinline__ int moe_routed_expert(MoeShared &sh, const int32_t *t
     return found ? __builtin_amdgcn_readlane(e, __ffsll((unsigned long long)found) - 1) : -1;
 }
 
+// The expert's pairs, in pair order, into sh.rows; their count (uniform in the workgroup).
+template <class S>
+__device__ __forceinline__ int moe_pairs(S &sh, const int32_t *topk_ids, int P, int e, int tid, int lane, int wave) {
+    const uint64_t below = lane == 0 ? 0ull : (~0ull >> (64 - lane));
+    int count = 0;
+    for (int p0 = 0; p0 < P; p0 += kThreads) {
+        const int p = p0 + tid;
+        const bool hit = p < P && topk_ids[p] == e;
+        const uint64_t bal = __ballot(hit);
+        if (lane == 0) sh.wc[wave] = __popcll(bal);
+        __syncthreads();
+        int base = count, tot = 0;
+#pragma unroll
+        for (int w = 0; w < kWaves; ++w) {
+            const int c = sh.wc[w];
+            base += w < wave ? c : 0;
+            tot += c;
+        }
+        if (hit) sh.rows[base + __popcll(bal & below)] = (uint16_t)p;
+        count += tot;
+        __syncthreads();  // wc is rewritten by the next round; rows complete after the last
+    }
+    return count;
+}
+
+// Adapter tile lt of an expert: its pairs' distinct adapters, ascending, and the APT of them that are
+// the tile's, into sh.tile_ad; false (for the whole workgroup) if none is.
+template <int APT, class S>
+__device__ __forceinline__ bool moe_tile_adapters(S &sh, const int32_t *ids, int top_k, int n_adapters, int count,
+                                                  int lt, int tid, int lane, int wave) {
+    const int nw = (n_adapters + 31) >> 5;  // <= kBitWords = 2 kThreads
+    for (int w = tid; w < nw; w += kThreads) sh.bits[w] = 0u;
+    __syncthreads();
+    for (int j = tid; j < count; j += kThreads) {
+        const int i = ids[sh.rows[j] / top_k];
+        if (i >= 0 && i < n_adapters) atomicOr(&sh.bits[i >> 5], 1u << (i & 31));
+    }
+    __syncthreads();
+    const int w0 = 2 * tid;
+    const int c0 = w0 < nw ? __popc(sh.bits[w0]) : 0;
+    const int c1 = w0 + 1 < nw ? __popc(sh.bits[w0 + 1]) : 0;
+    int v = c0 + c1;
+#pragma unroll
+    for (int d = 1; d < 64; d <<= 1) {
+        const int u = __shfl_up(v, d, 64);
+        if (lane >= d) v += u;
+    }
+    if (lane == 63) sh.wc[wave] = v;
+    __syncthreads();
+    int wb = 0, T = 0;
+#pragma unroll
+    for (int w = 0; w < kWaves; ++w) {
+        const int c = sh.wc[w];
+        wb += w < wave ? c : 0;
+        T += c;
+    }
+    const int excl = wb + v - c0 - c1;
+    if (w0 < nw) sh.wpre[w0] = excl;
+    if (w0 + 1 < nw) sh.wpre[w0 + 1] = excl + c0;
+    if (lt * APT >= T) return false;
+    __syncthreads();
+    if (tid < APT) {
+        const int s = lt * APT + tid;
+        int ad = -1;
+        if (s < T) {
+            // the word holding slot s: the last word whose prefix is <= s
+            int lo = 0, hi = nw - 1;
+            while (lo < hi) {
+                const int mid = (lo + hi + 1) >> 1;
+                if (sh.wpre[mid] <= s) lo = mid;
+                else hi = mid - 1;
+            }
+            uint32_t bw = sh.bits[lo];
+            for (int k = s - sh.wpre[lo]; k > 0; --k) bw &= bw - 1u;
+            ad = 32 * lo + __ffs(bw) - 1;
+        }
+        sh.tile_ad[tid] = ad;
+    }
+    __syncthreads();
+    return true;
+}
+
 template <class C, int RM, MoeRows ROWS>
 __global__ __launch_bounds__(kThreads) void moe_gemm_kernel(MoeGemmArgs a) {
     __shared__ __attribute__((aligned(1024))) uint4 lds[kWaves * C::WAVE];
@@ -110,83 +194,12 @@ __global__ __launch_bounds__(kThreads) void moe_gemm_kernel(MoeGemmArgs a) {
     if (second) ct -= n_cols;
     const uint16_t *const W = second ? a.W[1] : a.W[0], *const A = second ? a.A[1] : a.A[0];
     float *const partial = second ? a.partial[1] : a.partial[0], *const tpart = second ? a.tpart[1] : a.tpart[0];
-    const uint64_t below = lane == 0 ? 0ull : (~0ull >> (64 - lane));
-
-    // 1. this expert's pairs, in pair order (count is uniform in the workgroup)
-    int count = 0;
-    for (int p0 = 0; p0 < a.P; p0 += kThreads) {
-        const int p = p0 + tid;
-        const bool hit = p < a.P && a.topk_ids[p] == e;
-        const uint64_t bal = __ballot(hit);
-        if (lane == 0) sh.wc[wave] = __popcll(bal);
-        __syncthreads();
-        int base = count, tot = 0;
-#pragma unroll
-        for (int w = 0; w < kWaves; ++w) {
-            const int c = sh.wc[w];
-            base += w < wave ? c : 0;
-            tot += c;
-        }
-        if (hit) sh.rows[base + __popcll(bal & below)] = (uint16_t)p;
-        count += tot;
-        __syncthreads();  // wc is rewritten by the next round; rows complete after the last
-    }
+    const int count = moe_pairs(sh, a.topk_ids, a.P, e, tid, lane, wave);
     if (count == 0) return;  // whole workgroup
-
-    // 2. adapter tiles: the expert's adapters, ascending, and this tile's share of them
     const bool adapter_tile = ct >= a.n_tn;
     const int lt = ct - a.n_tn;
-    if (adapter_tile) {
-        const int nw = (a.n_adapters + 31) >> 5;  // <= kBitWords = 2 kThreads
-        for (int w = tid; w < nw; w += kThreads) sh.bits[w] = 0u;
-        __syncthreads();
-        for (int j = tid; j < count; j += kThreads) {
-            const int i = a.ids[sh.rows[j] / a.top_k];
-            if (i >= 0 && i < a.n_adapters) atomicOr(&sh.bits[i >> 5], 1u << (i & 31));
-        }
-        __syncthreads();
-        const int w0 = 2 * tid;
-        const int c0 = w0 < nw ? __popc(sh.bits[w0]) : 0;
-        const int c1 = w0 + 1 < nw ? __popc(sh.bits[w0 + 1]) : 0;
-        int v = c0 + c1;
-#pragma unroll
-        for (int d = 1; d < 64; d <<= 1) {
-            const int u = __shfl_up(v, d, 64);
-            if (lane >= d) v += u;
-        }
-        if (lane == 63) sh.wc[wave] = v;
-        __syncthreads();
-        int wb = 0, T = 0;
-#pragma unroll
-        for (int w = 0; w < kWaves; ++w) {
-            const int c = sh.wc[w];
-            wb += w < wave ? c : 0;
-            T += c;
-        }
-        const int excl = wb + v - c0 - c1;
-        if (w0 < nw) sh.wpre[w0] = excl;
-        if (w0 + 1 < nw) sh.wpre[w0 + 1] = excl + c0;
-        if (lt * APT >= T) return;  // no adapter of this expert in this tile (whole workgroup)
-        __syncthreads();
-        if (tid < APT) {
-            const int s = lt * APT + tid;
-            int ad = -1;
-            if (s < T) {
-                // the word holding slot s: the last word whose prefix is <= s
-                int lo = 0, hi = nw - 1;
-                while (lo < hi) {
-                    const int mid = (lo + hi + 1) >> 1;
-                    if (sh.wpre[mid] <= s) lo = mid;
-                    else hi = mid - 1;
-                }
-                uint32_t bw = sh.bits[lo];
-                for (int k = s - sh.wpre[lo]; k > 0; --k) bw &= bw - 1u;
-                ad = 32 * lo + __ffs(bw) - 1;
-            }
-            sh.tile_ad[tid] = ad;
-        }
-        __syncthreads();
-    }
+    if (adapter_tile && !moe_tile_adapters<APT>(sh, a.ids, a.top_k, a.n_adapters, count, lt, tid, lane, wave))
+        return;  // whole workgroup
 
     // 3. per-lane sources: W[e] (row stride N), or the tile's A[i][e] (row stride r_stride);
     //    direct load q of a W stage: lane l fills position l % 16 of row 4 q + l / 16
@@ -361,8 +374,8 @@ __global__ __launch_bounds__(256) void moe_reduce_kernel(MoeReduceArgs a) {
 
 }  // namespace
 
-MoePlan moe_plan(int M, int top_k, int E, int K, int N, int r_max, int n_adapters, int n_proj) {
-    MoePlan p;
+MoePlan moe_plan(int M, int top_k, int E, int K, int N, int r_max, int n_adapters) {
+    MoePlan p{};
     const int P = M * top_k;
     p.rm = rank_bucket(r_max);
     p.bm = 32;
@@ -373,8 +386,23 @@ MoePlan moe_plan(int M, int top_k, int E, int K, int N, int r_max, int n_adapter
     p.n_lt = (distinct + apt - 1) / apt;
     // splits of K so that the W tiles of the experts that can be routed to fill the chip
     // about twice (at most 16 splits, each a multiple of 64 deep)
-    const long active = (long)(E < P ? E : P) * p.n_tn * n_proj;
+    const long active = (long)(E < P ? E : P) * p.n_tn;
     int ks = (int)((512 + active - 1) / active);
+    const int kq = (K + kBKW * kWaves - 1) / (kBKW * kWaves);
+    if (ks < 1) ks = 1;
+    if (ks > 16) ks = 16;
+    if (ks > kq) ks = kq;
+    p.k_per_split = (kq + ks - 1) / ks * kBKW * kWaves;
+    p.ks = (K + p.k_per_split - 1) / p.k_per_split;
+    return p;
+}
+
+MoePlan moe_layer_plan(int M, int top_k, int E, int K, int N, int r_max, int n_adapters, int n_proj) {
+    MoePlan p = moe_plan(M, top_k, E, K, N, r_max, n_adapters);
+    const int P = M * top_k, slots = E < P ? E : P;
+    // workgroups of a split, with an adapter tile per expert and projection
+    const long tiles = (long)slots * n_proj * (p.n_tn + 1);
+    int ks = (int)(256 / tiles);
     const int kq = (K + kBKW * kWaves - 1) / (kBKW * kWaves);
     if (ks < 1) ks = 1;
     if (ks > 16) ks = 16;

@@ -15,95 +15,114 @@ namespace {
 
 constexpr int kThreadsMoe = 256;
 
-// One pair's adapter: its first rank row of B's pool (times the expert), rank and scale; rank 0 without.
-struct PairAdapter {
-    size_t row0;
-    int rank;
-    float scale;
-};
-__device__ __forceinline__ PairAdapter pair_adapter(const MoeLayerArgs &a, int e, int i) {
-    PairAdapter p{0, 0, 0.0f};
-    if (i >= 0 && i < a.n_adapters) {
-        p.row0 = ((size_t)i * a.E + e) * a.r_stride;
-        p.rank = a.ranks ? min(max(a.ranks[i], 0), a.r_stride) : a.r_stride;
-        p.scale = a.scale[i];
-    }
-    return p;
-}
-
-// t[j] of pair p into LDS, by RM threads from `first` on
-template <int RM>
-__device__ __forceinline__ void pair_t(float *s_t, const MoeSums &s, int P, int p, int ks, int j) {
-    if (j < 0 || j >= RM) return;
-    float t = 0.0f;
-    for (int sp = 0; sp < ks; ++sp) t += s.tpart[((size_t)sp * P + p) * RM + j];
-    s_t[j] = t;
-}
-
-// z[4] = the splits of columns n .. n + 3 in order
-__device__ __forceinline__ float4 split_sum(const MoeSums &s, int P, int p, int np, int ks, int n) {
+// Four columns of one pair: the splits in order, plus scale_i t B[i][e].  Called by a group of at least
+// RM threads (thread `tj` of it) that share s_t and meet at sync(); every load whose address is known
+// is issued before the first wait: the partial sums, t's parts and the first rows of B together,
+// rows past the adapter's rank being read (the pool holds them) and not used.
+template <int RM, class F>
+__device__ __forceinline__ float4 pair_columns(const MoeLayerArgs &a, const MoeSums &s, int p, int e, int i, int np,
+                                               int ks, int N, int n, float *s_t, int tj, F sync) {
+    constexpr int BCH = RM < 16 ? RM : 16, EARLY = 4;
     const float *q = s.partial + (size_t)p * np + n;
-    float4 z = *reinterpret_cast<const float4 *>(q);
-#pragma unroll 4
-    for (int sp = 1; sp < ks; ++sp) {
-        const float4 v = *reinterpret_cast<const float4 *>(q + (size_t)sp * P * np);
+    const size_t qs = (size_t)a.P * np, ts = (size_t)a.P * RM;
+    float4 pv[EARLY];
+#pragma unroll
+    for (int sp = 0; sp < EARLY; ++sp)
+        if (sp < ks) pv[sp] = *reinterpret_cast<const float4 *>(q + sp * qs);
+    const bool has = i >= 0 && i < a.n_adapters;  // uniform in the group
+    const int ad = has ? i : 0;
+    int rank = 0;
+    float scale = 0.0f;
+    const uint16_t *bp = s.B + ((size_t)ad * a.E + e) * a.r_stride * N + n;
+    uint2 bv[BCH];
+    if (has) {
+        rank = a.ranks ? min(max(a.ranks[ad], 0), a.r_stride) : a.r_stride;
+        scale = a.scale[ad];
+#pragma unroll
+        for (int j = 0; j < BCH; ++j)
+            bv[j] = *reinterpret_cast<const uint2 *>(bp + (size_t)min(j, a.r_stride - 1) * N);
+        if (tj < RM) {
+            const float *tp = s.tpart + (size_t)p * RM + tj;
+            float tv[EARLY], t = 0.0f;
+#pragma unroll
+            for (int sp = 0; sp < EARLY; ++sp) tv[sp] = sp < ks ? tp[sp * ts] : 0.0f;
+#pragma unroll
+            for (int sp = 0; sp < EARLY; ++sp)
+                if (sp < ks) t += tv[sp];
+            for (int sp = EARLY; sp < ks; ++sp) t += tp[sp * ts];
+            s_t[tj] = t;
+        }
+    }
+    sync();
+    float4 z = pv[0];
+#pragma unroll
+    for (int sp = 1; sp < EARLY; ++sp)
+        if (sp < ks) { z.x += pv[sp].x; z.y += pv[sp].y; z.z += pv[sp].z; z.w += pv[sp].w; }
+    for (int sp = EARLY; sp < ks; ++sp) {
+        const float4 v = *reinterpret_cast<const float4 *>(q + sp * qs);
         z.x += v.x; z.y += v.y; z.z += v.z; z.w += v.w;
+    }
+    if (has) {
+        float4 d = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+        for (int j0 = 0; j0 < RM; j0 += BCH) {
+            if (j0 >= rank) break;  // uniform in the group
+            if (j0 > 0)
+#pragma unroll
+                for (int j = 0; j < BCH; ++j)
+                    bv[j] = *reinterpret_cast<const uint2 *>(bp + (size_t)min(j0 + j, a.r_stride - 1) * N);
+#pragma unroll
+            for (int j = 0; j < BCH; ++j) {
+                if (j0 + j >= rank) continue;
+                const float t = s_t[j0 + j];
+                d.x = fmaf(t, bf16_lo(bv[j].x), d.x); d.y = fmaf(t, bf16_hi(bv[j].x), d.y);
+                d.z = fmaf(t, bf16_lo(bv[j].y), d.z); d.w = fmaf(t, bf16_hi(bv[j].y), d.w);
+            }
+        }
+        z.x = fmaf(scale, d.x, z.x); z.y = fmaf(scale, d.y, z.y);
+        z.z = fmaf(scale, d.z, z.z); z.w = fmaf(scale, d.w, z.w);
     }
     return z;
 }
 
-// z += scale t B[rows][n .. n + 3]
-__device__ __forceinline__ void add_delta(float4 &z, const float *s_t, const uint16_t *B, const PairAdapter &ad,
-                                          int N, int n) {
-    const uint16_t *bp = B + ad.row0 * N + n;
-    float4 d = make_float4(0.f, 0.f, 0.f, 0.f);
-#pragma unroll 8
-    for (int j = 0; j < ad.rank; ++j) {
-        const uint2 b = *reinterpret_cast<const uint2 *>(bp + (size_t)j * N);
-        const float t = s_t[j];
-        d.x = fmaf(t, bf16_lo(b.x), d.x); d.y = fmaf(t, bf16_hi(b.x), d.y);
-        d.z = fmaf(t, bf16_lo(b.y), d.z); d.w = fmaf(t, bf16_hi(b.y), d.w);
-    }
-    z.x = fmaf(ad.scale, d.x, z.x); z.y = fmaf(ad.scale, d.y, z.y);
-    z.z = fmaf(ad.scale, d.z, z.z); z.w = fmaf(ad.scale, d.w, z.w);
-}
-
-// Block (column chunk, pair), four columns per thread.
+// Block (chunk of 512 columns, pair), four columns per thread: the first half of the block sums the
+// gate, the second up, which it hands over through LDS.
 template <int RM, bool PARTS>
 __global__ __launch_bounds__(kThreadsMoe) void moe_hidden_kernel(MoeLayerArgs a, MoeSums gate, MoeSums up, int N,
                                                                  int np, int ks, int act, uint16_t *h) {
+    constexpr int HALF = kThreadsMoe / 2;
+    static_assert(HALF >= 64, "RM threads of each half sum t");
     __shared__ float s_t[2][RM];
-    const int p = blockIdx.y, e = a.topk_ids[p];
+    __shared__ float4 s_up[HALF];
+    const int p = blockIdx.y, e = a.topk_ids[p], i = a.ids[p / a.top_k];
     if (e < 0 || e >= a.E) return;  // uniform in the block
-    const int n = (blockIdx.x * kThreadsMoe + threadIdx.x) * 4;
+    const int which = threadIdx.x / HALF, t = threadIdx.x % HALF;  // (uniform in a wave)
+    const int n = (blockIdx.x * HALF + t) * 4;
     const bool ok = n < N;
-    const int nc = ok ? n : 0;
-    const PairAdapter ad = pair_adapter(a, e, a.ids[p / a.top_k]);
-    float4 zg = split_sum(gate, a.P, p, np, ks, nc), zu = split_sum(up, a.P, p, np, ks, nc);
-    if (ad.rank > 0) {  // uniform in the block
-        pair_t<RM>(s_t[0], gate, a.P, p, ks, threadIdx.x);
-        pair_t<RM>(s_t[1], up, a.P, p, ks, (int)threadIdx.x - 64);
-        __syncthreads();
-        add_delta(zg, s_t[0], gate.B, ad, N, nc);
-        add_delta(zu, s_t[1], up.B, ad, N, nc);
-    }
-    if (!ok) return;
-    float z[4] = {zg.x, zg.y, zg.z, zg.w};
+    const float4 v = pair_columns<RM>(a, which ? up : gate, p, e, i, np, ks, N, ok ? n : 0, s_t[which], t,
+                                      [] { __syncthreads(); });
+    if (which) s_up[t] = v;
+    __syncthreads();
+    if (which || !ok) return;
+    const float4 zu = s_up[t];
+    float z[4] = {v.x, v.y, v.z, v.w};
     epi_act<4>(z, act);
     z[0] *= zu.x; z[1] *= zu.y; z[2] *= zu.z; z[3] *= zu.w;
     if constexpr (!PARTS) {
         // bf16: what the matrix instructions take; y's own rounding is as large
-        *reinterpret_cast<uint2 *>(h + (size_t)p * N + n) = make_uint2(cvt_bf16x2(z[0], z[1]), cvt_bf16x2(z[2], z[3]));
+        *reinterpret_cast<uint2 *>(h + (size_t)p * N + n) =
+            make_uint2(cvt_bf16x2(z[0], z[1]), cvt_bf16x2(z[2], z[3]));
     } else {
 #pragma unroll
         for (int q = 0; q < 4; ++q) {
             uint32_t b[4];
 #pragma unroll
-            for (int v = 0; v < 4; ++v) {
-                b[v] = q < 3 ? bf16_part(z[v]) : 0u;
-                z[v] = bf16_rest(z[v]);
+            for (int c = 0; c < 4; ++c) {
+                b[c] = q < 3 ? bf16_part(z[c]) : 0u;
+                z[c] = bf16_rest(z[c]);
             }
-            *reinterpret_cast<uint2 *>(h + ((size_t)4 * p + q) * N + n) = make_uint2(b[0] | b[1] << 16, b[2] | b[3] << 16);
+            *reinterpret_cast<uint2 *>(h + ((size_t)4 * p + q) * N + n) =
+                make_uint2(b[0] | b[1] << 16, b[2] | b[3] << 16);
         }
     }
 }
@@ -121,20 +140,24 @@ __global__ __launch_bounds__(kThreadsMoe) void moe_out_kernel(MoeLayerArgs a, Mo
     const bool ok = n < N;
     const int nc = ok ? n : 0;
     const int i = a.ids[m];
-    float4 sum = make_float4(0.f, 0.f, 0.f, 0.f);
+    const size_t at = (size_t)m * N + n;
+    float4 sum = make_float4(0.f, 0.f, 0.f, 0.f), res = sum;
+    if (residual && wave == 0 && ok) {
+        if constexpr (YF32) {
+            res = *reinterpret_cast<const float4 *>(static_cast<const float *>(residual) + at);
+        } else {
+            const uint2 r = *reinterpret_cast<const uint2 *>(static_cast<const uint16_t *>(residual) + at);
+            res = make_float4(bf16_lo(r.x), bf16_hi(r.x), bf16_lo(r.y), bf16_hi(r.y));
+        }
+    }
     for (int j = wave; j < a.top_k; j += NW) {
         const int p = m * a.top_k + j, e = a.topk_ids[p];
-        if (e < 0 || e >= a.E) continue;  // uniform in the wave
-        const PairAdapter ad = pair_adapter(a, e, i);
-        float4 z = split_sum(down, a.P, p, np, ks, nc);
-        if (ad.rank > 0) {
-            // (LDS accesses of one wave complete in order; the compiler keeps them)
-            pair_t<RM>(s_t[wave], down, a.P, p, ks, lane);
-            __builtin_amdgcn_wave_barrier();
-            add_delta(z, s_t[wave], down.B, ad, N, nc);
-            __builtin_amdgcn_wave_barrier();
-        }
         const float w = a.topk_w ? a.topk_w[p] : 1.0f;
+        if (e < 0 || e >= a.E) continue;  // uniform in the wave
+        // (a wave's LDS accesses complete in order)
+        const float4 z = pair_columns<RM>(a, down, p, e, i, np, ks, N, nc, s_t[wave], lane,
+                                          [] { __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront"); __builtin_amdgcn_wave_barrier(); });
+        __builtin_amdgcn_wave_barrier();
         sum.x = fmaf(w, z.x, sum.x); sum.y = fmaf(w, z.y, sum.y);
         sum.z = fmaf(w, z.z, sum.z); sum.w = fmaf(w, z.w, sum.w);
     }
@@ -146,21 +169,12 @@ __global__ __launch_bounds__(kThreadsMoe) void moe_out_kernel(MoeLayerArgs a, Mo
         const float4 v = s_z[w][lane];
         sum.x += v.x; sum.y += v.y; sum.z += v.z; sum.w += v.w;
     }
-    const size_t at = (size_t)m * N + n;
-    if constexpr (YF32) {
-        if (residual) {
-            const float4 r = *reinterpret_cast<const float4 *>(static_cast<const float *>(residual) + at);
-            sum.x += r.x; sum.y += r.y; sum.z += r.z; sum.w += r.w;
-        }
+    sum.x += res.x; sum.y += res.y; sum.z += res.z; sum.w += res.w;
+    if constexpr (YF32)
         *reinterpret_cast<float4 *>(static_cast<float *>(y) + at) = sum;
-    } else {
-        if (residual) {
-            const uint2 r = *reinterpret_cast<const uint2 *>(static_cast<const uint16_t *>(residual) + at);
-            sum.x += bf16_lo(r.x); sum.y += bf16_hi(r.x); sum.z += bf16_lo(r.y); sum.w += bf16_hi(r.y);
-        }
+    else
         *reinterpret_cast<uint2 *>(static_cast<uint16_t *>(y) + at) =
             make_uint2(cvt_bf16x2(sum.x, sum.y), cvt_bf16x2(sum.z, sum.w));
-    }
 }
 
 bool moe_args_ok(const MoePlan &p, const MoeLayerArgs &a, int N) {
@@ -172,10 +186,12 @@ bool moe_args_ok(const MoePlan &p, const MoeLayerArgs &a, int N) {
 hipError_t launch_moe_hidden(const MoePlan &p, const MoeLayerArgs &a, const MoeSums &gate, const MoeSums &up,
                              int N, int act, bool parts, uint16_t *h, hipStream_t s) {
     if (!moe_args_ok(p, a, N)) return hipErrorInvalidValue;
-    const dim3 grid((unsigned)((N + 4 * kThreadsMoe - 1) / (4 * kThreadsMoe)), (unsigned)a.P);
+    const dim3 grid((unsigned)((N + 2 * kThreadsMoe - 1) / (2 * kThreadsMoe)), (unsigned)a.P);
+#define MOE_HIDDEN_ONE(RMX, PARTS)                                                               \
+    launch(moe_hidden_kernel<RMX, PARTS>, grid, dim3(kThreadsMoe), 0, s, a, gate, up, N, p.np, p.ks, act, h)
 #define MOE_HIDDEN(RMX)                                                                          \
-    if (parts) launch(moe_hidden_kernel<RMX, true>, grid, dim3(kThreadsMoe), 0, s, a, gate, up, N, p.np, p.ks, act, h); \
-    else launch(moe_hidden_kernel<RMX, false>, grid, dim3(kThreadsMoe), 0, s, a, gate, up, N, p.np, p.ks, act, h)
+    if (parts) MOE_HIDDEN_ONE(RMX, true);                                                        \
+    else MOE_HIDDEN_ONE(RMX, false)
     switch (p.rm) {
         case 8: MOE_HIDDEN(8); break;
         case 16: MOE_HIDDEN(16); break;
@@ -183,6 +199,7 @@ hipError_t launch_moe_hidden(const MoePlan &p, const MoeLayerArgs &a, const MoeS
         default: MOE_HIDDEN(64); break;
     }
 #undef MOE_HIDDEN
+#undef MOE_HIDDEN_ONE
     return hipGetLastError();
 }
 
