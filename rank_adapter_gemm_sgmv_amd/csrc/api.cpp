@@ -1187,10 +1187,10 @@ struct MoeLayerPlan {
     MoePlan in, out;
     size_t partial, tpart, hidden, bytes;  // bytes of each part
 };
-MoeLayerPlan moe_plans(const MoeLayerDims &z) {
+MoeLayerPlan moe_plans(const MoeLayerDims &z, bool y_f32) {
     MoeLayerPlan p;
-    p.in = moe_layer_plan(z.M, z.top_k, z.E, z.d, z.ff, z.r_max, z.n_adapters, 2);
-    p.out = moe_layer_plan(z.M, z.top_k, z.E, z.ff, z.d, z.r_max, z.n_adapters, 1);
+    p.in = moe_layer_plan(z.M, z.top_k, z.E, z.d, z.ff, z.r_max, z.n_adapters, 2, kMoeToken);
+    p.out = moe_layer_plan(z.M, z.top_k, z.E, z.ff, z.d, z.r_max, z.n_adapters, 1, y_f32 ? kMoeParts : kMoePair);
     const size_t a = 2 * round_up(moe_partial_floats(p.in, z.pairs()) * 4),
                  b = round_up(moe_partial_floats(p.out, z.pairs()) * 4),
                  ta = 2 * round_up(moe_tpart_floats(p.in, z.pairs()) * 4),
@@ -1207,7 +1207,7 @@ MoeLayerPlan moe_plans(const MoeLayerDims &z) {
 hipError_t run_moe_layer(const MoeLayerDims &z, const void *x, const lora_moe_weights_t &w, const float *scale,
                          const int32_t *ranks, const int32_t *ids, const int32_t *topk_ids, const float *topk_w,
                          const void *residual, lora_act_t act, void *y, bool y_f32, void *ws, hipStream_t s) {
-    const MoeLayerPlan pl = moe_plans(z);
+    const MoeLayerPlan pl = moe_plans(z, y_f32);
     const int P = z.pairs();
     char *const c = static_cast<char *>(ws);
     auto floats = [](char *p) { return reinterpret_cast<float *>(p); };
@@ -1252,7 +1252,7 @@ size_t lora_moe_layer_workspace_bytes(int32_t M, int32_t top_k, int32_t n_expert
                                       int32_t r_max, int32_t n_adapters) {
     const MoeLayerDims z{M, top_k, n_experts, d, d_ff, r_max, n_adapters};
     if (check_moe_layer_sizes(z) != LORA_OK || M == 0) return 0;
-    return moe_plans(z).bytes;
+    return moe_plans(z, true).bytes;  // (the same for both types of y)
 }
 
 lora_status_t lora_moe_layer(const void *x, const lora_moe_weights_t *weights, const float *scale,
@@ -1279,7 +1279,7 @@ lora_status_t lora_moe_layer(const void *x, const lora_moe_weights_t *weights, c
         !aligned(scale, 4) || !aligned(ids, 4) || !aligned(topk_ids, 4) || !aligned(topk_w, 4) ||
         !aligned(ranks, 4))
         return LORA_ERR_ALIGN;
-    if (ws_bytes < moe_plans(z).bytes) return LORA_ERR_WORKSPACE;
+    if (ws_bytes < moe_plans(z, true).bytes) return LORA_ERR_WORKSPACE;
     clear_stale_error();
     if ((mode & LORA_MODE_CHECKED) &&
         (st = check_moe_tables(ids, ranks, topk_ids, M, top_k, n_experts, r_max, n_adapters,

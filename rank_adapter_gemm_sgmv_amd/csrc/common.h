@@ -393,17 +393,18 @@ void shrink_plan(int d_in, int r_max, int *kc, int *ksplit);
 // into ks splits of k_per_split; pairs in blocks of bm rows; partial rows np floats apart.
 struct MoePlan {
     int rm, bm, n_tn, n_lt, ks, k_per_split, np;
+    bool few;  // blocks of 16 staged rows (lora_moe_layer)
 };
 MoePlan moe_plan(int M, int top_k, int E, int K, int N, int r_max, int n_adapters);
-// The plans of a whole expert layer's launches.  n_proj: projections that share the rows (gate and up in
-// one launch).
-MoePlan moe_layer_plan(int M, int top_k, int E, int K, int N, int r_max, int n_adapters, int n_proj);
 size_t moe_partial_floats(const MoePlan &p, int P);  // [ks][P][np]
 size_t moe_tpart_floats(const MoePlan &p, int P);    // [ks][P][rm]
 
 // The rows of x that a (token, slot) pair multiplies: its token's, its own, or its own row in four
 // bf16 parts that add up to it (rows 4 p .. 4 p + 3).
 enum MoeRows { kMoeToken, kMoePair, kMoeParts };
+// The plans of a whole expert layer's launches.  n_proj: projections that share the rows (gate and up in
+// one launch).
+MoePlan moe_layer_plan(int M, int top_k, int E, int K, int N, int r_max, int n_adapters, int n_proj, MoeRows rows);
 
 struct MoeGemmArgs {
     const uint16_t *x;         // [M][K], [P][K] or [4 P][K]

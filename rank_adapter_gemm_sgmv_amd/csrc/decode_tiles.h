@@ -35,20 +35,23 @@ constexpr int kThreads = 64 * kWaves;
 // 128-column tile reads each x byte for twice the W bytes a 64-column tile did.
 // X: bf16 (uint16_t), or (X8) x holds E4M3 codes (uint8_t) or integers (int8_t); a stage's rows are the
 // same 128 bytes, so 128 k, and the codes become bf16 (exactly) as they are read for the MFMAs.
-template <int BM_, class X_ = uint16_t>
+// XR: the rows of x that are staged, BM or (where a block has few) 16 of 32: the tile's other rows
+// then repeat them and are not used.
+template <int BM_, class X_ = uint16_t, int XR_ = BM_>
 struct Dec {
-    static constexpr int BM = BM_;
+    static constexpr int BM = BM_, XR = XR_;
     using X = X_;
     static constexpr bool X8 = sizeof(X) == 1;
     static constexpr int KX = X8 ? 2 * kBKX : kBKX;  // k of an x stage
     static constexpr int TM = BM / 32, TN = kBN / 32;
-    static constexpr int XSLOT = BM * kBKX * 2 / 16;     // uint4 per x stage (128-byte rows)
+    static constexpr int XSLOT = XR * kBKX * 2 / 16;     // uint4 per x stage (128-byte rows)
     static constexpr int WSLOT = kBKW * kBN * 2 / 16;    // uint4 per W stage
     static constexpr int XINS = XSLOT / 64;              // direct loads per x stage
     static constexpr int WINS = WSLOT / 64;              // direct loads per W stage
     static constexpr int WAVE = 2 * XSLOT + 4 * WSLOT;   // uint4 of LDS per wave
     static constexpr int TILE = BM * kBN;                 // floats per tile
     static_assert(BM == 32 || BM == 64, "decode tile rows");
+    static_assert(XR == BM || (BM == 32 && XR == 16), "staged rows");
     static_assert(TILE * 4 <= WAVE * 16, "a wave's partial tile fits its part of the LDS");
 };
 
@@ -74,7 +77,7 @@ __device__ __forceinline__ void dec_mfma(f32x16_t (&acc)[C::TM][C::TN], const ui
     bf16x8_t af[C::TM], bfr[C::TN];
 #pragma unroll
     for (int i = 0; i < C::TM; ++i) {
-        const int row = 32 * i + (lane & 31);
+        const int row = (32 * i + (lane & 31)) & (C::XR - 1);
         if constexpr (C::X8) {
             const uint2 v = reinterpret_cast<const uint2 *>(&xs[row * 8 + (quarter ^ (row & 7))])[lane >> 5];
             af[i] = __builtin_bit_cast(bf16x8_t, codes8_to_bf16<typename C::X>(v.x, v.y));
@@ -160,7 +163,7 @@ __device__ __forceinline__ void reduce_waves_put(const f32x16_t (&acc)[C::TM][C:
 #pragma unroll
         for (int j = 0; j < C::TN; ++j)
 #pragma unroll
-            for (int q = 0; q < 4; ++q)
+            for (int q = 0; q < (C::XR < 32 ? C::XR / 8 : 4); ++q)  // (rows below XR)
                 red_mine[((i * C::TN + j) * 4 + q) * 64 + lane] =
                     make_float4(acc[i][j][4 * q], acc[i][j][4 * q + 1], acc[i][j][4 * q + 2], acc[i][j][4 * q + 3]);
 }

@@ -235,7 +235,7 @@ __global__ __launch_bounds__(kThreads) void moe_gemm_kernel(MoeGemmArgs a) {
     const int kw0 = min(ks1, ks0 + wave * per_wave);
     const int kw1 = min(ks1, kw0 + per_wave);
     const int nst = (kw1 - kw0) / kBKW;
-    const int n_rb = (count * PARTS + C::BM - 1) / C::BM;
+    const int n_rb = (count * PARTS + C::XR - 1) / C::XR;
     const int col = tid & 127;
 
     for (int rb = 0; rb < n_rb; ++rb) {
@@ -245,7 +245,7 @@ __global__ __launch_bounds__(kThreads) void moe_gemm_kernel(MoeGemmArgs a) {
         for (int q = 0; q < C::XINS; ++q) {
             const int row = 8 * q + (lane >> 3);
             const int lc = (lane & 7) ^ (lane >> 3);
-            const int j = rb * C::BM + row;
+            const int j = rb * C::XR + row;
             const int p = sh.rows[min(j / PARTS, count - 1)];
             const int xr = ROWS == kMoeToken ? p / a.top_k : PARTS * p + j % PARTS;
             src.xp[q] = a.x + (size_t)xr * a.K + lc * 8;
@@ -265,14 +265,14 @@ __global__ __launch_bounds__(kThreads) void moe_gemm_kernel(MoeGemmArgs a) {
         reduce_waves_put<C>(acc, red + wave * (C::TILE / 4), lane);
         __syncthreads();
 #pragma unroll
-        for (int q = 0; q < C::BM / 8; ++q) {
+        for (int q = 0; q < C::XR / 8; ++q) {
             const int g = (tid >> 7) + 2 * q;  // rows 4 g .. 4 g + 3 of the block
             const float4 s = reduce_waves_group<C>(red, g, col);
             // (four parts of one pair: the last is zeros)
             const float sv[4] = {PARTS == 4 ? s.x + (s.y + s.z) : s.x, s.y, s.z, s.w};
 #pragma unroll
             for (int v = 0; v < 4 / PARTS; ++v) {
-                const int j = (rb * C::BM + 4 * g) / PARTS + v;
+                const int j = (rb * C::XR + 4 * g) / PARTS + v;
                 if (j >= count) continue;
                 const int p = sh.rows[j];
                 if (!adapter_tile) {
@@ -397,11 +397,12 @@ MoePlan moe_plan(int M, int top_k, int E, int K, int N, int r_max, int n_adapter
     return p;
 }
 
-MoePlan moe_layer_plan(int M, int top_k, int E, int K, int N, int r_max, int n_adapters, int n_proj) {
+MoePlan moe_layer_plan(int M, int top_k, int E, int K, int N, int r_max, int n_adapters, int n_proj, MoeRows rows) {
     MoePlan p = moe_plan(M, top_k, E, K, N, r_max, n_adapters);
     const int P = M * top_k, slots = E < P ? E : P;
     // workgroups of a split, with an adapter tile per expert and projection
     const long tiles = (long)slots * n_proj * (p.n_tn + 1);
+    p.few = rows != kMoeParts && P <= 10 * slots;
     int ks = (int)(256 / tiles);
     const int kq = (K + kBKW * kWaves - 1) / (kBKW * kWaves);
     if (ks < 1) ks = 1;
@@ -430,17 +431,26 @@ hipError_t launch_moe_gemm(const MoePlan &p, const MoeGemmArgs &args, hipStream_
     const dim3 grid((unsigned)((long)p.ks * a.n_slots * a.n_proj * (p.n_tn + p.n_lt)));
 #define MOE_GEMM(RMX)                                                                            \
     if (a.rows == kMoeToken)                                                                     \
-        launch(moe_gemm_kernel<Dec<32>, RMX, kMoeToken>, grid, dim3(kThreads), 0, s, a);         \
+        launch(moe_gemm_kernel<DEC, RMX, kMoeToken>, grid, dim3(kThreads), 0, s, a);             \
     else if (a.rows == kMoePair)                                                                 \
-        launch(moe_gemm_kernel<Dec<32>, RMX, kMoePair>, grid, dim3(kThreads), 0, s, a);          \
+        launch(moe_gemm_kernel<DEC, RMX, kMoePair>, grid, dim3(kThreads), 0, s, a);              \
     else                                                                                         \
-        launch(moe_gemm_kernel<Dec<32>, RMX, kMoeParts>, grid, dim3(kThreads), 0, s, a)
-    switch (p.rm) {
-        case 8: MOE_GEMM(8); break;
-        case 16: MOE_GEMM(16); break;
-        case 32: MOE_GEMM(32); break;
-        default: MOE_GEMM(64); break;
+        launch(moe_gemm_kernel<DEC, RMX, kMoeParts>, grid, dim3(kThreads), 0, s, a)
+#define MOE_RM()                                                                                 \
+    switch (p.rm) {                                                                              \
+        case 8: MOE_GEMM(8); break;                                                              \
+        case 16: MOE_GEMM(16); break;                                                            \
+        case 32: MOE_GEMM(32); break;                                                            \
+        default: MOE_GEMM(64); break;                                                            \
     }
+    if (p.few) {
+        using DEC = Dec<32, uint16_t, 16>;
+        MOE_RM()
+    } else {
+        using DEC = Dec<32>;
+        MOE_RM()
+    }
+#undef MOE_RM
 #undef MOE_GEMM
     return hipGetLastError();
 }

@@ -22,7 +22,7 @@ constexpr int kThreadsMoe = 256;
 template <int RM, class F>
 __device__ __forceinline__ float4 pair_columns(const MoeLayerArgs &a, const MoeSums &s, int p, int e, int i, int np,
                                                int ks, int N, int n, float *s_t, int tj, F sync) {
-    constexpr int BCH = RM < 16 ? RM : 16, EARLY = 4;
+    constexpr int BCH = RM < 32 ? RM : 32, EARLY = 4;
     const float *q = s.partial + (size_t)p * np + n;
     const size_t qs = (size_t)a.P * np, ts = (size_t)a.P * RM;
     float4 pv[EARLY];
