@@ -47,10 +47,21 @@ struct MoeShared {
     int32_t wc[kWaves];
 };
 
-template <class S>
-__device__ __forceinline__ int moe_slot(const S &sh, int i) {
-    const int w = i >> 5;
-    return sh.wpre[w] + __popc(sh.bits[w] & ((1u << (i & 31)) - 1u));
+// Batches of at most 64 pairs need no list in LDS and no barrier to find a workgroup's work: every wave
+// holds all pairs, one per lane.  A lane's rank: how many different values below its own the kept lanes
+// (of the first n) hold; different: how many they hold in all.
+__device__ __forceinline__ int wave_rank(int v, bool kept, int n, int &different) {
+    int rank = 0;
+    different = 0;
+    for (int q = 0; q < n; ++q) {  // (n and what is read of lane q are uniform)
+        const int u = __builtin_amdgcn_readlane(v, q);
+        const uint64_t same = __ballot(kept && v == u);
+        if ((same & ((2ull << q) - 1)) == (1ull << q)) {  // lane q is kept and the first of its value
+            rank += u < v;
+            ++different;
+        }
+    }
+    return rank;
 }
 
 // The a-th expert, ascending, that some pair is routed to (-1: fewer are).  Only batches with fewer
@@ -58,6 +69,13 @@ __device__ __forceinline__ int moe_slot(const S &sh, int i) {
 template <class S>
 __device__ __forceinline__ int moe_routed_expert(S &sh, const int32_t *topk_ids, int P, int E, int a, int tid,
                                                  int lane) {
+    if (P <= 64) {
+        const int v = lane < P ? topk_ids[lane] : -1;
+        const bool kept = v >= 0 && v < E;
+        int different;
+        const uint64_t found = __ballot(kept && wave_rank(v, kept, P, different) == a);
+        return found ? __builtin_amdgcn_readlane(v, __ffsll((unsigned long long)found) - 1) : -1;
+    }
     const int nw = (E + 31) >> 5;  // at most 128 words
     for (int w = tid; w < nw; w += kThreads) sh.bits[w] = 0u;
     __syncthreads();
@@ -91,6 +109,13 @@ __device__ __forceinline__ int moe_routed_expert(S &sh, const int32_t *topk_ids,
 template <class S>
 __device__ __forceinline__ int moe_pairs(S &sh, const int32_t *topk_ids, int P, int e, int tid, int lane, int wave) {
     const uint64_t below = lane == 0 ? 0ull : (~0ull >> (64 - lane));
+    if (P <= 64) {  // every wave writes the same list
+        const bool hit = lane < P && topk_ids[lane] == e;
+        const uint64_t bal = __ballot(hit);
+        if (hit) sh.rows[__popcll(bal & below)] = (uint16_t)lane;
+        __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");  // (a wave's LDS accesses complete in order)
+        return __popcll(bal);
+    }
     int count = 0;
     for (int p0 = 0; p0 < P; p0 += kThreads) {
         const int p = p0 + tid;
@@ -117,6 +142,17 @@ __device__ __forceinline__ int moe_pairs(S &sh, const int32_t *topk_ids, int P, 
 template <int APT, class S>
 __device__ __forceinline__ bool moe_tile_adapters(S &sh, const int32_t *ids, int top_k, int n_adapters, int count,
                                                   int lt, int tid, int lane, int wave) {
+    if (count <= 64) {
+        const int i = lane < count ? ids[sh.rows[lane] / top_k] : -1;
+        const bool kept = i >= 0 && i < n_adapters;
+        int different;
+        const int s = wave_rank(i, kept, count, different) - lt * APT;
+        // (every wave writes the same values: no slot is written twice with two)
+        if (kept && s >= 0 && s < APT) sh.tile_ad[s] = i;
+        if (lane < APT && lt * APT + lane >= different) sh.tile_ad[lane] = -1;
+        __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+        return lt * APT < different;
+    }
     const int nw = (n_adapters + 31) >> 5;  // <= kBitWords = 2 kThreads
     for (int w = tid; w < nw; w += kThreads) sh.bits[w] = 0u;
     __syncthreads();
@@ -280,8 +316,7 @@ __global__ __launch_bounds__(kThreads) void moe_gemm_kernel(MoeGemmArgs a) {
                 } else {
                     const int i = a.ids[p / a.top_k];
                     if (i < 0 || i >= a.n_adapters) continue;
-                    const int sl = moe_slot(sh, i) - lt * APT;
-                    if (sl == col / RM) tpart[((size_t)split * a.P + p) * RM + col % RM] = sv[v];
+                    if (sh.tile_ad[col / RM] == i) tpart[((size_t)split * a.P + p) * RM + col % RM] = sv[v];
                 }
             }
         }
