@@ -20,7 +20,7 @@ namespace lora {
 namespace {
 
 constexpr int kThreadsRope = 256;
-constexpr int kTableMax = 1024;  // (cos, sin) pairs a block holds
+constexpr int kTableMax = LORA_ROPE_MAX_DIM / 2;  // (cos, sin) pairs of a row
 
 // cos and sin of 2 pi t, both times factor.  |t - its quarter| <= 1/8, where the Taylor polynomials
 // of degree 9 and 10 are within 2e-9 of the functions.
@@ -68,33 +68,35 @@ __device__ __forceinline__ void st_el(char *p, float v) {
     else *reinterpret_cast<uint16_t *>(p) = (uint16_t)f32_to_bf16_rne(v);
 }
 
-// Block (rows r0 .. r0 + rows, heads h0 .. h0 + heads of q's and k's laid end to end).
-// VEC: pairs go in whole 16-byte pieces; else pair by pair.
+// n / d for n d < 2^32: a product with 2^32 / d rounded up (0 stands for d = 1).
+struct Divisor {
+    uint32_t d, inv;
+    explicit Divisor(uint32_t n) : d(n), inv(n > 1 ? 0xFFFFFFFFu / n + 1u : 0u) {}
+    __device__ __forceinline__ int of(int n) const { return inv ? (int)__umulhi((uint32_t)n, inv) : n; }
+};
+
+// Block (row, heads h0 .. h0 + heads of q's and k's laid end to end).  A head is n_all items: its pairs,
+// then what passes through.  VEC: pairs go in whole 16-byte pieces; else pair by pair.
 template <bool F32, bool VEC, bool INTER>
-__global__ __launch_bounds__(kThreadsRope) void rope_kernel(RopeArgs a, int rows, int heads) {
+__global__ __launch_bounds__(kThreadsRope) void rope_kernel(RopeArgs a, int heads, int n_rot, Divisor n_all) {
     constexpr int EL = F32 ? 4 : 2, V = 16 / EL;
     __shared__ float2 tab[kTableMax];
     const int tid = threadIdx.x, half = a.rot_dim / 2;
-    const int r0 = blockIdx.x * rows, nr = min(rows, a.M - r0);
+    const int64_t row = blockIdx.x;
     const int h0 = blockIdx.y * heads, nh = min(heads, a.q.heads + a.k.heads - h0);
-    for (int i = tid; i < nr * half; i += kThreadsRope) {
-        const int row = i / half, p = i - row * half;
-        tab[i] = turn_cos_sin((double)a.positions[r0 + row] * a.freqs[p], a.factor, a.inverse ? -1.0f : 1.0f);
-    }
+    const double pos = a.positions[row];
+    for (int i = tid; i < half; i += kThreadsRope)
+        tab[i] = turn_cos_sin(pos * a.freqs[i], a.factor, a.inverse ? -1.0f : 1.0f);
     __syncthreads();
-    // items of a head: the pairs (V at a time), then what passes through (not in place)
-    const int n_rot = VEC ? (INTER ? a.rot_dim / V : half / V) : half;
-    const int n_all = n_rot + (VEC ? (a.head_dim - a.rot_dim) / V : (a.head_dim - a.rot_dim) / 2);
-    const int items = nr * nh * n_all;
+    const float2 *const cs = tab;
+    const int items = nh * (int)n_all.d;
     for (int it = tid; it < items; it += kThreadsRope) {
-        const int head = it / n_all, i = it - head * n_all;
-        const int row = head / nh, h = h0 + head - row * nh;
+        const int head = n_all.of(it), i = it - head * (int)n_all.d, h = h0 + head;
         const bool is_q = h < a.q.heads;
         const RopeHeads &t = is_q ? a.q : a.k;
         const int hh = is_q ? h : h - a.q.heads;
-        const char *x = static_cast<const char *>(t.x) + ((r0 + row) * t.x_stride + (int64_t)hh * a.head_dim) * EL;
-        char *y = static_cast<char *>(t.y) + ((r0 + row) * t.y_stride + (int64_t)hh * a.head_dim) * EL;
-        const float2 *cs = tab + row * half;
+        const char *x = static_cast<const char *>(t.x) + (row * t.x_stride + (int64_t)hh * a.head_dim) * EL;
+        char *y = static_cast<char *>(t.y) + (row * t.y_stride + (int64_t)hh * a.head_dim) * EL;
         if constexpr (VEC) {
             if (i >= n_rot) {
                 const int at = (a.rot_dim + (i - n_rot) * V) * EL;
@@ -146,9 +148,13 @@ hipError_t launch_rope(const RopeArgs &a, hipStream_t s) {
     const int V = a.f32 ? 4 : 8, half = a.rot_dim / 2, n_heads = a.q.heads + a.k.heads;
     if (a.M < 1 || n_heads < 1 || half < 1 || half > kTableMax || a.head_dim % 8 != 0) return hipErrorInvalidValue;
     const bool vec = (a.interleaved ? a.rot_dim % V : half % V) == 0;
-    const int rows = 1, heads = n_heads;
-    const dim3 grid((unsigned)((a.M + rows - 1) / rows), (unsigned)((n_heads + heads - 1) / heads));
-#define ROPE_ONE(F, VE, IN) launch((rope_kernel<F, VE, IN>), grid, dim3(kThreadsRope), 0, s, a, rows, heads)
+    const int n_rot = vec ? (a.interleaved ? a.rot_dim / V : half / V) : half;
+    const int n_all = n_rot + (a.head_dim - a.rot_dim) / (vec ? V : 2);
+    // a block per row; few rows of many items take more blocks, four items a thread
+    int heads = n_heads;
+    if (a.M < 512 && n_heads * n_all > 4 * kThreadsRope) heads = n_all < 4 * kThreadsRope ? 4 * kThreadsRope / n_all : 1;
+    const dim3 grid((unsigned)a.M, (unsigned)((n_heads + heads - 1) / heads));
+#define ROPE_ONE(F, VE, IN) launch((rope_kernel<F, VE, IN>), grid, dim3(kThreadsRope), 0, s, a, heads, n_rot, Divisor((uint32_t)n_all))
 #define ROPE_VEC(F, VE)                                                                        \
     if (a.interleaved) ROPE_ONE(F, VE, true);                                                  \
     else ROPE_ONE(F, VE, false)

@@ -252,21 +252,25 @@ def _buf(a, name: str, n: int, dtypes) -> Optional[int]:
 
 
 def _rows(a, name: str, M: int, width: int, stride: int, dtypes) -> Optional[int]:
-    """_buf of M rows of `width` elements, `stride` apart: a tensor must hold each row's elements side
-    by side, from its first element on."""
+    """_buf of M rows of `width` elements, `stride` apart: a tensor must hold each row's elements side by
+    side, from its first element on."""
     if a is None or isinstance(a, int) or M <= 0:
         return _ptr(a)
     if a.dtype not in dtypes:
         raise ValueError(f"{name}: {a.dtype} given, {dtypes[0]} wanted")
-    at = 1  # elements that the dimensions behind the first hold side by side
-    for n, s in zip(reversed(a.shape[1:]), reversed(a.stride()[1:])):
-        if n != 1 and s != at:
-            at = -1
-            break
-        at *= n
-    if a.dim() < 2 or a.shape[0] < M or at < width or (M > 1 and a.stride(0) != stride):
+    shape, strides = a.shape, a.stride()
+    if len(strides) == 2:
+        held = shape[1] if strides[1] == 1 or shape[1] == 1 else -1
+    else:
+        held = 1  # elements that the dimensions behind the first hold side by side
+        for n, s in zip(reversed(shape[1:]), reversed(strides[1:])):
+            if n != 1 and s != held:
+                held = -1
+                break
+            held *= n
+    if len(strides) < 2 or shape[0] < M or held < width or (M > 1 and strides[0] != stride):
         raise ValueError(f"{name}: {M} rows of {width} elements, {stride} apart, wanted, got"
-                         f" {tuple(a.shape)} with strides {a.stride()}")
+                         f" {tuple(shape)} with strides {strides}")
     dev = a.get_device()
     if dev < 0 or dev != _current_device():
         raise ValueError(f"{name}: a tensor of the current device wanted, got one on {a.device}")
