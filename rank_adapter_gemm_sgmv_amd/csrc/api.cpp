@@ -83,10 +83,10 @@ size_t gemm_bytes(int32_t M, int32_t d_in, int32_t d_out, int32_t r_max, int32_t
     return round_up((a > b ? a : b) * sizeof(float));
 }
 
-// The same of lora_linear_fp8: its tiles' K slices or, for decode batches, the decode plans'.
-size_t fp8_gemm_bytes(int32_t M, int32_t d_in, int32_t d_out, int32_t r_max, int32_t n_adapters) {
+// The same of lora_linear_fp8 and (ints) lora_linear_int8: its tiles' K slices or, for decode batches, the decode plans'.
+size_t fp8_gemm_bytes(int32_t M, int32_t d_in, int32_t d_out, int32_t r_max, int32_t n_adapters, bool ints) {
     const size_t a = fp8_partial_floats(M, d_in, d_out, r_max, n_adapters),
-                 b = decode_fp8_partial_floats(M, d_in, d_out, rank_bucket(r_max), n_adapters);
+                 b = decode_fp8_partial_floats(M, d_in, d_out, rank_bucket(r_max), n_adapters, ints);
     return round_up((a > b ? a : b) * sizeof(float));
 }
 
@@ -586,7 +586,7 @@ namespace {
 // lora_linear_fp8 and lora_linear_int8 (arguments already validated, M > 0):
 //   up to 128 rows, pool padded at a rank bucket: the split-K fp8 GEMM with the shrink as
 //            adapter tiles of the same launch, then the reduction (two launches, no segments)
-//   up to 192 rows: the split-K fp8 GEMM with build_segments in one extra workgroup, the shrink
+//   up to 192 rows (integers: up to 2048 in one round of tiles): the split-K fp8 GEMM with build_segments in one extra workgroup, the shrink
 //            on the codes (chunk sums), the reduction
 //   otherwise: build_segments, the shrink, then the 128 x 128 or 256 x 256 tiles of gemm_fp8.hip
 //            with delta and epilogue fused or, where they are too few to fill the chip, K
@@ -609,7 +609,7 @@ hipError_t run_fp8(const Gemm8<X> &g, const uint16_t *A, const uint16_t *B, cons
     shrink_plan(g.K, rb, &kc, &ksplit);
     hipError_t e;
     const DecodeLora lo{spart, ksplit, B, scale, ids, ranks, rb, n_adapters, nullptr, 0, r_max};
-    const bool decode = decode_fp8_supported(g.M, g.K, g.N);
+    const bool decode = decode_fp8_supported(g.M, g.K, g.N, std::is_same_v<X, int8_t>);
     if (decode && g.M <= kDecodeMaxRows && r_max == rb) {
         if ((e = launch_decode_gemm_fp8_lora_x8(g.x8, g.W8, g.w_scale, A, g.M, g.K, g.N, lo, gpart, s)) !=
             hipSuccess)
@@ -1324,7 +1324,7 @@ size_t workspace8(int32_t M, int32_t d_in, int32_t d_out, int32_t r_max, int32_t
     if (check_common(M, r_max, n_adapters) != LORA_OK || !dim8_ok(d_in, ints) || !dim_ok(d_out)) return 0;
     if (M == 0) return 0;
     return segments_bytes(M, n_adapters) + shrink_partial_bytes(M, d_in, r_max) +
-           fp8_gemm_bytes(M, d_in, d_out, r_max, n_adapters);
+           fp8_gemm_bytes(M, d_in, d_out, r_max, n_adapters, ints);
 }
 
 // lora_linear_fp8 (X: uint8_t) and lora_linear_int8 (int8_t).

@@ -360,8 +360,9 @@ hipError_t launch_decode_gemm_fp8_lora(const uint16_t *x, const uint8_t *W8, con
 // rows' scales are the reduction's epilogue's.  K may be any multiple of 16 from 128
 // (decode_fp8_supported).
 constexpr int kFp8DecodeMaxRows = 192;
-bool decode_fp8_supported(int M, int K, int N);
-size_t decode_fp8_partial_floats(int M, int K, int N, int r_max, int n_adapters);
+constexpr int kInt8DecodeMaxRows = 2048;  // (above kDecodeMaxRows only in one round of tiles)
+bool decode_fp8_supported(int M, int K, int N, bool ints);
+size_t decode_fp8_partial_floats(int M, int K, int N, int r_max, int n_adapters, bool ints);
 template <class X>
 hipError_t launch_decode_gemm_fp8_x8(const X *x8, const X *W8, const float *w_scale,
                                      int M, int K, int N, float *partial, const SegBuild *build,

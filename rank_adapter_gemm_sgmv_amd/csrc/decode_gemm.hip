@@ -1060,12 +1060,25 @@ bool decode_act_supported(int M, int K, int N) {
     return M >= 1 && M <= kDecodeGemmMaxRows && K % 8 == 0 && K >= 128 && N >= 8 && N % 4 == 0;
 }
 
-bool decode_fp8_supported(int M, int K, int N) {
-    return decode_act_supported(M, K, N) && M <= kFp8DecodeMaxRows && K % 16 == 0 && N % 8 == 0;
+// What the kernels of this file take of a batch's sizes, in one launch or another.
+static bool decode_dims_ok(int M, int K, int N) {
+    return M >= 1 && M <= kInt8DecodeMaxRows && K % 8 == 0 && K >= 128 && N >= 8 && N % 4 == 0;
 }
 
-size_t decode_fp8_partial_floats(int M, int K, int N, int r_max, int n_adapters) {
-    if (!decode_fp8_supported(M, K, N)) return 0;
+// Integers need no widening per row tile, so they stay here for more rows than E4M3 codes, as long as
+// the tiles are one round of CUs.  us here and in gemm_fp8.hip's slices or tiles, rank 16 of 8 adapters:
+// 140 x 4096 x 4096 22.5 and 34.1, 256 rows 24.0 and 38.4, 512 rows 34.2 and 41.2; 1024 x 4096 x 2048 33.9
+// and 40.8, 2048 x 4096 x 1024 35.2 and 41.9; rank 32 of 200 adapters 448 x 4096 x 2048 32.8 and 53.5.
+// Beyond: 4096 x 4096 x 512 48.9 and 45.4; more tiles: 192 x 4096 x 11008 (258, 64 adapters) 51.5 and 46.5,
+// 512 x 4096 x 8192 (512) 49.2 and 41.9.
+bool decode_fp8_supported(int M, int K, int N, bool ints) {
+    if (!decode_dims_ok(M, K, N) || K % 16 != 0 || N % 8 != 0) return false;
+    if (!ints || M <= kDecodeMaxRows) return M <= kFp8DecodeMaxRows;
+    return (long)((M + 63) / 64) * ((N + kBN - 1) / kBN) <= 256;
+}
+
+size_t decode_fp8_partial_floats(int M, int K, int N, int r_max, int n_adapters, bool ints) {
+    if (!decode_fp8_supported(M, K, N, ints)) return 0;
     const DecPlan p0 = dec_plan(M, K, N, 0);
     size_t f = (size_t)p0.ks * p0.n_tm * p0.n_tn * p0.bm * kBN;
     if (M <= kDecodeMaxRows) {
@@ -1146,7 +1159,7 @@ template <class X, class WT>
 hipError_t launch_f8(const X *x, const WT *W8, const float *w_scale, int M, int K, int N,
                      float *partial, const SegBuild *build, hipStream_t s) {
     constexpr bool X8 = sizeof(X) == 1;
-    if (!(X8 ? decode_fp8_supported(M, K, N) : decode_gemm_supported(M, K, N)) || N % 8 != 0 || partial == nullptr || w_scale == nullptr)
+    if (!(X8 ? decode_fp8_supported(M, K, N, std::is_same_v<X, int8_t>) : decode_gemm_supported(M, K, N)) || N % 8 != 0 || partial == nullptr || w_scale == nullptr)
         return hipErrorInvalidValue;
     if (build && (build->ids == nullptr || build->n_adapters < 1 || build->n_adapters > LORA_MAX_ADAPTERS))
         return hipErrorInvalidValue;
@@ -1174,7 +1187,7 @@ template <class X, class WT>
 hipError_t launch_f8_lora(const X *x, const WT *W8, const float *w_scale, const uint16_t *A, int M,
                           int K, int N, const DecodeLora &lo, float *partial, hipStream_t s) {
     constexpr bool X8 = sizeof(X) == 1;
-    if (!(X8 ? decode_fp8_supported(M, K, N) : decode_gemm_supported(M, K, N)) || M > kDecodeMaxRows || N % 8 != 0 || partial == nullptr ||
+    if (!(X8 ? decode_fp8_supported(M, K, N, std::is_same_v<X, int8_t>) : decode_gemm_supported(M, K, N)) || M > kDecodeMaxRows || N % 8 != 0 || partial == nullptr ||
         w_scale == nullptr || A == nullptr || lo.ids == nullptr || !rank_ok(lo.r_max) ||
         lo.n_adapters < 1)
         return hipErrorInvalidValue;
@@ -1243,7 +1256,7 @@ template hipError_t launch_decode_gemm_fp8_lora_x8(const int8_t *, const int8_t 
 hipError_t launch_decode_reduce(const float *partial, int M, int K, int N, void *y, bool y_f32,
                                 const DecodeLora &lo, bool adapters, const Seg *seg,
                                 hipStream_t s, const Epilogue *epi) {
-    if (!decode_act_supported(M, K, N) || partial == nullptr || !rank_ok(lo.r_max) ||
+    if (!decode_dims_ok(M, K, N) || partial == nullptr || !rank_ok(lo.r_max) ||
         (!adapters && (lo.tpart == nullptr || lo.n_chunks < 1)))
         return hipErrorInvalidValue;
     const int n_lt = adapters ? adapter_tiles(M, lo.r_max, lo.n_adapters) : 0;
