@@ -618,13 +618,15 @@ hipError_t run_fp8(const Gemm8<X> &g, const uint16_t *A, const uint16_t *B, cons
     }
     if (decode) {
         const SegBuild bld{ids, n_adapters, sg};
+        DecodeLora split = lo;
+        split.two = std::is_same_v<X, int8_t>;  // (72 KB of LDS)
         if ((e = launch_decode_gemm_fp8_x8(g.x8, g.W8, g.w_scale, g.M, g.K, g.N, gpart,
                                            segs ? nullptr : &bld, s)) != hipSuccess)
             return e;
         if ((e = launch_shrink_x8(g.x8, A, ranks, r_max, g.M, g.K, rb, n_adapters, sg, spart, kc, ksplit,
                                   s)) != hipSuccess)
             return e;
-        return launch_decode_reduce(gpart, g.M, g.K, g.N, y, y_f32, lo, false, &sg, s, &epi);
+        return launch_decode_reduce(gpart, g.M, g.K, g.N, y, y_f32, split, false, &sg, s, &epi);
     }
     if (!segs && (e = launch_build_segments(ids, g.M, n_adapters, sg, s)) != hipSuccess) return e;
     if ((e = launch_shrink_x8(g.x8, A, ranks, r_max, g.M, g.K, rb, n_adapters, sg, spart, kc, ksplit,

@@ -305,6 +305,7 @@ struct DecodeLora {
     const int32_t *roff;   // [n] first rank row of each adapter (rank-compact pool), or nullptr
     int pool_rows;
     int pstride;           // padded pool: rank rows per adapter (<= r_max)
+    bool two = false;      // the GEMM before it can hold two workgroups on a CU (dec_plan)
 };
 
 // The segment build the medium-batch decode GEMM launch runs in one extra workgroup beside
