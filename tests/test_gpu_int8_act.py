@@ -89,6 +89,23 @@ def test_matches_64_bits(shape, k):
     c.check(c.run(), f"{shape} {opt}")
 
 
+# The borders of the launch sequences: 64-row tiles that are one round of CUs and one more, splits of K that a
+# quarter more workgroups than CUs makes, 2048 rows and one more, K slices and whole tiles behind them
+BORDERS = [(128, 2048, 11008, 5, 16), (129, 512, 10880, 5, 16), (130, 512, 11008, 5, 16), (256, 1040, 8192, 9, 8),
+           (333, 1040, 2760, 30, 24), (2048, 272, 1024, 40, 16), (2049, 272, 1024, 40, 16), (2048, 160, 1032, 3, 8),
+           (1024, 4112, 2760, 64, 64), (2100, 4096, 264, 6, 16), (1100, 6160, 2056, 4, 5), (2048, 128, 8, 2048, 64)]
+
+
+@pytest.mark.parametrize("shape", BORDERS, ids=lambda c: "x".join(map(str, c)))
+def test_borders_of_the_sequences(shape):
+    at = BORDERS.index(shape)
+    log(f"linear_int8 border {shape}")
+    for f32 in (False, True):
+        c = Call(700 + at, *shape, act=ACTS[at % 5], bias=True, residual=at % 2 == 0, mul=at % 3 == 0, f32=f32,
+                 codes="any")
+        c.check(c.run(), f"{shape} f32={f32}")
+
+
 @pytest.mark.parametrize("M,K,N", BATCHES)
 def test_integer_sums_are_exact(M, K, N):
     """Scales 1, no adapters, fp32: every product sum below 2^24 is returned as it is."""
