@@ -454,7 +454,8 @@ lora_status_t lora_quant_int8(const void *x, int32_t M, int32_t d, void *y8, flo
  * Limits: 1 <= q_heads, k_heads <= LORA_ROPE_MAX_HEADS; head_dim a multiple of 8 up to
  * LORA_ROPE_MAX_DIM; rot_dim even, 2 .. head_dim; strides multiples of 8 from heads * head_dim to
  * LORA_ROPE_MAX_STRIDE (else LORA_ERR_SHAPE).  q, k, q_out, k_out 16-byte aligned, freqs 8.
- * Errors: LORA_ERR_SHAPE (also: in place with two strides), _DTYPE, _MODE (layout), _VALUE (factor not
+ * Errors: LORA_ERR_SHAPE (also: in place with two strides, outputs over each other or over other rows
+ * than their own, as far as the strides show it), _DTYPE, _MODE (layout), _VALUE (factor not
  * finite or not positive, inverse not 0 or 1), _NULL, _ALIGN, _HIP. */
 typedef enum LORA_ENUM_INT { LORA_ROPE_HALF = 0, LORA_ROPE_INTERLEAVED = 1 } lora_rope_t;
 #define LORA_ROPE_MAX_HEADS 1024

@@ -1442,6 +1442,40 @@ lora_status_t lora_quant_int8(const void *x, int32_t M, int32_t d, void *y8, flo
     return rows_call(x, nullptr, nullptr, 1.0f, M, d, nullptr, nullptr, y8, y_scale, true, false, stream);
 }
 
+}  // extern "C"
+
+namespace {
+
+// M rows of `width` bytes, `stride` apart.
+struct RowSet {
+    uintptr_t at;
+    int64_t width, stride;
+};
+
+// Whether two of them share a byte (of different strides: where one has no gaps, or their first rows do).
+bool rows_overlap(const RowSet &a, const RowSet &b, int32_t M) {
+    auto end = [M](const RowSet &r) { return r.at + (uintptr_t)(r.stride * (M - 1) + r.width); };
+    if (a.at >= end(b) || b.at >= end(a)) return false;
+    if (M == 1) return true;
+    if (a.stride != b.stride) {
+        for (const auto &[full, other] : {std::pair{a, b}, std::pair{b, a}}) {
+            if (full.stride != full.width) continue;
+            // the first of other's rows that ends behind full's start
+            const int64_t before = (int64_t)(full.at - other.at) - other.width;
+            const int64_t m = full.at > other.at && before >= 0 ? before / other.stride + 1 : 0;
+            if (m < M && other.at + (uintptr_t)(m * other.stride) < end(full)) return true;
+        }
+        return a.at < b.at + (uintptr_t)b.width && b.at < a.at + (uintptr_t)a.width;
+    }
+    const RowSet &lo = a.at <= b.at ? a : b, &hi = a.at <= b.at ? b : a;
+    const int64_t d = (int64_t)((hi.at - lo.at) % (uintptr_t)a.stride);
+    return d < lo.width || d + hi.width > a.stride;
+}
+
+}  // namespace
+
+extern "C" {
+
 lora_status_t lora_rope(const void *q, const void *k, const int32_t *positions, const double *freqs,
                         int32_t M, int32_t q_heads, int32_t k_heads, int32_t head_dim, int32_t rot_dim,
                         int64_t q_stride, int64_t k_stride, lora_rope_t layout, float factor,
@@ -1469,6 +1503,18 @@ lora_status_t lora_rope(const void *q, const void *k, const int32_t *positions, 
     if (!aligned(q, 16) || !aligned(q_out, 16) || !aligned(positions, 4) || !aligned(freqs, 8) ||
         (k_heads > 0 && (!aligned(k, 16) || !aligned(k_out, 16))))
         return LORA_ERR_ALIGN;
+    auto rows = [&](const void *p, int32_t heads, int64_t stride) {
+        const int64_t el = dtype == LORA_F32 ? 4 : 2;
+        return RowSet{reinterpret_cast<uintptr_t>(p), heads * (int64_t)head_dim * el, stride * el};
+    };
+    const RowSet rq = rows(q, q_heads, q_stride), ro = rows(q_out, q_heads, q_out_stride);
+    if (q != q_out && rows_overlap(rq, ro, M)) return LORA_ERR_SHAPE;
+    if (k_heads > 0) {
+        const RowSet rk = rows(k, k_heads, k_stride), so = rows(k_out, k_heads, k_out_stride);
+        if ((k != k_out && rows_overlap(rk, so, M)) || rows_overlap(ro, so, M) || rows_overlap(rq, so, M) ||
+            rows_overlap(rk, ro, M))
+            return LORA_ERR_SHAPE;
+    }
     clear_stale_error();
     return hip_status(launch_rope(a, (hipStream_t)stream));
 }

@@ -765,7 +765,7 @@ __global__ __launch_bounds__(256) void reduce_lora_kernel(const float *__restric
 constexpr int kSubRows = 4;
 constexpr int kSegCpt = 2;               // columns per thread
 constexpr int kSegCols = 256 * kSegCpt;  // columns per item
-constexpr int kSegMaxTiles = 512;        // tiles a block scans (lora_max_tiles at M <= 256)
+constexpr int kSegMaxTiles = 512;        // tiles a block scans (lora_max_tiles: M / 16 and one per adapter)
 template <int RM, bool YF32, int MS, bool PADRM, bool EPI>
 __global__ __launch_bounds__(256) void reduce_seg_kernel(const float *__restrict__ partial,
                                                          int M, int N, int n_tm, int n_tn,

@@ -280,3 +280,16 @@ def test_operands_past_4_gib():
         assert torch.equal(c.y[rows].double(), want)
         del c, x
         torch.cuda.empty_cache()
+
+
+@pytest.mark.parametrize("M,K,N", [(512, 272, 1032), (2048, 160, 264), (2048, 128, 1024)])
+def test_the_largest_adapter_table(M, K, N):
+    """Segments of 16384 adapters in one workgroup beside the GEMM, ids that use a few and the last of them."""
+    n, r = L.LORA_MAX_ADAPTERS, 8
+    c = Call(23, M, K, N, n, r, act="silu", bias=True, mul=True)
+    c.check(c.run(), f"{M} {K} {N}")
+    want = c.run().clone()
+    seg = L.Segments(M, n)
+    L.lora_build_segments(c.ids, M, n, seg)
+    c.y.fill_(7)
+    assert torch.equal(c.run(segs=seg), want)

@@ -40,6 +40,53 @@ def test_rope_rejects(over, code):
     assert e.value.status == code
 
 
+E = 2  # bytes of bf16
+
+
+@pytest.mark.parametrize("over", [
+    dict(),  # (k_out lies on q_out)
+    dict(k_out=FAKE), dict(k_out=3 * FAKE, q_out=FAKE + 16), dict(q=FAKE, k=4 * FAKE, k_out=FAKE + 512 * E),
+    dict(k_out=2 * FAKE + 3 * 512 * E + 16), dict(M=1, k_out=2 * FAKE + 1008),
+    # a row of q, k and v: k_out reaches into q's part, q_out into the next row's
+    dict(q_stride=768, k_stride=768, q_out_stride=768, k_out_stride=768, k=FAKE + 512 * E, q_out=FAKE,
+         k_out=FAKE + 504 * E),
+    dict(q_stride=768, k_stride=768, q_out_stride=768, k_out_stride=768, q=3 * FAKE + 512 * E, k=5 * FAKE,
+         q_out=2 * FAKE + 272 * E, k_out=2 * FAKE + 768 * 4 * E - 32),
+    dict(q_stride=640, q_out_stride=640, q=FAKE, q_out=FAKE + 640 * E, k_out=9 * FAKE, k=8 * FAKE),
+])
+def test_rope_rejects_outputs_over_each_other(over):
+    with pytest.raises(L.LoraError) as e:
+        _rope(**over)
+    assert e.value.status == 2
+
+
+@pytest.mark.skipif(torch.cuda.is_available(), reason="addresses of no memory must not reach a GPU")
+@pytest.mark.parametrize("seed", range(4))
+def test_rope_takes_rows_beside_each_other(seed):
+    """Outputs given over rows against a plain count of bytes: what is refused overlaps, and every overlap that
+    equal or gapless strides show is refused.  (A call that passes would launch; without a GPU it ends in
+    another error.)"""
+    import random
+
+    rnd = random.Random(seed)
+    seen = [0, 0]
+    for _ in range(400):
+        M, qw, kw = rnd.choice([1, 2, 5]), 16 * rnd.randint(1, 3), 16
+        dense = rnd.random() < 0.5
+        sq = qw if dense else qw + 16 * rnd.randint(0, 4)
+        sk = sq if not dense and sq >= kw else kw + 8 * rnd.randint(0, 6)
+        qo, ko = FAKE, FAKE + 16 * rnd.randint(-30, 60)
+        a = {qo + 2 * (m * sq + j) for m in range(M) for j in range(qw)}
+        b = {ko + 2 * (m * sk + j) for m in range(M) for j in range(kw)}
+        hit = bool(a & b)
+        seen[hit] += 1
+        with pytest.raises(L.LoraError) as e:
+            _rope(M=M, q_heads=qw // 16, k_heads=1, head_dim=16, rot_dim=16, q=FAKE << 8, k=FAKE << 9,
+                  q_stride=sq, k_stride=sk, q_out=qo, q_out_stride=sq, k_out=ko, k_out_stride=sk)
+        assert (e.value.status == 2) == hit, (M, qw, sq, sk, ko - qo)
+    assert min(seen) > 40
+
+
 def test_rope_empty_batch_is_noop():
     _rope(M=0, q=None, k=None, q_out=None, k_out=None, positions=None, freqs=None)
     _rope(M=0, k_heads=0, k=None, k_out=None, k_stride=0, k_out_stride=0)
