@@ -435,8 +435,16 @@ MoePlan moe_plan(int M, int top_k, int E, int K, int N, int r_max, int n_adapter
 MoePlan moe_layer_plan(int M, int top_k, int E, int K, int N, int r_max, int n_adapters, int n_proj, MoeRows rows) {
     MoePlan p = moe_plan(M, top_k, E, K, N, r_max, n_adapters);
     const int P = M * top_k, slots = E < P ? E : P;
-    // workgroups of a split, with an adapter tile per expert and projection
-    const long tiles = (long)slots * n_proj * (p.n_tn + 1);
+    // workgroups of a split, with the adapter tiles that an expert's average pairs can need
+    const int apt = kBN / p.rm, per = (P + slots - 1) / slots, distinct = n_adapters < per ? n_adapters : per;
+    const long tiles = (long)slots * n_proj * (p.n_tn + (distinct + apt - 1) / apt);
+    // Rows of a block, by the pairs an expert has on average: a block streams the expert's W once more, and a
+    // larger one has more x to stage and more to multiply.  us of the layer's call, 8 experts of 1040 x 2768,
+    // 40 adapters of rank 24.  16 or 32 rows in bf16: 5 pairs 108 and 111 (32 experts of 1440 x 1440), 10:
+    // 121.5 and 121.9, 12: 132 and 126.  32 or 64: 12 pairs 62.3 and 65.9, 25: 71.0 and 74.6, 32: 88.5 and 87.0,
+    // 50: 126 and 102, 100: 194 and 162.  Parts of rows, four to a pair, 32 or 64: 4 pairs 56.5 and 58.3, 6:
+    // 59.2 and 58.0, 7: 65.2 and 60.2, 25: 97.7 and 85.1, 100: 350 and 255.
+    if (P > (rows == kMoeParts ? 5 : 30) * slots) p.bm = 64;
     p.few = rows != kMoeParts && P <= 10 * slots;
     int ks = (int)(256 / tiles);
     const int kq = (K + kBKW * kWaves - 1) / (kBKW * kWaves);
@@ -454,7 +462,7 @@ size_t moe_tpart_floats(const MoePlan &p, int P) { return (size_t)p.ks * P * p.r
 hipError_t launch_moe_gemm(const MoePlan &p, const MoeGemmArgs &args, hipStream_t s) {
     if (args.P < 1 || args.P > LORA_MOE_MAX_PAIRS || args.K % 16 != 0 || args.K < 128 || args.n_proj < 1 || args.n_proj > 2 ||
         args.N < 8 || args.N % 8 != 0 || args.r_stride % 8 != 0 || args.r_stride > p.rm ||
-        args.n_adapters > LORA_MAX_ADAPTERS || p.bm != 32)
+        args.n_adapters > LORA_MAX_ADAPTERS || (p.bm != 32 && p.bm != 64))
         return hipErrorInvalidValue;
     MoeGemmArgs a = args;
     a.n_tn = p.n_tn;
@@ -480,6 +488,9 @@ hipError_t launch_moe_gemm(const MoePlan &p, const MoeGemmArgs &args, hipStream_
     }
     if (p.few) {
         using DEC = Dec<32, uint16_t, 16>;
+        MOE_RM()
+    } else if (p.bm == 64) {
+        using DEC = Dec<64>;
         MOE_RM()
     } else {
         using DEC = Dec<32>;

@@ -134,6 +134,7 @@ SHAPES = [
     (33, 4, 4, 384, 1408, 33, 56), (64, 4, 32, 256, 384, 8, 16), (100, 2, 6, 2064, 144, 7, 40),
     (65, 1, 3, 160, 2880, 100, 16), (7, 64, 70, 128, 144, 4, 8), (300, 2, 4, 176, 208, 5, 16),
     (50, 2, 700, 128, 144, 3, 8), (33, 2, 128, 144, 128, 90, 64), (16, 4, 66, 128, 272, 20, 16),
+    (17, 2, 6, 144, 272, 9, 16), (99, 3, 5, 272, 144, 11, 24), (241, 1, 8, 128, 400, 64, 64),
     (2, 2, 4096, 128, 128, 2, 8), (9, 3, 700, 144, 128, 3, 8), (130, 8, 9, 128, 256, 500, 8), (40, 5, 3, 128, 144, 2, 8),
 ]
 
