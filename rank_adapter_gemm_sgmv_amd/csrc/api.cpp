@@ -584,10 +584,11 @@ lora_status_t check_fp8w(const void *x, const void *W8, const float *w_scale, co
 namespace {
 
 // lora_linear_fp8 and lora_linear_int8 (arguments already validated, M > 0):
-//   up to 128 rows, pool padded at a rank bucket: the split-K fp8 GEMM with the shrink as
-//            adapter tiles of the same launch, then the reduction (two launches, no segments)
-//   up to 192 rows (integers: up to 2048 in one round of tiles): the split-K fp8 GEMM with build_segments in one extra workgroup, the shrink
-//            on the codes (chunk sums), the reduction
+//   up to 128 rows, pool padded at a rank bucket (integers: at a multiple of 8, and more rows with few
+//            adapter tiles): the split-K 8-bit GEMM with the shrink as adapter tiles of the same
+//            launch, then the reduction (two launches, no segments)
+//   up to 192 rows (integers: up to 2048 in one round of tiles): the split-K 8-bit GEMM with
+//            build_segments in one extra workgroup, the shrink on the codes (chunk sums), the reduction
 //   otherwise: build_segments, the shrink, then the 128 x 128 or 256 x 256 tiles of gemm_fp8.hip
 //            with delta and epilogue fused or, where they are too few to fill the chip, K
 //            slices and the pass that adds slices, delta and epilogue
@@ -610,7 +611,18 @@ hipError_t run_fp8(const Gemm8<X> &g, const uint16_t *A, const uint16_t *B, cons
     hipError_t e;
     const DecodeLora lo{spart, ksplit, B, scale, ids, ranks, rb, n_adapters, nullptr, 0, r_max};
     const bool decode = decode_fp8_supported(g.M, g.K, g.N, std::is_same_v<X, int8_t>);
-    if (decode && g.M <= kDecodeMaxRows && r_max == rb) {
+    if constexpr (std::is_same_v<X, int8_t>) {
+        if (decode && r_max % 8 == 0 && decode_int8_fused(g.M, rb, n_adapters)) {
+            const Int8Decode d = decode_int8_plan(g.M, g.K, g.N);
+            DecodeLora t = lo;
+            t.tpart = gpart + d.t_at;
+            t.n_chunks = d.n_c;
+            t.two = true;
+            if ((e = launch_decode_gemm_int8_lora(g.x8, g.W8, g.w_scale, A, g.M, g.K, g.N, lo, gpart, s)) != hipSuccess)
+                return e;
+            return launch_decode_reduce(gpart, g.M, g.K, g.N, y, y_f32, t, false, nullptr, s, &epi);
+        }
+    } else if (decode && g.M <= kDecodeMaxRows && r_max == rb) {
         if ((e = launch_decode_gemm_fp8_lora_x8(g.x8, g.W8, g.w_scale, A, g.M, g.K, g.N, lo, gpart, s)) !=
             hipSuccess)
             return e;

@@ -368,10 +368,21 @@ template <class X>
 hipError_t launch_decode_gemm_fp8_x8(const X *x8, const X *W8, const float *w_scale,
                                      int M, int K, int N, float *partial, const SegBuild *build,
                                      hipStream_t s);
-template <class X>
-hipError_t launch_decode_gemm_fp8_lora_x8(const X *x8, const X *W8, const float *w_scale,
+hipError_t launch_decode_gemm_fp8_lora_x8(const uint8_t *x8, const uint8_t *W8, const float *w_scale,
                                           const uint16_t *A, int M, int K, int N,
                                           const DecodeLora &lo, float *partial, hipStream_t s);
+// The same on integers (batches of decode_int8_fused; a pool whose stride is a multiple of 8): adapter tiles with
+// chunks of K of their own, t's sums at partial + t_at as [n_c][M][r_max], after what the reduction
+// without adapter tiles (DecodeLora::two) adds.
+struct Int8Decode {
+    int k_per_chunk, n_c;
+    size_t t_at;
+};
+Int8Decode decode_int8_plan(int M, int K, int N);
+bool decode_int8_fused(int M, int r_max, int n_adapters);  // (r_max: the rank bucket)
+hipError_t launch_decode_gemm_int8_lora(const int8_t *x8, const int8_t *W8, const float *w_scale,
+                                        const uint16_t *A, int M, int K, int N, const DecodeLora &lo,
+                                        float *partial, hipStream_t s);
 
 // y = (split partials added in order) + scale_a * t B_a, t from the adapter tiles' splits
 // (`adapters`) or from the segment-path shrink's chunk sums; rounds once into y.  With the

@@ -369,7 +369,8 @@ struct DecF8 {
     static constexpr int SLOT = XSLOT + kWaves * WSLOT_W;  // uint4 per ring slot
     static constexpr int TILE = BM * kBN;
     static constexpr int BUILD16 = ((LORA_MAX_ADAPTERS + 1 + 15) / 16 * 64 + 64 * 4 + 15) / 16;
-    static constexpr int LDS16 = 3 * SLOT > BUILD16 ? 3 * SLOT : BUILD16;  // uint4 of LDS
+    static constexpr int RING16 = 3 * SLOT;                                  // uint4 of the ring
+    static constexpr int LDS16 = RING16 > BUILD16 ? RING16 : BUILD16;        // uint4 of LDS
     static_assert(XI >= 1 && XSLOT % (kWaves * 64) == 0, "whole x loads per wave");
 };
 
@@ -597,6 +598,96 @@ __global__ __launch_bounds__(kThreads) void decode_gemm_fp8_lora_kernel(
     dec_kloop<CB>(acc, src, lds + wave * CB::WAVE, kw0, (kw1 - kw0) / kBKW, K, RM, lane);
     dec_tile_out<CB, true>(acc, lds, lo, M, partial + ((size_t)split * n_tiles + tile) * CB::TILE, tid,
                      lane, wave);
+}
+
+// The same on integers (lora_linear_int8), with adapter tiles of their own: rows in blocks of CB::XR = 16,
+// K in n_c chunks of k_per_chunk, workgroup (row block, lt, chunk).  An adapter tile
+// streams bf16, so twice a W tile's bytes for the same k, and with W's split and row tiles it was what the
+// launch waited for: 40 x 4096 x 11008 20.7 us per call where the base alone takes 13.8.  The block's
+// distinct adapters stand side by side, ascending, 128 / RM to a tile; each row keeps its own adapter's columns, as
+// a chunk's sums of t for the reduction.  80 KB of LDS: two workgroups fit a CU.
+template <class CF, class CB, int RM>
+__global__ __launch_bounds__(kThreads, 2) void decode_gemm_int8_lora_kernel(
+    const int8_t *__restrict__ x, const int8_t *__restrict__ W8, const float *__restrict__ w_scale,
+    const uint16_t *__restrict__ A, int M, int K, int N, int n_tm, int n_tn, int k_per_split,
+    float *__restrict__ partial, DecodeLora lo, int n_adapter_blocks, int n_lt, int n_c, int k_per_chunk,
+    float *__restrict__ tpart) {
+    constexpr int L16 = CF::RING16 > kWaves * CB::WAVE ? CF::RING16 : kWaves * CB::WAVE;
+    static_assert(L16 * 16 <= 80 << 10, "two workgroups per CU");
+    constexpr int APT = AdapterTiles<RM>::APT, XR = CB::XR;
+    __shared__ __attribute__((aligned(1024))) uint4 lds[L16];
+
+    const int tid = threadIdx.x, lane = tid & 63;
+    const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+    if ((int)blockIdx.x >= n_adapter_blocks) {
+        const int n_tiles = n_tm * n_tn, n_gemm = gridDim.x - n_adapter_blocks;
+        int lin = blockIdx.x - n_adapter_blocks;
+        if (n_tm > 1 && (n_gemm & 7) == 0) lin = (lin & 7) * (n_gemm >> 3) + (lin >> 3);
+        const int tile = lin % n_tiles, split = lin / n_tiles;
+        f8_tile<CF, true>(lds, x, W8, w_scale, M, K, N, n_tiles, tile, split, tile % n_tm, tile / n_tm,
+                          k_per_split, partial, lane, wave);
+        return;
+    }
+    int lin = blockIdx.x;
+    const int chunk = lin % n_c;
+    lin /= n_c;
+    const int lt = lin % n_lt, m0 = lin / n_lt * XR;
+    // every wave finds the tile's adapters (slots lt * APT ..) by itself: lane k < APT holds slot k's, or -1
+    const int id = lane < XR && m0 + lane < M ? lo.ids[m0 + lane] : -1;
+    const bool kept = id >= 0 && id < lo.n_adapters;
+    int different;
+    const int rank = wave_rank(id, kept, XR, different), slot = kept ? rank - lt * APT : -1;
+    if (lt * APT >= different) return;  // whole workgroup
+    int ad = -1;
+#pragma unroll
+    for (int q = 0; q < XR; ++q) {
+        const int u = __builtin_amdgcn_readlane(id, q);
+        if (__builtin_amdgcn_readlane(slot, q) == lane) ad = u;
+    }
+    const int first = __builtin_amdgcn_readlane(ad, 0);
+    DecSrc<CB> src;
+#pragma unroll
+    for (int q = 0; q < CB::WINS; ++q) {
+        const int r = 4 * q + (lane >> 4);
+        const int col = ((lane & 15) ^ wsw(r)) * 8;
+        int a = __shfl(ad, col / RM, 64);
+        if (a < 0) a = first;          // an empty slot reads a valid adapter, unused
+        int cc = col % RM;
+        if (cc >= lo.pstride) cc = 0;  // bucket columns past the pool's: unused
+        src.wp[q] = A + ((size_t)a * K + r) * lo.pstride + cc;
+    }
+    dec_x_src<CB>(src, x, M, K, m0, lane);
+    const int col = tid & 127;
+    const int mine = __shfl(ad, col / RM, 64);  // this thread's column's adapter
+    f32x16_t acc[CB::TM][CB::TN];
+#pragma unroll
+    for (int i = 0; i < CB::TM; ++i)
+#pragma unroll
+        for (int j = 0; j < CB::TN; ++j)
+#pragma unroll
+            for (int v = 0; v < 16; ++v) acc[i][j][v] = 0.0f;
+    const int ks0 = chunk * k_per_chunk;
+    const int ks1 = min(K, ks0 + k_per_chunk);
+    const int per_wave = k_per_chunk / kWaves;  // multiple of 16
+    const int kw0 = min(ks1, ks0 + wave * per_wave);
+    const int kw1 = min(ks1, kw0 + per_wave);
+    dec_kloop<CB>(acc, src, lds + wave * CB::WAVE, kw0, (kw1 - kw0) / kBKW, K, lo.pstride, lane);
+    touch_tables(lo, M, tid);  // (waits for the ring's last loads)
+    __syncthreads();           // every wave is done with its stages
+    float4 *const red = reinterpret_cast<float4 *>(lds);
+    reduce_waves_put<CB>(acc, red + wave * (CB::TILE / 4), lane);
+    __syncthreads();
+#pragma unroll
+    for (int q = 0; q < XR / 8; ++q) {
+        const int g = (tid >> 7) + 2 * q;  // rows 4 g .. 4 g + 3 of the block
+        const float4 s = reduce_waves_group<CB>(red, g, col);
+        const float sv[4] = {s.x, s.y, s.z, s.w};
+#pragma unroll
+        for (int v = 0; v < 4; ++v) {
+            const int m = m0 + 4 * g + v;
+            if (m < M && mine >= 0 && lo.ids[m] == mine) st_wt(&tpart[((size_t)chunk * M + m) * RM + col % RM], sv[v]);
+        }
+    }
 }
 
 // y[m, n .. n+3] = (sum over splits, in order, of the partial tiles)
@@ -1080,11 +1171,42 @@ bool decode_fp8_supported(int M, int K, int N, bool ints) {
     return (long)((M + 63) / 64) * ((N + kBN - 1) / kBN) <= 256;
 }
 
+// The most adapter tiles of a block of rows of decode_gemm_int8_lora_kernel.
+constexpr int kInt8BlockRows = 16;
+static int int8_adapter_tiles(int r_max, int n_adapters) {
+    const int apt = kBN / r_max, distinct = n_adapters < kInt8BlockRows ? n_adapters : kInt8BlockRows;
+    return (distinct + apt - 1) / apt;
+}
+
+// More rows than the decode batches' take that launch while its adapter tiles are few; each streams its
+// adapters again, which the shrink on segments reads once.  us per call, fused and on segments: 32 tiles (256 x
+// 4096 x 4096, 128 adapters of rank 16) 20.8 and 24.7, (512 rows, 8 of rank 16) 28.2 and 31.3; 36 (140 rows, 8 of
+// rank 64) 21.4 and 26.8; 64 (1024 x 4096 x 2048, 8 of rank 16) 39.2 and 31.7; 84 (333 x 4112 x 2760, 128 of rank 24)
+// 35.8 and 33.9; 128 (256 x 4096 x 4096, 64 of rank 64) 41.2 and 34.5.
+bool decode_int8_fused(int M, int r_max, int n_adapters) {
+    return M <= kDecodeMaxRows ||
+           (long)(M + kInt8BlockRows - 1) / kInt8BlockRows * int8_adapter_tiles(r_max, n_adapters) <= 48;
+}
+
+// Chunks of 512 k: eight steps a wave, one x stage.  us per call with chunks of 256, 512 and half a split of W:
+// 40 x 4096 x 11008, 32 adapters of rank 16 18.0, 18.1, 20.3; 100 x 4096 x 2048, 50 of rank 24 18.9, 15.3, 18.8;
+// 128 x 4096 x 4096, 200 of rank 64 40, 34, 34; 1 x 11008 x 4096 15.5, 14.9, 15.2.  At most 64 (the reduction
+// stages that many of 64 ranks).
+Int8Decode decode_int8_plan(int M, int K, int N) {
+    const DecPlan p = dec_plan(M, K, N, 0, true);
+    Int8Decode d;
+    for (d.k_per_chunk = 512; (d.n_c = (K + d.k_per_chunk - 1) / d.k_per_chunk) > 64;) d.k_per_chunk *= 2;
+    d.t_at = (size_t)p.ks * p.n_tm * p.n_tn * p.bm * kBN;
+    return d;
+}
+
 size_t decode_fp8_partial_floats(int M, int K, int N, int r_max, int n_adapters, bool ints) {
     if (!decode_fp8_supported(M, K, N, ints)) return 0;
     const DecPlan p0 = dec_plan(M, K, N, 0, ints);
     size_t f = (size_t)p0.ks * p0.n_tm * p0.n_tn * p0.bm * kBN;
-    if (M <= kDecodeMaxRows) {
+    if (ints) {
+        if (decode_int8_fused(M, r_max, n_adapters)) f += (size_t)decode_int8_plan(M, K, N).n_c * M * r_max;
+    } else if (M <= kDecodeMaxRows) {
         const DecPlan p = dec_plan(M, K, N, adapter_tiles(M, r_max, n_adapters));
         const size_t fa = (size_t)p.ks * p.n_tm * (p.n_tn + p.n_lt) * p.bm * kBN;
         if (fa > f) f = fa;
@@ -1243,18 +1365,45 @@ hipError_t launch_decode_gemm_fp8_lora(const uint16_t *x, const uint8_t *W8, con
     return launch_f8_lora(x, W8, w_scale, A, M, K, N, lo, partial, s);
 }
 
-template <class X>
-hipError_t launch_decode_gemm_fp8_lora_x8(const X *x8, const X *W8, const float *w_scale,
+hipError_t launch_decode_gemm_fp8_lora_x8(const uint8_t *x8, const uint8_t *W8, const float *w_scale,
                                           const uint16_t *A, int M, int K, int N,
                                           const DecodeLora &lo, float *partial, hipStream_t s) {
     return launch_f8_lora(x8, W8, w_scale, A, M, K, N, lo, partial, s);
 }
-template hipError_t launch_decode_gemm_fp8_lora_x8(const uint8_t *, const uint8_t *, const float *,
-                                                   const uint16_t *, int, int, int, const DecodeLora &,
-                                                   float *, hipStream_t);
-template hipError_t launch_decode_gemm_fp8_lora_x8(const int8_t *, const int8_t *, const float *,
-                                                   const uint16_t *, int, int, int, const DecodeLora &,
-                                                   float *, hipStream_t);
+
+hipError_t launch_decode_gemm_int8_lora(const int8_t *x8, const int8_t *W8, const float *w_scale,
+                                        const uint16_t *A, int M, int K, int N, const DecodeLora &lo,
+                                        float *partial, hipStream_t s) {
+    if (!decode_fp8_supported(M, K, N, true) || partial == nullptr || w_scale == nullptr || A == nullptr ||
+        lo.ids == nullptr || !rank_ok(lo.r_max) || lo.n_adapters < 1 ||
+        !decode_int8_fused(M, lo.r_max, lo.n_adapters) || lo.pstride % 8 != 0 || lo.pstride < 8 ||
+        lo.pstride > lo.r_max)
+        return hipErrorInvalidValue;
+    const DecPlan p = dec_plan(M, K, N, 0, true);
+    const Int8Decode d = decode_int8_plan(M, K, N);
+    constexpr int XR = kInt8BlockRows;
+    const int n_lt = int8_adapter_tiles(lo.r_max, lo.n_adapters), n_ad = (M + XR - 1) / XR * n_lt * d.n_c;
+    const dim3 grid(n_ad + p.n_tm * p.n_tn * p.ks);
+#define I8L_ONE(BM, RMX)                                                                        \
+    launch((decode_gemm_int8_lora_kernel<DecF8<BM, int8_t>, Dec<32, int8_t, XR>, RMX>), grid, dim3(kThreads), 0, \
+           s, x8, W8, w_scale, A, M, K, N, p.n_tm, p.n_tn, p.k_per_split, partial, lo, n_ad, n_lt, d.n_c, \
+           d.k_per_chunk, partial + d.t_at)
+#define I8L_RANK(BM)                                                                            \
+    switch (lo.r_max) {                                                                         \
+        case 8: I8L_ONE(BM, 8); break;                                                          \
+        case 16: I8L_ONE(BM, 16); break;                                                        \
+        case 32: I8L_ONE(BM, 32); break;                                                        \
+        default: I8L_ONE(BM, 64); break;                                                        \
+    }
+    if (p.bm == 32) {
+        I8L_RANK(32)
+    } else {
+        I8L_RANK(64)
+    }
+#undef I8L_RANK
+#undef I8L_ONE
+    return hipGetLastError();
+}
 
 hipError_t launch_decode_reduce(const float *partial, int M, int K, int N, void *y, bool y_f32,
                                 const DecodeLora &lo, bool adapters, const Seg *seg,
@@ -1267,8 +1416,12 @@ hipError_t launch_decode_reduce(const float *partial, int M, int K, int N, void 
     const bool padrm = lo.roff == nullptr && lo.pstride == lo.r_max;
     const Epilogue ep = epi ? *epi : Epilogue{};
     // (at most kDecodeMaxRows rows the rows of an adapter are too few to share B; there the
-    // row kernel's shorter chain wins)
-    if (!adapters && seg != nullptr && M > kDecodeMaxRows &&
+    // row kernel's shorter chain wins; behind integers' GEMM, whose few splits make the partial tiles no longer
+    // the larger part, it does up to rank 32 for all rows.  us of lora_linear_int8, by rows and by items: 200 x
+    // 4096 x 4096, rank 16 22.9 and 24.0, 333 x 4112 x 2760, 128 of rank 24 34.1 and 35.4, 2048 x 2048 x 1024,
+    // 200 of rank 32 40.8 and 43.4; 512 x 4096 x 4096, 32 of rank 64 44.2 and 42.1)
+    const bool by_rows = lo.two && lo.r_max <= 32;
+    if (!adapters && !by_rows && seg != nullptr && M > kDecodeMaxRows &&
         lora_max_tiles(M, lo.n_adapters) <= kSegMaxTiles) {
         // one block per (item, kSegCols columns), as many items as a batch of M rows and
         // n adapters can have

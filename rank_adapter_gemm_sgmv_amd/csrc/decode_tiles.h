@@ -192,6 +192,22 @@ struct AdapterTiles {
     static constexpr int APT = kBN / RM;  // adapters per tile
 };
 
+// A lane's rank: how many different values below its own the kept lanes (of the first n) hold; different:
+// how many they hold in all.
+__device__ __forceinline__ int wave_rank(int v, bool kept, int n, int &different) {
+    int rank = 0;
+    different = 0;
+    for (int q = 0; q < n; ++q) {  // (n and what is read of lane q are uniform)
+        const int u = __builtin_amdgcn_readlane(v, q);
+        const uint64_t same = __ballot(kept && v == u);
+        if ((same & ((2ull << q) - 1)) == (1ull << q)) {  // lane q is kept and the first of its value
+            rank += u < v;
+            ++different;
+        }
+    }
+    return rank;
+}
+
 // The K loop of one wave: acc += x[rows, kw0 .. kw0 + 16 nst) W[same k, tile], streamed
 // through the wave's own part of the LDS (mine_lds, C::WAVE uint4) by direct loads; the
 // stages past the last reload it and are not computed.  Returns with loads of the ring still

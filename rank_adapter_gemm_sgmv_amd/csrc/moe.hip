@@ -48,21 +48,7 @@ struct MoeShared {
 };
 
 // Batches of at most 64 pairs need no list in LDS and no barrier to find a workgroup's work: every wave
-// holds all pairs, one per lane.  A lane's rank: how many different values below its own the kept lanes
-// (of the first n) hold; different: how many they hold in all.
-__device__ __forceinline__ int wave_rank(int v, bool kept, int n, int &different) {
-    int rank = 0;
-    different = 0;
-    for (int q = 0; q < n; ++q) {  // (n and what is read of lane q are uniform)
-        const int u = __builtin_amdgcn_readlane(v, q);
-        const uint64_t same = __ballot(kept && v == u);
-        if ((same & ((2ull << q) - 1)) == (1ull << q)) {  // lane q is kept and the first of its value
-            rank += u < v;
-            ++different;
-        }
-    }
-    return rank;
-}
+// holds all pairs, one per lane.
 
 // The a-th expert, ascending, that some pair is routed to (-1: fewer are).  Only batches with fewer
 // pairs than experts ask; the others give every expert its workgroups.

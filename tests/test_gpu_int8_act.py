@@ -93,7 +93,10 @@ def test_matches_64_bits(shape, k):
 # quarter more workgroups than CUs makes, 2048 rows and one more, K slices and whole tiles behind them
 BORDERS = [(128, 2048, 11008, 5, 16), (129, 512, 10880, 5, 16), (130, 512, 11008, 5, 16), (256, 1040, 8192, 9, 8),
            (333, 1040, 2760, 30, 24), (2048, 272, 1024, 40, 16), (2049, 272, 1024, 40, 16), (2048, 160, 1032, 3, 8),
-           (1024, 4112, 2760, 64, 64), (2100, 4096, 264, 6, 16), (1100, 6160, 2056, 4, 5), (2048, 128, 8, 2048, 64)]
+           (1024, 4112, 2760, 64, 64), (2100, 4096, 264, 6, 16), (1100, 6160, 2056, 4, 5), (2048, 128, 8, 2048, 64),
+           # adapter tiles beside W's: blocks of 16 rows, chunks of 512 k, 48 tiles and one more
+           (17, 512, 264, 17, 24), (128, 528, 1032, 300, 64), (768, 1040, 512, 8, 16), (769, 1040, 512, 8, 16),
+           (96, 144, 128, 40, 56), (192, 4608, 136, 30, 32), (193, 4624, 136, 30, 32), (3, 65552, 136, 5, 48)]
 
 
 @pytest.mark.parametrize("shape", BORDERS, ids=lambda c: "x".join(map(str, c)))
