@@ -22,6 +22,10 @@
 //    at half the rate (the 8-bit 32x32x16 instruction has the same adder).
 //  * A lane's 32 codes of an operand are chunks g and g + 2 of its row (g = lane / 32).  Which k
 //    they are does not matter as long as both operands agree, as the MFMA pairs equal places.
+//  * Integers: v_mfma_i32_32x32x32_i8 takes a lane's 16-byte chunk as it lies, half the k of the E4M3
+//    instruction at the same rate per k, and sums exactly, so y in fp32 needs no second form.  4096 x 11008 x
+//    4096 172 us in the GEMM (2.15 POP/s with delta, epilogue and store; a library product of 4096^3 2.07, of
+//    8192^3 2.52).
 //  * Enough tiles to fill the chip: rows in segment order, the LoRA delta as extra bf16 MFMA
 //    steps, then the epilogue and the only store (big_tiles.h).  Fewer: K is split over ks
 //    workgroups per tile, which write scaled fp32 slices [ks][M][N]; the reduction that follows

@@ -26,7 +26,8 @@
 //    each pair only its own adapter's columns).
 //  * The same kernel serves a whole expert layer (lora_moe_layer): gate and up side by side in one
 //    launch, and the down projection on each pair's own hidden row, or on four bf16 parts of it,
-//    which meet W in the same pass and add up in the partial tile.
+//    which meet W in the same pass and add up in the partial tile.  Experts of 2880 x 2880, 4 of 32 per token:
+//    gate and up of one token 25 us (133 MB: 5.3 TB/s), of 64 tokens 189 (1.06 GB: 5.6), down 14 and 97.
 //  * moe_reduce_kernel, block (column chunk, pair): the splits added in order, t summed over
 //    the splits in order, scale_i t B[i][e] added, the routing weight applied, rounded once
 //    into y.  No atomics: results do not depend on scheduling.
