@@ -296,3 +296,48 @@ def test_the_largest_adapter_table(M, K, N):
     L.lora_build_segments(c.ids, M, n, seg)
     c.y.fill_(7)
     assert torch.equal(c.run(segs=seg), want)
+
+
+# With segments beside the GEMM (many adapter tiles, or a stride that is no multiple of 8), and adapter tiles for
+# more than 128 rows
+WAYS = [(333, 1040, 2760, 30, 24), (100, 512, 264, 6, 5), (700, 256, 264, 40, 64), (300, 528, 264, 6, 13),
+        (257, 1040, 264, 12, 16), (17, 656, 136, 17, 40)]
+
+
+@pytest.mark.parametrize("shape", WAYS, ids=lambda c: "x".join(map(str, c)))
+def test_ways_of_wide_batches(shape):
+    """Given segments, a graph whose ids change between its replays, two calls at once, NaN in an adapter."""
+    M, K, N, n, r = shape
+    a = Call(31, *shape, act="silu", bias=True, mul=True, residual=True)
+    b = Call(32, *shape, residual=True, f32=True)
+    want_a, want_b = a.run().clone(), b.run().clone()
+    a.check(want_a, f"{shape}"), b.check(want_b, f"{shape} f32")
+    seg = L.Segments(M, n)
+    L.lora_build_segments(a.ids, M, n, seg)
+    a.y.fill_(7)
+    assert torch.equal(a.run(segs=seg), want_a)
+    s1, s2 = torch.cuda.Stream(), torch.cuda.Stream()
+    torch.cuda.synchronize()
+    for _ in range(3):
+        a.y.fill_(7), b.y.fill_(7)
+        torch.cuda.synchronize()
+        a.enqueue(stream=s1), b.enqueue(stream=s2)
+        torch.cuda.synchronize()
+        assert torch.equal(a.y, want_a) and torch.equal(b.y, want_b)
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        a.enqueue()
+    ids = a.ids.clone()
+    for rep in range(3):
+        a.ids.copy_(torch.roll(ids, rep * 5 + 1) if rep < 2 else ids)
+        a.y.fill_(7)
+        torch.cuda.synchronize()
+        g.replay()
+        torch.cuda.synchronize()
+        got = a.y.clone()
+        assert torch.equal(got, a.run()), rep
+    assert torch.equal(got, want_a)
+    i = int(b.ids[b.ids >= 0][0])
+    b.B[i, 0, 3] = float("nan")
+    got, hit = b.run(), b.ids == i
+    assert torch.equal(got[~hit], want_b[~hit]) and torch.isnan(got[hit, 3]).all()
