@@ -192,6 +192,13 @@ __device__ __forceinline__ bool moe_tile_adapters(S &sh, const int32_t *ids, int
     return true;
 }
 
+// A sum over a row's leading parts and that over its other ones, joined.  A leading part is zero or infinite only
+// where the row's element is, so the first sum shows an infinity or a NaN among the products as the formula
+// has it; the others' may be 0 times an infinity, or one of the other sign, and are left out then.
+__device__ __forceinline__ float join_parts(float lead, float rest) {
+    return fabsf(lead) < __builtin_inff() ? lead + rest : lead;
+}
+
 template <class C, int RM, MoeRows ROWS>
 __global__ __launch_bounds__(kThreads) void moe_gemm_kernel(MoeGemmArgs a) {
     __shared__ __attribute__((aligned(1024))) uint4 lds[kWaves * C::WAVE];
@@ -291,8 +298,7 @@ __global__ __launch_bounds__(kThreads) void moe_gemm_kernel(MoeGemmArgs a) {
         for (int q = 0; q < C::XR / 8; ++q) {
             const int g = (tid >> 7) + 2 * q;  // rows 4 g .. 4 g + 3 of the block
             const float4 s = reduce_waves_group<C>(red, g, col);
-            // (four parts of one pair: the last is zeros)
-            const float sv[4] = {PARTS == 4 ? s.x + (s.y + s.z) : s.x, s.y, s.z, s.w};
+            const float sv[4] = {PARTS == 4 ? join_parts(s.x, s.y + s.z) : s.x, s.y, s.z, s.w};  // (the last part: zeros)
 #pragma unroll
             for (int v = 0; v < 4 / PARTS; ++v) {
                 const int j = (rb * C::XR + 4 * g) / PARTS + v;
