@@ -406,6 +406,7 @@ void shrink_plan(int d_in, int r_max, int *kc, int *ksplit);
 // into ks splits of k_per_split; pairs in blocks of bm rows; partial rows np floats apart.
 struct MoePlan {
     int rm, bm, n_tn, n_lt, ks, k_per_split, np;
+    int n_slots;  // the experts that get workgroups: E, every one, or P, those that the pairs name
     bool few;  // blocks of 16 staged rows (lora_moe_layer)
 };
 MoePlan moe_plan(int M, int top_k, int E, int K, int N, int r_max, int n_adapters);

@@ -638,7 +638,7 @@ __global__ __launch_bounds__(kThreads, 2) void decode_gemm_int8_lora_kernel(
     const int id = lane < XR && m0 + lane < M ? lo.ids[m0 + lane] : -1;
     const bool kept = id >= 0 && id < lo.n_adapters;
     int different;
-    const int rank = wave_rank(id, kept, XR, different), slot = kept ? rank - lt * APT : -1;
+    const int rank = wave_rank(id, kept, lo.n_adapters, lane, different), slot = kept ? rank - lt * APT : -1;
     if (lt * APT >= different) return;  // whole workgroup
     int ad = -1;
 #pragma unroll

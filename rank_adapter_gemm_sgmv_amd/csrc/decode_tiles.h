@@ -192,20 +192,21 @@ struct AdapterTiles {
     static constexpr int APT = kBN / RM;  // adapters per tile
 };
 
-// A lane's rank: how many different values below its own the kept lanes (of the first n) hold; different:
-// how many they hold in all.
-__device__ __forceinline__ int wave_rank(int v, bool kept, int n, int &different) {
-    int rank = 0;
-    different = 0;
-    for (int q = 0; q < n; ++q) {  // (n and what is read of lane q are uniform)
-        const int u = __builtin_amdgcn_readlane(v, q);
-        const uint64_t same = __ballot(kept && v == u);
-        if ((same & ((2ull << q) - 1)) == (1ull << q)) {  // lane q is kept and the first of its value
-            rank += u < v;
-            ++different;
-        }
+// A kept lane's rank: how many different values below its own the kept lanes hold; different: how many they
+// hold in all.  Kept values are in [0, limit).  Bit by bit from the top, so its length is the width of the largest
+// value and not the number of lanes: a step per lane took lora_moe_linear of 4 tokens, 4 of 32 experts of
+// 2880 x 2880, from 45 to 48.5 us.
+__device__ __forceinline__ int wave_rank(int v, bool kept, int limit, int lane, int &different) {
+    uint64_t same = __ballot(kept), less = 0;  // of the kept lanes, by the bits so far
+    for (int b = 31 - __clz((limit - 1) | 1); b >= 0; --b) {
+        const bool one = (v >> b) & 1;
+        const uint64_t ones = __ballot(one);
+        less |= one ? same & ~ones : 0;
+        same &= one ? ones : ~ones;
     }
-    return rank;
+    const uint64_t firsts = __ballot(kept && (same & ((1ull << lane) - 1)) == 0);
+    different = __popcll(firsts);
+    return __popcll(less & firsts);
 }
 
 // The K loop of one wave: acc += x[rows, kw0 .. kw0 + 16 nst) W[same k, tile], streamed

@@ -49,19 +49,19 @@ struct MoeShared {
 };
 
 // Batches of at most 64 pairs need no list in LDS and no barrier to find a workgroup's work: every wave
-// holds all pairs, one per lane.
+// holds all pairs' experts, one per lane (`mine`, -1 past the last).
 
-// The a-th expert, ascending, that some pair is routed to (-1: fewer are).  Only batches with fewer
-// pairs than experts ask; the others give every expert its workgroups.
+// The a-th expert, ascending, that some pair is routed to (-1: fewer are).  Only launches with fewer
+// workgroups than every expert's ask (MoePlan::n_slots).
 template <class S>
-__device__ __forceinline__ int moe_routed_expert(S &sh, const int32_t *topk_ids, int P, int E, int a, int tid,
-                                                 int lane) {
+__device__ __forceinline__ int moe_routed_expert(S &sh, const int32_t *topk_ids, int mine, int P, int E, int a,
+                                                 int tid, int lane) {
     if (P <= 64) {
-        const int v = lane < P ? topk_ids[lane] : -1;
-        const bool kept = v >= 0 && v < E;
+        const bool kept = mine >= 0 && mine < E;
         int different;
-        const uint64_t found = __ballot(kept && wave_rank(v, kept, P, different) == a);
-        return found ? __builtin_amdgcn_readlane(v, __ffsll((unsigned long long)found) - 1) : -1;
+        const int rank = wave_rank(mine, kept, E, lane, different);
+        const uint64_t found = __ballot(kept && rank == a);
+        return found ? __builtin_amdgcn_readlane(mine, __ffsll((unsigned long long)found) - 1) : -1;
     }
     const int nw = (E + 31) >> 5;  // at most 128 words
     for (int w = tid; w < nw; w += kThreads) sh.bits[w] = 0u;
@@ -94,10 +94,11 @@ __device__ __forceinline__ int moe_routed_expert(S &sh, const int32_t *topk_ids,
 
 // The expert's pairs, in pair order, into sh.rows; their count (uniform in the workgroup).
 template <class S>
-__device__ __forceinline__ int moe_pairs(S &sh, const int32_t *topk_ids, int P, int e, int tid, int lane, int wave) {
+__device__ __forceinline__ int moe_pairs(S &sh, const int32_t *topk_ids, int mine, int P, int e, int tid, int lane,
+                                         int wave) {
     const uint64_t below = lane == 0 ? 0ull : (~0ull >> (64 - lane));
     if (P <= 64) {  // every wave writes the same list
-        const bool hit = lane < P && topk_ids[lane] == e;
+        const bool hit = mine == e;
         const uint64_t bal = __ballot(hit);
         if (hit) sh.rows[__popcll(bal & below)] = (uint16_t)lane;
         __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");  // (a wave's LDS accesses complete in order)
@@ -133,7 +134,7 @@ __device__ __forceinline__ bool moe_tile_adapters(S &sh, const int32_t *ids, int
         const int i = lane < count ? ids[sh.rows[lane] / top_k] : -1;
         const bool kept = i >= 0 && i < n_adapters;
         int different;
-        const int s = wave_rank(i, kept, count, different) - lt * APT;
+        const int s = wave_rank(i, kept, n_adapters, lane, different) - lt * APT;
         // (every wave writes the same values: no slot is written twice with two)
         if (kept && s >= 0 && s < APT) sh.tile_ad[s] = i;
         if (lane < APT && lt * APT + lane >= different) sh.tile_ad[lane] = -1;
@@ -215,8 +216,9 @@ __global__ __launch_bounds__(kThreads) void moe_gemm_kernel(MoeGemmArgs a) {
     lin /= n_cols * a.n_proj;
     const int split = lin / a.n_slots;
     int e = lin % a.n_slots;
+    const int mine = a.P <= 64 && lane < a.P ? a.topk_ids[lane] : -1;
     if (a.n_slots < a.E) {
-        e = moe_routed_expert(sh, a.topk_ids, a.P, a.E, e, tid, lane);
+        e = moe_routed_expert(sh, a.topk_ids, mine, a.P, a.E, e, tid, lane);
         if (e < 0) return;  // whole workgroup
     }
     // gate and up: their column tiles side by side
@@ -224,7 +226,7 @@ __global__ __launch_bounds__(kThreads) void moe_gemm_kernel(MoeGemmArgs a) {
     if (second) ct -= n_cols;
     const uint16_t *const W = second ? a.W[1] : a.W[0], *const A = second ? a.A[1] : a.A[0];
     float *const partial = second ? a.partial[1] : a.partial[0], *const tpart = second ? a.tpart[1] : a.tpart[0];
-    const int count = moe_pairs(sh, a.topk_ids, a.P, e, tid, lane, wave);
+    const int count = moe_pairs(sh, a.topk_ids, mine, a.P, e, tid, lane, wave);
     if (count == 0) return;  // whole workgroup
     const bool adapter_tile = ct >= a.n_tn;
     const int lt = ct - a.n_tn;
@@ -422,12 +424,21 @@ MoePlan moe_plan(int M, int top_k, int E, int K, int N, int r_max, int n_adapter
     if (ks > kq) ks = kq;
     p.k_per_split = (kq + ks - 1) / ks * kBKW * kWaves;
     p.ks = (K + p.k_per_split - 1) / p.k_per_split;
+    // Fewer pairs than experts: workgroups for every expert, or for as many as the pairs can name, each looking
+    // up its own.  One without a pair holds its CU for about a microsecond, the CU's share of some 30 KB of W, but
+    // while W streams for longer than that it is hidden, and it keeps the others from ending together.  us of the call, every
+    // expert's and looked up: 4 of 16 experts of 2880 x 2880 23.3 and 25.4 (1728 workgroups less for 66 MB), 8 of 32 31.0 and
+    // 33.9, 8 of 64 32.1 and 33.9 (4032, 133 MB); 4 of 32 27.0 and 25.8 (4032, 66 MB), 1 of 32 32.8 and 15.1, 8 of 32
+    // of 1024 x 1408 22.7 and 17.7.
+    p.n_slots = E;
+    if (P < E && (long)(E - P) * (p.n_tn + p.n_lt) * p.ks * 30000 > 2L * P * K * N) p.n_slots = P;
     return p;
 }
 
 MoePlan moe_layer_plan(int M, int top_k, int E, int K, int N, int r_max, int n_adapters, int n_proj, MoeRows rows) {
     MoePlan p = moe_plan(M, top_k, E, K, N, r_max, n_adapters);
     const int P = M * top_k, slots = E < P ? E : P;
+    p.n_slots = slots;
     // workgroups of a split, with the adapter tiles that an expert's average pairs can need
     const int apt = kBN / p.rm, per = (P + slots - 1) / slots, distinct = n_adapters < per ? n_adapters : per;
     const long tiles = (long)slots * n_proj * (p.n_tn + (distinct + apt - 1) / apt);
@@ -455,15 +466,14 @@ size_t moe_tpart_floats(const MoePlan &p, int P) { return (size_t)p.ks * P * p.r
 hipError_t launch_moe_gemm(const MoePlan &p, const MoeGemmArgs &args, hipStream_t s) {
     if (args.P < 1 || args.P > LORA_MOE_MAX_PAIRS || args.K % 16 != 0 || args.K < 128 || args.n_proj < 1 || args.n_proj > 2 ||
         args.N < 8 || args.N % 8 != 0 || args.r_stride % 8 != 0 || args.r_stride > p.rm ||
-        args.n_adapters > LORA_MAX_ADAPTERS || (p.bm != 32 && p.bm != 64))
+        args.n_adapters > LORA_MAX_ADAPTERS || (p.bm != 32 && p.bm != 64) || (p.n_slots != args.E && p.n_slots != args.P))
         return hipErrorInvalidValue;
     MoeGemmArgs a = args;
     a.n_tn = p.n_tn;
     a.n_lt = p.n_lt;
     a.k_per_split = p.k_per_split;
     a.np = p.np;
-    // workgroups for as many experts as the pairs can name
-    a.n_slots = a.E < a.P ? a.E : a.P;
+    a.n_slots = p.n_slots;
     const dim3 grid((unsigned)((long)p.ks * a.n_slots * a.n_proj * (p.n_tn + p.n_lt)));
 #define MOE_GEMM(RMX)                                                                            \
     if (a.rows == kMoeToken)                                                                     \
