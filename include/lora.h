@@ -573,8 +573,8 @@ lora_status_t lora_moe_linear_profiled(const void *x, const void *W, const void 
  *     h[m][j] = act(x[m] gate[e]) * (x[m] up[e])
  *     y[m]    = residual[m] + sum_j topk_w[m][j] (h[m][j] down[e])      (one rounding, into y's type)
  * A slot with no expert (-1, or outside [0, n_experts)) adds nothing; an expert that a token names
- * twice counts twice.  Everything is summed in fp32; h enters the down projection rounded to bf16 with
- * y in bf16, and with all of its 24 bits (three bf16 parts) with y in fp32.
+ * twice counts twice.  Everything is summed in fp32; h enters the down projection as two bf16 values
+ * (16 bits, within 2^-16 of itself) with y in bf16, and with all of its 24 bits (three) with y in fp32.
  * weights: a HOST struct read during the call, of device arrays: gate and up W [n_experts][d][d_ff],
  * A [n_adapters][n_experts][d][r_max], B [n_adapters][n_experts][r_max][d_ff]; down the same with d and
  * d_ff exchanged; all required.  x: bf16 [M][d].  residual: [M][d] in y's type, y itself or apart from

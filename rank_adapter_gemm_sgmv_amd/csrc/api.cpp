@@ -1204,7 +1204,7 @@ struct MoeLayerPlan {
 MoeLayerPlan moe_plans(const MoeLayerDims &z, bool y_f32) {
     MoeLayerPlan p;
     p.in = moe_layer_plan(z.M, z.top_k, z.E, z.d, z.ff, z.r_max, z.n_adapters, 2, kMoeToken);
-    p.out = moe_layer_plan(z.M, z.top_k, z.E, z.ff, z.d, z.r_max, z.n_adapters, 1, y_f32 ? kMoeParts : kMoePair);
+    p.out = moe_layer_plan(z.M, z.top_k, z.E, z.ff, z.d, z.r_max, z.n_adapters, 1, y_f32 ? kMoeParts4 : kMoeParts2);
     const size_t a = 2 * round_up(moe_partial_floats(p.in, z.pairs()) * 4),
                  b = round_up(moe_partial_floats(p.out, z.pairs()) * 4),
                  ta = 2 * round_up(moe_tpart_floats(p.in, z.pairs()) * 4),
@@ -1222,6 +1222,7 @@ hipError_t run_moe_layer(const MoeLayerDims &z, const void *x, const lora_moe_we
                          const int32_t *ranks, const int32_t *ids, const int32_t *topk_ids, const float *topk_w,
                          const void *residual, lora_act_t act, void *y, bool y_f32, void *ws, hipStream_t s) {
     const MoeLayerPlan pl = moe_plans(z, y_f32);
+    const MoeRows rows = y_f32 ? kMoeParts4 : kMoeParts2;  // of a pair's hidden row
     const int P = z.pairs();
     char *const c = static_cast<char *>(ws);
     auto floats = [](char *p) { return reinterpret_cast<float *>(p); };
@@ -1245,14 +1246,14 @@ hipError_t run_moe_layer(const MoeLayerDims &z, const void *x, const lora_moe_we
     if (e != hipSuccess) return e;
     const MoeLayerArgs a{scale, ranks, topk_ids, ids, topk_w, P, z.top_k, z.E, z.r_max, z.n_adapters};
     if ((e = launch_moe_hidden(pl.in, a, MoeSums{g.partial[0], g.tpart[0], bf16(w.gate.B)},
-                               MoeSums{g.partial[1], g.tpart[1], bf16(w.up.B)}, z.ff, act,
-                               y_f32, h, s)) != hipSuccess)
+                               MoeSums{g.partial[1], g.tpart[1], bf16(w.up.B)}, z.ff, act, rows,
+                               h, s)) != hipSuccess)
         return e;
     g.x = h;
     g.W[0] = bf16(w.down.W);
     g.A[0] = bf16(w.down.A);
     g.K = z.ff; g.N = z.d; g.n_proj = 1;
-    g.rows = y_f32 ? kMoeParts : kMoePair;
+    g.rows = rows;
     if ((e = launch_moe_gemm(pl.out, g, s)) != hipSuccess) return e;
     return launch_moe_out(pl.out, a, MoeSums{g.partial[0], g.tpart[0], bf16(w.down.B)}, z.M, z.d, residual, y,
                           y_f32, s);

@@ -413,15 +413,16 @@ MoePlan moe_plan(int M, int top_k, int E, int K, int N, int r_max, int n_adapter
 size_t moe_partial_floats(const MoePlan &p, int P);  // [ks][P][np]
 size_t moe_tpart_floats(const MoePlan &p, int P);    // [ks][P][rm]
 
-// The rows of x that a (token, slot) pair multiplies: its token's, its own, or its own row in four
-// bf16 parts that add up to it (rows 4 p .. 4 p + 3).
-enum MoeRows { kMoeToken, kMoePair, kMoeParts };
+// The rows of x that a (token, slot) pair multiplies: its token's, or its own in bf16 parts that add up to it: two
+// (rows 2 p and 2 p + 1: its value to 2^-16) or four (rows 4 p .. 4 p + 3: all 24 bits in three, and zeros).
+enum MoeRows { kMoeToken, kMoeParts2, kMoeParts4 };
+constexpr int moe_rows_of_pair(MoeRows r) { return r == kMoeToken ? 1 : r == kMoeParts2 ? 2 : 4; }
 // The plans of a whole expert layer's launches.  n_proj: projections that share the rows (gate and up in
 // one launch).
 MoePlan moe_layer_plan(int M, int top_k, int E, int K, int N, int r_max, int n_adapters, int n_proj, MoeRows rows);
 
 struct MoeGemmArgs {
-    const uint16_t *x;         // [M][K], [P][K] or [4 P][K]
+    const uint16_t *x;         // [M][K], [2 P][K] or [4 P][K]
     const uint16_t *W[2];      // n_proj of them: [E][K][N]
     const uint16_t *A[2];      // [n_adapters][E][K][r_stride]
     const int32_t *topk_ids;   // [P] = [M][top_k]
@@ -461,10 +462,9 @@ struct MoeLayerArgs {
     const float *topk_w;       // [P] or nullptr (= 1)
     int P, top_k, E, r_stride, n_adapters;
 };
-// h[p] = act(gate) * up of every pair with an expert, in bf16 ([P][N]) or (parts) in four bf16 parts
-// ([4 P][N]).
+// h[p] = act(gate) * up of every pair with an expert, in two bf16 parts ([2 P][N]) or four ([4 P][N]).
 hipError_t launch_moe_hidden(const MoePlan &p, const MoeLayerArgs &a, const MoeSums &gate, const MoeSums &up,
-                             int N, int act, bool parts, uint16_t *h, hipStream_t s);
+                             int N, int act, MoeRows rows, uint16_t *h, hipStream_t s);
 // y[m] = residual[m] + the sum over the token's slots of topk_w * down.
 hipError_t launch_moe_out(const MoePlan &p, const MoeLayerArgs &a, const MoeSums &down, int M, int N,
                           const void *residual, void *y, bool y_f32, hipStream_t s);

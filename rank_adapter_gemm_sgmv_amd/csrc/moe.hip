@@ -25,7 +25,7 @@
 //    partial[split][pair][column] (W tiles) or tpart[split][pair][0 .. RM) (adapter tiles,
 //    each pair only its own adapter's columns).
 //  * The same kernel serves a whole expert layer (lora_moe_layer): gate and up side by side in one
-//    launch, and the down projection on each pair's own hidden row, or on four bf16 parts of it,
+//    launch, and the down projection on two or three bf16 parts of each pair's own hidden row,
 //    which meet W in the same pass and add up in the partial tile.  Experts of 2880 x 2880, 4 of 32 per token:
 //    gate and up of one token 25 us (133 MB: 5.3 TB/s), of 64 tokens 189 (1.06 GB: 5.6), down 14 and 97.
 //  * moe_reduce_kernel, block (column chunk, pair): the splits added in order, t summed over
@@ -209,7 +209,7 @@ __global__ __launch_bounds__(kThreads) void moe_gemm_kernel(MoeGemmArgs a) {
 
     const int tid = threadIdx.x, lane = tid & 63;
     const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
-    constexpr int PARTS = ROWS == kMoeParts ? 4 : 1;
+    constexpr int PARTS = moe_rows_of_pair(ROWS);
     const int n_cols = a.n_tn + a.n_lt;
     int lin = blockIdx.x;
     int ct = lin % (n_cols * a.n_proj);
@@ -300,7 +300,12 @@ __global__ __launch_bounds__(kThreads) void moe_gemm_kernel(MoeGemmArgs a) {
         for (int q = 0; q < C::XR / 8; ++q) {
             const int g = (tid >> 7) + 2 * q;  // rows 4 g .. 4 g + 3 of the block
             const float4 s = reduce_waves_group<C>(red, g, col);
-            const float sv[4] = {PARTS == 4 ? join_parts(s.x, s.y + s.z) : s.x, s.y, s.z, s.w};  // (the last part: zeros)
+            float sv[4] = {s.x, s.y, s.z, s.w};
+            if constexpr (PARTS == 2) {
+                sv[0] = join_parts(s.x, s.y);
+                sv[1] = join_parts(s.z, s.w);
+            }
+            if constexpr (PARTS == 4) sv[0] = join_parts(s.x, s.y + s.z);  // (the last part: zeros)
 #pragma unroll
             for (int v = 0; v < 4 / PARTS; ++v) {
                 const int j = (rb * C::XR + 4 * g) / PARTS + v;
@@ -443,13 +448,14 @@ MoePlan moe_layer_plan(int M, int top_k, int E, int K, int N, int r_max, int n_a
     const int apt = kBN / p.rm, per = (P + slots - 1) / slots, distinct = n_adapters < per ? n_adapters : per;
     const long tiles = (long)slots * n_proj * (p.n_tn + (distinct + apt - 1) / apt);
     // Rows of a block, by the pairs an expert has on average: a block streams the expert's W once more, and a
-    // larger one has more x to stage and more to multiply.  us of the layer's call, 8 experts of 1040 x 2768,
-    // 40 adapters of rank 24.  16 or 32 rows in bf16: 5 pairs 108 and 111 (32 experts of 1440 x 1440), 10:
-    // 121.5 and 121.9, 12: 132 and 126.  32 or 64: 12 pairs 62.3 and 65.9, 25: 71.0 and 74.6, 32: 88.5 and 87.0,
-    // 50: 126 and 102, 100: 194 and 162.  Parts of rows, four to a pair, 32 or 64: 4 pairs 56.5 and 58.3, 6:
-    // 59.2 and 58.0, 7: 65.2 and 60.2, 25: 97.7 and 85.1, 100: 350 and 255.
-    if (P > (rows == kMoeParts ? 5 : 30) * slots) p.bm = 64;
-    p.few = rows != kMoeParts && P <= 10 * slots;
+    // larger one has more x to stage and more to multiply.  us of the layer's call with blocks of 16, 32 and 64 rows,
+    // 8 experts of 1040 x 2768, 40 adapters of rank 24.  A row to a pair: 5 pairs 108 and 111 (32 experts of 1440 x
+    // 1440), 10: 121.5 and 121.9, 12: 132 and 126; 12: -, 62.3 and 65.9, 25: 71.0 and 74.6, 32: 88.5 and 87.0,
+    // 50: 126 and 102, 100: 194 and 162.  Two: 1 pair 45.5, 46.1 and 47.4 (32 of 2880 x 2880), 4: 53.4, 50.2 and 53.2, 8:
+    // 57.5, 51.9 and 53.0, 10: 75.7, 71.1 and 65.7, 12: -, 64.4 and 60.2, 25: -, 81.8 and 73.1, 250: -, 600 and 484.
+    // Four, 32 or 64: 4 pairs 56.5 and 58.3, 6: 59.2 and 58.0, 7: 65.2 and 60.2, 25: 97.7 and 85.1, 100: 350 and 255.
+    if (P > (rows == kMoeParts4 ? 5 : rows == kMoeParts2 ? 9 : 30) * slots) p.bm = 64;
+    p.few = P <= (rows == kMoeParts4 ? 0 : rows == kMoeParts2 ? 2 : 10) * slots;
     int ks = (int)(256 / tiles);
     const int kq = (K + kBKW * kWaves - 1) / (kBKW * kWaves);
     if (ks < 1) ks = 1;
@@ -478,10 +484,10 @@ hipError_t launch_moe_gemm(const MoePlan &p, const MoeGemmArgs &args, hipStream_
 #define MOE_GEMM(RMX)                                                                            \
     if (a.rows == kMoeToken)                                                                     \
         launch(moe_gemm_kernel<DEC, RMX, kMoeToken>, grid, dim3(kThreads), 0, s, a);             \
-    else if (a.rows == kMoePair)                                                                 \
-        launch(moe_gemm_kernel<DEC, RMX, kMoePair>, grid, dim3(kThreads), 0, s, a);              \
+    else if (a.rows == kMoeParts2)                                                               \
+        launch(moe_gemm_kernel<DEC, RMX, kMoeParts2>, grid, dim3(kThreads), 0, s, a);            \
     else                                                                                         \
-        launch(moe_gemm_kernel<DEC, RMX, kMoeParts>, grid, dim3(kThreads), 0, s, a)
+        launch(moe_gemm_kernel<DEC, RMX, kMoeParts4>, grid, dim3(kThreads), 0, s, a)
 #define MOE_RM()                                                                                 \
     switch (p.rm) {                                                                              \
         case 8: MOE_GEMM(8); break;                                                              \

@@ -90,7 +90,7 @@ __device__ __forceinline__ float4 pair_columns(const MoeLayerArgs &a, const MoeS
 
 // Block (chunk of 512 columns, pair), four columns per thread: the first half of the block sums the
 // gate, the second up, which it hands over through LDS.
-template <int RM, bool PARTS>
+template <int RM, MoeRows ROWS>
 __global__ __launch_bounds__(kThreadsMoe) void moe_hidden_kernel(MoeLayerArgs a, MoeSums gate, MoeSums up, int N,
                                                                  int np, int ks, int act, uint16_t *h) {
     constexpr int HALF = kThreadsMoe / 2;
@@ -111,22 +111,19 @@ __global__ __launch_bounds__(kThreadsMoe) void moe_hidden_kernel(MoeLayerArgs a,
     float z[4] = {v.x, v.y, v.z, v.w};
     epi_act<4>(z, act);
     z[0] *= zu.x; z[1] *= zu.y; z[2] *= zu.z; z[3] *= zu.w;
-    if constexpr (!PARTS) {
-        // bf16: what the matrix instructions take; y's own rounding is as large
-        *reinterpret_cast<uint2 *>(h + (size_t)p * N + n) =
-            make_uint2(cvt_bf16x2(z[0], z[1]), cvt_bf16x2(z[2], z[3]));
-    } else {
+    // The matrix instructions take bf16, a value's parts add up in fp32: two of them for y in bf16, whose own
+    // rounding is 2^8 times as large as what they leave out; with y in fp32 nothing is.
+    constexpr int NP = moe_rows_of_pair(ROWS);
 #pragma unroll
-        for (int q = 0; q < 4; ++q) {
-            uint32_t b[4];
+    for (int q = 0; q < NP; ++q) {
+        uint32_t b[4];
 #pragma unroll
-            for (int c = 0; c < 4; ++c) {
-                b[c] = q < 3 ? bf16_part(z[c]) : 0u;
-                z[c] = bf16_rest(z[c]);
-            }
-            *reinterpret_cast<uint2 *>(h + ((size_t)4 * p + q) * N + n) =
-                make_uint2(b[0] | b[1] << 16, b[2] | b[3] << 16);
+        for (int c = 0; c < 4; ++c) {
+            b[c] = q < 3 ? bf16_part(z[c]) : 0u;
+            z[c] = bf16_rest(z[c]);
         }
+        *reinterpret_cast<uint2 *>(h + ((size_t)NP * p + q) * N + n) =
+            make_uint2(b[0] | b[1] << 16, b[2] | b[3] << 16);
     }
 }
 
@@ -187,14 +184,14 @@ bool moe_args_ok(const MoePlan &p, const MoeLayerArgs &a, int N) {
 }  // namespace
 
 hipError_t launch_moe_hidden(const MoePlan &p, const MoeLayerArgs &a, const MoeSums &gate, const MoeSums &up,
-                             int N, int act, bool parts, uint16_t *h, hipStream_t s) {
-    if (!moe_args_ok(p, a, N)) return hipErrorInvalidValue;
+                             int N, int act, MoeRows rows, uint16_t *h, hipStream_t s) {
+    if (!moe_args_ok(p, a, N) || rows == kMoeToken) return hipErrorInvalidValue;
     const dim3 grid((unsigned)((N + 2 * kThreadsMoe - 1) / (2 * kThreadsMoe)), (unsigned)a.P);
-#define MOE_HIDDEN_ONE(RMX, PARTS)                                                               \
-    launch(moe_hidden_kernel<RMX, PARTS>, grid, dim3(kThreadsMoe), 0, s, a, gate, up, N, p.np, p.ks, act, h)
+#define MOE_HIDDEN_ONE(RMX, ROWS)                                                                \
+    launch(moe_hidden_kernel<RMX, ROWS>, grid, dim3(kThreadsMoe), 0, s, a, gate, up, N, p.np, p.ks, act, h)
 #define MOE_HIDDEN(RMX)                                                                          \
-    if (parts) MOE_HIDDEN_ONE(RMX, true);                                                        \
-    else MOE_HIDDEN_ONE(RMX, false)
+    if (rows == kMoeParts4) MOE_HIDDEN_ONE(RMX, kMoeParts4);                                     \
+    else MOE_HIDDEN_ONE(RMX, kMoeParts2)
     switch (p.rm) {
         case 8: MOE_HIDDEN(8); break;
         case 16: MOE_HIDDEN(16); break;
