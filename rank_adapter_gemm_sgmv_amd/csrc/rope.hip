@@ -17,6 +17,8 @@
 //    several blocks, each with a table of its own (4 rows of 128 heads of 256: 41.3 us in a block per
 //    row, 4.6 in several).  Four items ahead in registers took 80.6 us at 8192 rows, where one at a time takes
 //    33.1 (40 heads of 128 in bf16, 168 MB: 5.1 TB/s); one row 2.4 us on the GPU, 7.3 per call.
+#include <type_traits>
+
 #include "common.h"
 
 namespace lora {
@@ -130,11 +132,10 @@ __global__ __launch_bounds__(kThreadsRope) void rope_kernel(RopeArgs a, int head
             }
         } else {
             if (i >= n_rot) {
+                // (as bits: a conversion would quiet a NaN)
+                using Two = std::conditional_t<F32, uint2, uint32_t>;
                 const int at = (a.rot_dim + (i - n_rot) * 2) * EL;
-                if (x != y) {
-                    st_el<F32>(y + at, ld_el<F32>(x + at));
-                    st_el<F32>(y + at + EL, ld_el<F32>(x + at + EL));
-                }
+                if (x != y) *reinterpret_cast<Two *>(y + at) = *reinterpret_cast<const Two *>(x + at);
                 continue;
             }
             const int pa = (INTER ? 2 * i : i) * EL, pb = (INTER ? 2 * i + 1 : i + half) * EL;
