@@ -444,10 +444,10 @@ lora_status_t lora_quant_int8(const void *x, int32_t M, int32_t d, void *y8, flo
  * (i, i + rot_dim / 2) or, interleaved, (2 i, 2 i + 1), turns by its row's angle:
  *     (a, b) -> factor * (a cos t - b sin t, a sin t + b cos t),
  *     t = 2 pi positions[m] freqs[i]                (the turns and their fraction in 64 bits)
- * Elements past rot_dim are copied.  inverse = 1 turns by -t: the gradient of q and k from that of
- * q_out and k_out.  q: [M][q_heads][head_dim], rows q_stride elements apart (a slice of a row of q, k
- * and v, say); k alike, or k_heads = 0 (k and k_out are then not read); q_out and k_out with strides of
- * their own, in q's type (dtype: LORA_BF16 or LORA_F32; fp32 arithmetic, one rounding).  q_out may be
+ * Elements past rot_dim are copied.  inverse = 1 turns by -t, with the same factor: the gradient of q and k
+ * from that of q_out and k_out.  It undoes a turn where factor is 1; with 1 / factor it undoes any.
+ * q: [M][q_heads][head_dim], rows q_stride elements apart (a slice of a row of q, k and v, say); k alike,
+ * or k_heads = 0 (k and k_out are then not read); q_out and k_out with strides of their own, in q's type (dtype: LORA_BF16 or LORA_F32; fp32 arithmetic, one rounding).  q_out may be
  * q itself with the same stride, and k_out k; outputs overlap nothing otherwise.  Between the rows'
  * heads nothing is read or written.  positions: int32 [M], any value.  freqs: double [rot_dim / 2],
  * turns per position, as lora_rope_freqs writes them (device memory).

@@ -1,4 +1,9 @@
-"""lora_rope: what passes through keeps its bits."""
+"""lora_rope: what passes through keeps its bits; the way back.
+
+The way back in fp32, u = 2^-24, S = |a| + |b| of a pair, f the factor: the forward turn is off by 8 u f S
+(tests/test_gpu_rope.py) and a rounding, at most 9 u f S; its two outputs together are at most 2 f S.  Turned back with
+1 / f, both errors enter with at most 1 / f (18 u S), the turn's own is 8 u (2 f S) / f, 1 / f itself and the output are
+rounded: 36 u S together, and f^2 times that with f both ways."""
 
 import pytest
 import torch
@@ -38,3 +43,36 @@ def test_what_passes_through_keeps_its_bits(shape, layout, dtype):
     for heads, was, got in ((hq, q, qo), (hk, k, ko)):
         was, got = (t.view(bits).view(M, heads, D) for t in (was, got))
         assert torch.equal(got[:, :, rot:], was[:, :, rot:])
+
+
+@pytest.mark.parametrize("layout", LAYOUTS, ids=["half", "inter"])
+def test_one_over_the_factor_turns_back(layout):
+    M, h, D, rot = 130, 3, 72, 64
+    freqs, f = L.lora_rope_freqs(rot, 10000.0, L.LORA_ROPE_YARN, 8.0, 4096.0)
+    assert f > 1.2
+    x = torch.empty(M, h * D, device="cuda").normal_()
+    pos = torch.randint(-1000, 30000, (M,), device="cuda", dtype=torch.int32)
+
+    def turn(v, factor, inverse):
+        y = torch.empty_like(v)
+        L.lora_rope(v, None, pos, freqs, M, h, 0, D, rot, h * D, h * D, layout, factor, inverse, y, h * D, None, 0,
+                    L.LORA_F32)
+        return y
+
+    y = turn(x, f, 0)
+    back, again = turn(y, 1.0 / f, 1), turn(y, f, 1)
+    torch.cuda.synchronize()
+    v = x.view(M, h, D)[:, :, :rot].abs().double()
+    if layout == L.LORA_ROPE_HALF:
+        size = (v[:, :, :rot // 2] + v[:, :, rot // 2:]).repeat(1, 1, 2)
+    else:
+        size = (v[:, :, 0::2] + v[:, :, 1::2]).repeat_interleave(2, 2)
+    bound = torch.zeros(M, h, D, dtype=torch.float64, device="cuda")
+    bound[:, :, :rot] = 36 * 2.0 ** -24 * size
+    bound = bound.view(M, h * D)
+    assert bool(((back.double() - x.double()).abs() <= bound).all())
+    # with the factor both ways: the gradient's direction, the factor's square of what passed the pairs
+    square = torch.ones(D, dtype=torch.float64, device="cuda")
+    square[:rot] = f * f
+    square = square.repeat(h)
+    assert bool(((again.double() - x.double() * square).abs() <= bound * f * f).all())
