@@ -42,9 +42,9 @@ __device__ __forceinline__ uint32_t pack_e4m3x4(float a, float b, float c, float
     return (uint32_t)__builtin_amdgcn_cvt_pk_fp8_f32(c, d, v, true);
 }
 
-// rint(127 p / top), ties to even, exactly.  q0 = p (127 / top) is off by at most 2^-16 of it, so only
-// quotients that close to a border (a few in ten thousand, and the ties that short significands
-// like bf16's make) take the exact remainder.  p is not above top; a NaN gives 0.
+// rint(127 p / top), ties to even, exactly.  q0 = p (127 / top) is off by at most 2^-23 of itself, so by 2^-16,
+// and only quotients within 2^-11 of a border take the exact remainder: one in a thousand, three to five in a
+// thousand of bf16 rows as they are, whose short significands make ties.  p is not above top; a NaN gives 0.
 __device__ __forceinline__ int int8_code(float p, float f, float top) {
     const float q0 = p * f;
     float k = rintf(q0);
