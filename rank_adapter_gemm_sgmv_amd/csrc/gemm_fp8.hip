@@ -347,14 +347,15 @@ hipError_t launch_fp8_cfg(const Gemm8<X> &g, const Fp8Plan &p, void *y, bool y_f
 #define FP8_ONE(WIDE, O32)                                                                     \
     launch((gemm_fp8_kernel<C, X, FUSED, WIDE, O32>), grid, dim3(C::NT), 0, s, g.x8, g.W8, g.w_scale, \
            g.M, g.K, g.N, p.k_per_split, partial, y, n_tm, n_tn, seg, ep, epi)
-    if constexpr (C::BM == 128) {  // (fp8_plan: fp32 y takes the small tiles)
+    if (y_f32 && C::BM != 128) return hipErrorInvalidValue;  // (fp8_plan: fp32 y takes the small tiles)
+    // (slices of integers are the same for both types of y)
+    if constexpr (C::BM == 128 && (FUSED || std::is_same_v<X, uint8_t>)) {
         if (y_f32) {
             if (o32) FP8_ONE(true, true);
             else FP8_ONE(true, false);
             return hipGetLastError();
         }
     }
-    if (y_f32) return hipErrorInvalidValue;
     if (o32) FP8_ONE(false, true);
     else FP8_ONE(false, false);
 #undef FP8_ONE
