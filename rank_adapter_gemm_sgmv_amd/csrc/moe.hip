@@ -27,7 +27,7 @@
 //  * The same kernel serves a whole expert layer (lora_moe_layer): gate and up side by side in one
 //    launch, and the down projection on two or three bf16 parts of each pair's own hidden row,
 //    which meet W in the same pass and add up in the partial tile.  Experts of 2880 x 2880, 4 of 32 per token:
-//    gate and up of one token 25 us (133 MB: 5.3 TB/s), of 64 tokens 189 (1.06 GB: 5.6), down 14 and 97.
+//    gate and up of one token 25 us (133 MB: 5.3 TB/s), of 64 tokens 189 (1.06 GB: 5.6), down 14 and 101.
 //  * moe_reduce_kernel, block (column chunk, pair): the splits added in order, t summed over
 //    the splits in order, scale_i t B[i][e] added, the routing weight applied, rounded once
 //    into y.  No atomics: results do not depend on scheduling.

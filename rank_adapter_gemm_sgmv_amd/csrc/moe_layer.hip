@@ -7,8 +7,8 @@
 // with t the adapter tiles' sums.  Everything is added in a fixed order: results do not depend on
 // scheduling.  Both are bound by the length of their chain of dependent loads (routing and ids, then
 // the adapter's rank and B), so a block loads the partial sums while it follows it.  us of hidden and out: one
-// token, 4 of 32 experts of 2880 x 2880 4.8 and 4.3; 64 tokens 9.1 and 6.7; 23 tokens, 2 of 8 experts of 1040 x
-// 2768, fp32 6.4 and 5.5.
+// token, 4 of 32 experts of 2880 x 2880 4.7 and 4.6; 64 tokens 9.5 and 6.7; 23 tokens, 2 of 8 experts of 1040 x
+// 2768, fp32 6.4 and 5.2.
 #include "epilogue.h"
 
 namespace lora {
